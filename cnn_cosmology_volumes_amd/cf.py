@@ -55,6 +55,7 @@ class cf_adam_larc_params(ctypes.Structure):
 CF_MAX_DENSE = 4
 CF_POOL_MAX, CF_POOL_AVG, CF_POOL_NONE = 0, 1, 2
 CF_OPT_SGD, CF_OPT_ADAM_LARC = 0, 1
+CF_ACT_LRELU, CF_ACT_SILU = 0, 1
 
 
 class cf_net_desc(ctypes.Structure):
@@ -103,6 +104,11 @@ _SIG = {
                          ctypes.c_int),
     "cf_batchnorm_bwd": ([ctypes.c_int, cf_dims, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
                          ctypes.c_int),
+    "cf_groupnorm_workspace_size": ([ctypes.c_int, cf_dims, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+    "cf_groupnorm_fwd": ([ctypes.c_int, cf_dims, _P, ctypes.c_int32, _P, _P, ctypes.c_float, ctypes.c_int,
+                          ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_groupnorm_bwd": ([ctypes.c_int, cf_dims, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int,
+                          ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "cf_net_param_count": ([ctypes.POINTER(cf_net_desc), ctypes.POINTER(ctypes.c_int64)], ctypes.c_int32),
     "cf_net_train_step_workspace_size": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32], ctypes.c_size_t),
     "cf_net_train_step": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.POINTER(_P),
@@ -472,6 +478,72 @@ def cf_batchnorm_bwd(X, dY, gamma, mean, invstd, dX=None, ws=None, stream=None):
     ws = _ws(int(lib().cf_batchnorm_workspace_size(dt, dims(X.shape))), X.device, ws)
     check(lib().cf_batchnorm_bwd(dt, dims(X.shape), _ptr(X), _ptr(dY), _ptr(gamma), _ptr(mean), _ptr(invstd),
                                  _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws), _stream(stream)))
+    return dX, dgamma, dbeta
+
+
+def _packed(name, t, dtype=None, shape=None):
+    """Raises where a tensor is not what the library will take it for."""
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _record(stream, *tensors):
+    """Tensors made here on the current stream and used on `stream`: their
+    memory is not reused before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+# --------------------------------------------------------------- group norm
+def cf_groupnorm_workspace_size(dtype, xshape, groups, backward):
+    return int(lib().cf_groupnorm_workspace_size(dtype, dims(xshape), int(groups), int(bool(backward))))
+
+
+def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y=None, mean=None, rstd=None, ws=None,
+                     stream=None):
+    """Group norm of NDHWC X, then the activation -> (Y, mean [N, groups],
+    rstd [N, groups])."""
+    dt = dtype_code(X.dtype)
+    N, C = int(X.shape[0]), int(X.shape[4])
+    _packed("X", X)
+    _packed("gamma", gamma, torch.float32, (C,))
+    _packed("beta", beta, torch.float32, (C,))
+    Y = torch.empty_like(X) if Y is None else Y
+    mean = torch.empty((N, int(groups)), dtype=torch.float32, device=X.device) if mean is None else mean
+    rstd = torch.empty((N, int(groups)), dtype=torch.float32, device=X.device) if rstd is None else rstd
+    ws = _ws(cf_groupnorm_workspace_size(dt, X.shape, groups, False), X.device, ws)
+    check(lib().cf_groupnorm_fwd(dt, dims(X.shape), _ptr(X), int(groups), _ptr(gamma), _ptr(beta), float(eps),
+                                 int(act), float(slope), _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws),
+                                 _stream(stream)))
+    _record(stream, Y, mean, rstd, ws)
+    return Y, mean, rstd
+
+
+def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, slope=1.0, dX=None, ws=None,
+                     stream=None):
+    """-> (dX, dgamma, dbeta) from the forward's mean and rstd."""
+    dt = dtype_code(X.dtype)
+    N, C = int(X.shape[0]), int(X.shape[4])
+    _packed("X", X)
+    _packed("dY", dY, X.dtype, X.shape)
+    _packed("gamma", gamma, torch.float32, (C,))
+    _packed("beta", beta, torch.float32, (C,))
+    _packed("mean", mean, torch.float32, (N, int(groups)))
+    _packed("rstd", rstd, torch.float32, (N, int(groups)))
+    dX = torch.empty_like(X) if dX is None else dX
+    dgamma = torch.empty((C,), dtype=torch.float32, device=X.device)
+    dbeta = torch.empty((C,), dtype=torch.float32, device=X.device)
+    ws = _ws(cf_groupnorm_workspace_size(dt, X.shape, groups, True), X.device, ws)
+    check(lib().cf_groupnorm_bwd(dt, dims(X.shape), _ptr(X), _ptr(dY), int(groups), _ptr(gamma), _ptr(beta),
+                                 _ptr(mean), _ptr(rstd), int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta),
+                                 _ptr(ws), _wsbytes(ws), _stream(stream)))
+    _record(stream, dX, dgamma, dbeta, ws)
     return dX, dgamma, dbeta
 
 

@@ -930,6 +930,80 @@ cf_status cf_batchnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
     return CF_OK;
 }
 
+// -------------------------------------------- group norm with activation
+static cf_status check_gn(cf_dtype dtype, const cf_dims& x, int32_t groups, const char* fn)
+{
+    cf_status st = check_dtype(dtype);
+    if (st != CF_OK) return st;
+    if ((st = check_dims(x, "x")) != CF_OK) return st;
+    if (groups < 1 || x.c % groups) return fail(CF_ERR_INVALID, "%s: channels must be a multiple of groups", fn);
+    if (x.c > 4096 || x.n > 65535)
+        return fail(CF_ERR_UNSUPPORTED, "%s: at most 4096 channels and 65535 samples", fn);
+    return CF_OK;
+}
+
+static cf_status check_act(cf_act act, float slope, const char* fn)
+{
+    if (act != CF_ACT_LRELU && act != CF_ACT_SILU) return fail(CF_ERR_INVALID, "%s: unknown activation %d", fn, (int)act);
+    if (act == CF_ACT_LRELU && !(slope >= 0.f && slope < INFINITY))
+        return fail(CF_ERR_INVALID, "%s: slope must be >= 0 and finite", fn);
+    return CF_OK;
+}
+
+size_t cf_groupnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t groups, int32_t backward)
+{
+    if (check_gn(dtype, x, groups, "cf_groupnorm_workspace_size") != CF_OK) return 0;
+    return gn_ws_bytes(dtype, x, groups, backward != 0);
+}
+
+cf_status cf_groupnorm_fwd(cf_dtype dtype, cf_dims x, const void* X, int32_t groups, const float* gamma,
+                           const float* beta, float eps, cf_act act, float slope, void* Y, float* mean, float* rstd,
+                           void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    cf_status st = check_gn(dtype, x, groups, "cf_groupnorm_fwd");
+    if (st != CF_OK) return st;
+    if ((st = check_act(act, slope, "cf_groupnorm_fwd")) != CF_OK) return st;
+    if (!X || !gamma || !beta || !Y || !mean || !rstd) return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: null pointer");
+    if (!al16(X) || !al16(gamma) || !al16(beta) || !al16(Y) || !al16(mean) || !al16(rstd))
+        return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: pointers must be 16-byte aligned");
+    if (!(eps > 0.f) || !(eps < INFINITY)) return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: eps must be positive and finite");
+    const size_t need = gn_ws_bytes(dtype, x, groups, false);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "cf_groupnorm_fwd: workspace %zu < %zu bytes", ws_bytes, need);
+    if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: workspace null or misaligned");
+    hipError_t e = dtype == CF_F32
+                       ? launch_gn_fwd<float>((const float*)X, gamma, beta, eps, act, slope, (float*)Y, mean, rstd, x,
+                                              groups, ws, stream)
+                       : launch_gn_fwd<uint16_t>((const uint16_t*)X, gamma, beta, eps, act, slope, (uint16_t*)Y, mean,
+                                                 rstd, x, groups, ws, stream);
+    CF_TRY_HIP(e, "group norm forward");
+    return CF_OK;
+}
+
+cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void* dY, int32_t groups,
+                           const float* gamma, const float* beta, const float* mean, const float* rstd, cf_act act,
+                           float slope, void* dX, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           hipStream_t stream)
+{
+    cf_status st = check_gn(dtype, x, groups, "cf_groupnorm_bwd");
+    if (st != CF_OK) return st;
+    if ((st = check_act(act, slope, "cf_groupnorm_bwd")) != CF_OK) return st;
+    if (!X || !dY || !gamma || !beta || !mean || !rstd || !dX || !dgamma || !dbeta)
+        return fail(CF_ERR_INVALID, "cf_groupnorm_bwd: null pointer");
+    if (!al16(X) || !al16(dY) || !al16(gamma) || !al16(beta) || !al16(mean) || !al16(rstd) || !al16(dX) ||
+        !al16(dgamma) || !al16(dbeta))
+        return fail(CF_ERR_INVALID, "cf_groupnorm_bwd: pointers must be 16-byte aligned");
+    const size_t need = gn_ws_bytes(dtype, x, groups, true);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "cf_groupnorm_bwd: workspace %zu < %zu bytes", ws_bytes, need);
+    if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "cf_groupnorm_bwd: workspace null or misaligned");
+    hipError_t e = dtype == CF_F32
+                       ? launch_gn_bwd<float>((const float*)X, (const float*)dY, gamma, beta, mean, rstd, act, slope,
+                                              (float*)dX, dgamma, dbeta, x, groups, ws, stream)
+                       : launch_gn_bwd<uint16_t>((const uint16_t*)X, (const uint16_t*)dY, gamma, beta, mean, rstd, act,
+                                                 slope, (uint16_t*)dX, dgamma, dbeta, x, groups, ws, stream);
+    CF_TRY_HIP(e, "group norm backward");
+    return CF_OK;
+}
+
 // ------------------------------------------------------------ training step
 namespace {
 

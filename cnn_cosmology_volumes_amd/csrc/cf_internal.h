@@ -318,4 +318,14 @@ template <typename T>
 hipError_t launch_bn_bwd(const T* X, const T* dY, const float* gamma, const float* mean, const float* invstd, T* dX,
                          float* dgamma, float* dbeta, const cf_dims& x, void* ws, hipStream_t s);
 
+// Group normalisation with an activation (k_groupnorm.hip); C % groups == 0.
+size_t gn_ws_bytes(cf_dtype dt, const cf_dims& x, int groups, bool bwd);
+template <typename T>
+hipError_t launch_gn_fwd(const T* X, const float* gamma, const float* beta, float eps, cf_act act, float slope, T* Y,
+                         float* mean, float* rstd, const cf_dims& x, int groups, void* ws, hipStream_t s);
+template <typename T>
+hipError_t launch_gn_bwd(const T* X, const T* dY, const float* gamma, const float* beta, const float* mean,
+                         const float* rstd, cf_act act, float slope, T* dX, float* dgamma, float* dbeta,
+                         const cf_dims& x, int groups, void* ws, hipStream_t s);
+
 }  // namespace cf

@@ -1,0 +1,885 @@
+// Group normalisation with an activation on NDHWC activations, forward and
+// backward.
+//
+// Per sample n and group g of cg = C / G neighbouring channels, over the M =
+// D H W cg values of the group:
+//   mean = sum x / M, var = sum (x - mean)^2 / M, rstd = 1 / sqrt(var + eps)
+//   xhat = (x - mean) rstd, z = xhat gamma_c + beta_c, y = act(z)
+// and, with dz = dy act'(z),
+//   dgamma_c = sum_n,voxels dz xhat, dbeta_c = sum_n,voxels dz
+//   dx = rstd (gamma_c dz - s1 - xhat s2), s1 = sum_group gamma dz / M,
+//   s2 = sum_group gamma dz xhat / M.
+//
+// A sample is one flat array of D H W C values read 16 bytes at a time.  A
+// "row" is lcm(V, C) values (V values per 16 bytes), so a thread that steps
+// by whole rows meets the same V channels every time, whatever C is: its
+// coefficients and its V partial sums stay in registers.  Blocks hold a whole
+// number of rows (k rows of `cols` vectors) rounded up to whole waves, so few
+// threads idle for any C.
+// Vectors are loaded and stored without an alignment demand beyond the
+// element's (odd C puts samples at odd offsets); the last S % row values of a
+// sample go element by element.
+//
+// Sums: the forward adds x and x^2 in fp64 (products of fp32 values are exact
+// there up to one rounding), so a mean far above the spread costs no digits;
+// the backward adds fp32 products in fp64.  Blocks write partial sums that
+// are added in a fixed order: no atomics, results are reproducible bit for
+// bit.
+//
+// Groups small enough for one block's registers take a single launch that
+// reads every input once (gn_*_small); larger ones take a reducing launch and
+// an applying launch (with a short joining launch between them in the
+// backward).
+#include "cf_internal.h"
+
+#include <algorithm>
+#include <numeric>
+
+namespace cf {
+namespace {
+
+constexpr int GN_T = 512;        // most threads of a streaming block
+constexpr int GN_TS = 1024;      // most threads of a small-group block
+constexpr int GN_ROWS_F = 8;     // vectors per thread held by the small forward
+constexpr int GN_ROWS_B = 4;     // and by the small backward (of x and dy each)
+constexpr size_t GN_LDS = 65536; // most LDS of a small-group block
+constexpr int GN_BLOCKS = 1024;  // streaming blocks per launch, about 4 per CU
+
+// V values of T as one 16-byte access (V = 1: one element).
+template <typename T, int V> struct Vec {
+    T v[V];
+};
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> vload(const T* p)
+{
+    Vec<T, V> r;
+    __builtin_memcpy(&r, p, sizeof(r));
+    return r;
+}
+template <typename T, int V> __device__ __forceinline__ void vstore(T* p, const Vec<T, V>& r)
+{
+    __builtin_memcpy(p, &r, sizeof(r));
+}
+__device__ __forceinline__ float wide(float x) { return x; }
+__device__ __forceinline__ float wide(uint16_t x) { return bf2f(x); }
+__device__ __forceinline__ void narrow(float& d, float x) { d = x; }
+__device__ __forceinline__ void narrow(uint16_t& d, float x) { d = f2bf(x); }
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    return v;
+}
+
+// How a sample (or a slice of its channels) is cut into rows and blocks.
+struct GnGeom {
+    int64_t S;       // values per sample
+    int64_t nrows;   // whole rows per sample
+    int C, G, cg;
+    int row;         // values per row
+    int cols;        // vectors per row
+    int cc;          // vectors of a row that one block takes
+    int chunks;      // ceil(cols / cc)
+    int k;           // rows a block has in flight; k * cc <= threads
+    int nb;          // blocks per sample and chunk
+};
+
+// First stage of a block's sums.  Thread t < k * cc holds in v[j] a partial
+// sum of row position t % cc * V + j, of W = cc * V positions.  Afterwards
+// sh[i * W + p] for i < the returned count hold position p's total in that
+// many parts.  sh: k * W doubles.
+template <int V>
+__device__ __forceinline__ int sum_rows(const double (&v)[V], double* sh, int k, int cc)
+{
+    const int W = cc * V, t = (int)threadIdx.x, T = (int)blockDim.x;
+    const int parts = max(1, min(k, T / W));
+    __syncthreads();             // the previous sums have been read
+    if (t < k * cc) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) sh[t * V + j] = v[j];
+    }
+    __syncthreads();
+    for (int e = t; e < parts * W; e += T) {
+        double a = sh[e];
+        for (int i = e + parts * W; i < k * W; i += parts * W) a += sh[i];
+        sh[e] = a;
+    }
+    __syncthreads();
+    return parts;
+}
+
+// Total over the row positions p0 <= p < p0 + W whose channel (p mod C) lies
+// in group g, from sum_rows' result; one wave, returned in every lane.
+__device__ __forceinline__ double group_total(const double* sh, int parts, int W, int p0, int g, int cg, int C,
+                                              int row)
+{
+    const int n = row / C * cg;
+    double a = 0.0;
+    for (int e = (int)(threadIdx.x & 63); e < n * parts; e += 64) {
+        const int i = e / n, f = e - i * n;
+        const int p = f / cg * C + g * cg + f % cg - p0;
+        if (p >= 0 && p < W) a += sh[i * W + p];
+    }
+    return wave_sum(a);
+}
+
+// Mean and 1 / sqrt(var + eps) from fp64 sums of x and x^2 over M values.
+__device__ __forceinline__ float2 moments(double s, double ss, double M, float eps)
+{
+    const double mu = s / M;
+    double var = ss / M - mu * mu;
+    if (var < 0.0) var = 0.0;
+    return make_float2((float)mu, (float)(1.0 / sqrt(var + (double)eps)));
+}
+
+// ------------------------------------------------------------- activation
+template <int ACT> __device__ __forceinline__ float act_fwd(float z, float slope)
+{
+    if (ACT == CF_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
+    return z > 0.f ? z : slope * z;
+}
+
+// dz = dy act'(z).  The leaky ReLU's derivative jumps at z = 0, where fp32's
+// rounding of z can take the wrong side: within that rounding (2^-21 of the
+// product's size covers its three roundings) the sign is taken in fp64.
+template <int ACT>
+__device__ __forceinline__ float act_bwd(float dy, float x, float mu, float rs, float xhat, float ga, float be,
+                                         float slope)
+{
+    const float t = xhat * ga;
+    const float z = t + be;
+    if (ACT == CF_ACT_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
+        return dy * (s * (1.f + z * (1.f - s)));
+    }
+    bool pos = z > 0.f;
+    if (fabsf(z) <= 0x1p-21f * fabsf(t))
+        pos = ((double)x - (double)mu) * (double)rs * (double)ga + (double)be > 0.0;
+    return pos ? dy : slope * dy;
+}
+
+// -------------------------------------------------------- streaming forward
+// Partial sums of x and x^2: part[n][block][chunk][group] = (sum, squares).
+template <typename T, int V>
+__global__ __launch_bounds__(GN_T) void gn_stats_kernel(const T* __restrict__ X, GnGeom q, double2* __restrict__ part)
+{
+    extern __shared__ double sh[];
+    const int t = (int)threadIdx.x, r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
+    const T* x = X + (int64_t)blockIdx.z * q.S + (int64_t)col * V;
+    double s[V] = {}, ss[V] = {};
+    auto add1 = [&](int j, T w) {
+        const double d = (double)wide(w);
+        s[j] += d;
+        ss[j] = fma(d, d, ss[j]);
+    };
+    if (r < q.k && col < q.cols) {
+        const int64_t step = (int64_t)q.nb * q.k;
+        int64_t i = (int64_t)blockIdx.x * q.k + r;
+        for (; i + 3 * step < q.nrows; i += 4 * step) {
+            Vec<T, V> u[4];
+#pragma unroll
+            for (int l = 0; l < 4; ++l) u[l] = vload<T, V>(x + (i + l * step) * q.row);
+#pragma unroll
+            for (int l = 0; l < 4; ++l)
+#pragma unroll
+                for (int j = 0; j < V; ++j) add1(j, u[l].v[j]);
+        }
+        for (; i < q.nrows; i += step) {
+            const Vec<T, V> u = vload<T, V>(x + i * q.row);
+#pragma unroll
+            for (int j = 0; j < V; ++j) add1(j, u.v[j]);
+        }
+        if (blockIdx.x == 0 && r == 0) {      // the values after the last whole row
+            const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < left) add1(j, x[q.nrows * q.row + j]);
+        }
+    }
+    const int p0 = (int)blockIdx.y * q.cc * V, W = q.cc * V;
+    double2* out = part + (((int64_t)blockIdx.z * q.nb + blockIdx.x) * q.chunks + blockIdx.y) * q.G;
+    int parts = sum_rows<V>(s, sh, q.k, q.cc);
+    for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
+        const double a = group_total(sh, parts, W, p0, g, q.cg, q.C, q.row);
+        if ((t & 63) == 0) out[g].x = a;
+    }
+    parts = sum_rows<V>(ss, sh, q.k, q.cc);
+    for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
+        const double a = group_total(sh, parts, W, p0, g, q.cg, q.C, q.row);
+        if ((t & 63) == 0) out[g].y = a;
+    }
+}
+
+// y = act((x - mean) (rstd gamma) + beta).  Every block first adds its
+// sample's partial sums (npart of them per group, in the same order).
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X, GnGeom q, int npart,
+                                                        const double2* __restrict__ part,
+                                                        const float* __restrict__ gamma,
+                                                        const float* __restrict__ beta, float eps, float slope,
+                                                        T* __restrict__ Y, float* __restrict__ mean,
+                                                        float* __restrict__ rstd)
+{
+    extern __shared__ float2 stat[];     // [G] mean, rstd
+    const int t = (int)threadIdx.x, n = (int)blockIdx.z;
+    part += (int64_t)n * npart * q.G;
+    for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
+        double s = 0.0, ss = 0.0;
+        for (int b = t & 63; b < npart; b += 64) {
+            const double2 v = part[(int64_t)b * q.G + g];
+            s += v.x;
+            ss += v.y;
+        }
+        s = wave_sum(s);
+        ss = wave_sum(ss);
+        if ((t & 63) == 0) {
+            const float2 m = moments(s, ss, (double)(q.S / q.C) * q.cg, eps);
+            stat[g] = m;
+            if (blockIdx.x == 0 && blockIdx.y == 0) {
+                mean[(int64_t)n * q.G + g] = m.x;
+                rstd[(int64_t)n * q.G + g] = m.y;
+            }
+        }
+    }
+    __syncthreads();
+    const int r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
+    if (r >= q.k || col >= q.cols) return;
+    float mu[V], sc[V], be[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (col * V + j) % q.C;
+        const float2 m = stat[c / q.cg];
+        mu[j] = m.x;
+        sc[j] = m.y * gamma[c];
+        be[j] = beta[c];
+    }
+    const int64_t at = (int64_t)n * q.S + (int64_t)col * V;
+    const T* x = X + at;
+    T* y = Y + at;
+    auto out1 = [&](int j, T w) { return act_fwd<ACT>(fmaf(wide(w) - mu[j], sc[j], be[j]), slope); };
+    auto out = [&](const Vec<T, V>& u, int64_t i) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) narrow(o.v[j], out1(j, u.v[j]));
+        vstore<T, V>(y + i * q.row, o);
+    };
+    const int64_t step = (int64_t)q.nb * q.k;
+    int64_t i = (int64_t)blockIdx.x * q.k + r;
+    for (; i + 3 * step < q.nrows; i += 4 * step) {
+        Vec<T, V> u[4];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) u[l] = vload<T, V>(x + (i + l * step) * q.row);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) out(u[l], i + l * step);
+    }
+    for (; i < q.nrows; i += step) out(vload<T, V>(x + i * q.row), i);
+    if (blockIdx.x == 0 && r == 0) {
+        const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) narrow(y[q.nrows * q.row + j], out1(j, x[q.nrows * q.row + j]));
+    }
+}
+
+// ------------------------------------------------------- streaming backward
+// Per-channel partial sums of dz and dz xhat: part[n][block][chunk][channel].
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(GN_T) void gn_bwd_sums_kernel(const T* __restrict__ X, const T* __restrict__ dY,
+                                                           GnGeom q, const float* __restrict__ gamma,
+                                                           const float* __restrict__ beta,
+                                                           const float* __restrict__ mean,
+                                                           const float* __restrict__ rstd, float slope,
+                                                           double2* __restrict__ part)
+{
+    extern __shared__ double sh[];
+    const int t = (int)threadIdx.x, r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
+    const int64_t at = (int64_t)blockIdx.z * q.S + (int64_t)col * V;
+    const T* x = X + at;
+    const T* dy = dY + at;
+    double a[V] = {}, b[V] = {};
+    if (r < q.k && col < q.cols) {
+        float mu[V], rs[V], ga[V], be[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (col * V + j) % q.C;
+            const int64_t g = (int64_t)blockIdx.z * q.G + c / q.cg;
+            mu[j] = mean[g];
+            rs[j] = rstd[g];
+            ga[j] = gamma[c];
+            be[j] = beta[c];
+        }
+        auto add1 = [&](int j, T xw, T dw) {
+            const float xv = wide(xw), xhat = (xv - mu[j]) * rs[j];
+            const float dz = act_bwd<ACT>(wide(dw), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+            a[j] += (double)dz;
+            b[j] += (double)(dz * xhat);
+        };
+        const int64_t step = (int64_t)q.nb * q.k;
+        int64_t i = (int64_t)blockIdx.x * q.k + r;
+        for (; i + step < q.nrows; i += 2 * step) {
+            Vec<T, V> u[2], d[2];
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                u[l] = vload<T, V>(x + (i + l * step) * q.row);
+                d[l] = vload<T, V>(dy + (i + l * step) * q.row);
+            }
+#pragma unroll
+            for (int l = 0; l < 2; ++l)
+#pragma unroll
+                for (int j = 0; j < V; ++j) add1(j, u[l].v[j], d[l].v[j]);
+        }
+        for (; i < q.nrows; i += step) {
+            const Vec<T, V> u = vload<T, V>(x + i * q.row), d = vload<T, V>(dy + i * q.row);
+#pragma unroll
+            for (int j = 0; j < V; ++j) add1(j, u.v[j], d.v[j]);
+        }
+        if (blockIdx.x == 0 && r == 0) {
+            const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < left) add1(j, x[q.nrows * q.row + j], dy[q.nrows * q.row + j]);
+        }
+    }
+    const int p0 = (int)blockIdx.y * q.cc * V, W = q.cc * V;
+    double2* out = part + (((int64_t)blockIdx.z * q.nb + blockIdx.x) * q.chunks + blockIdx.y) * q.C;
+    auto channel = [&](int c, int parts) {
+        double v = 0.0;
+        for (int p = c - p0; p < W && p < q.row - p0; p += q.C)
+            if (p >= 0)
+                for (int i = 0; i < parts; ++i) v += sh[i * W + p];
+        return v;
+    };
+    int parts = sum_rows<V>(a, sh, q.k, q.cc);
+    for (int c = t; c < q.C; c += (int)blockDim.x) out[c].x = channel(c, parts);
+    parts = sum_rows<V>(b, sh, q.k, q.cc);
+    for (int c = t; c < q.C; c += (int)blockDim.x) out[c].y = channel(c, parts);
+}
+
+// One block per (group, sample): the blocks' partials to per-sample channel
+// sums chan[n][c] = (sum dz, sum dz xhat) and the group's s12[n][g] = (s1, s2).
+constexpr int GN_TJ = 256;
+__global__ __launch_bounds__(GN_TJ) void gn_bwd_join_kernel(GnGeom q, int npart, const double2* __restrict__ part,
+                                                            const float* __restrict__ gamma,
+                                                            double2* __restrict__ chan, float2* __restrict__ s12)
+{
+    __shared__ double la[GN_TJ], lb[GN_TJ];
+    const int t = (int)threadIdx.x, g = (int)blockIdx.x, n = (int)blockIdx.y;
+    const int cw = min(q.cg, GN_TJ), ways = GN_TJ / cw;      // `ways` threads share a channel
+    part += (int64_t)n * npart * q.C;
+    double s1 = 0.0, s2 = 0.0;
+    for (int c0 = 0; c0 < q.cg; c0 += cw) {
+        const int i = t % cw, way = t / cw, c = g * q.cg + c0 + i;
+        const bool on = way < ways && c0 + i < q.cg;
+        double a = 0.0, b = 0.0;
+        if (on)
+            for (int p = way; p < npart; p += ways) {
+                const double2 v = part[(int64_t)p * q.C + c];
+                a += v.x;
+                b += v.y;
+            }
+        __syncthreads();
+        la[t] = a;
+        lb[t] = b;
+        __syncthreads();
+        if (on && way == 0) {
+            for (int w = 1; w < ways; ++w) {
+                a += la[w * cw + i];
+                b += lb[w * cw + i];
+            }
+            chan[(int64_t)n * q.C + c] = make_double2(a, b);
+            s1 += (double)gamma[c] * a;
+            s2 += (double)gamma[c] * b;
+        }
+    }
+    __syncthreads();
+    la[t] = s1;
+    lb[t] = s2;
+    __syncthreads();
+    if (t < 64) {
+        double a = 0.0, b = 0.0;
+        for (int i = t; i < GN_TJ; i += 64) {
+            a += la[i];
+            b += lb[i];
+        }
+        a = wave_sum(a);
+        b = wave_sum(b);
+        const double M = (double)(q.S / q.C) * q.cg;
+        if (t == 0) s12[(int64_t)n * q.G + g] = make_float2((float)(a / M), (float)(b / M));
+    }
+}
+
+// dx = rstd (gamma dz - s1 - xhat s2); the first block of sample 0 also adds
+// the samples' channel sums into dgamma and dbeta.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(GN_T) void gn_bwd_apply_kernel(const T* __restrict__ X, const T* __restrict__ dY,
+                                                            GnGeom q, int N, const float* __restrict__ gamma,
+                                                            const float* __restrict__ beta,
+                                                            const float* __restrict__ mean,
+                                                            const float* __restrict__ rstd, float slope,
+                                                            const double2* __restrict__ chan,
+                                                            const float2* __restrict__ s12, T* __restrict__ dX,
+                                                            float* __restrict__ dgamma, float* __restrict__ dbeta)
+{
+    const int t = (int)threadIdx.x, r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        for (int c = t; c < q.C; c += (int)blockDim.x) {
+            double a = 0.0, b = 0.0;
+            for (int n = 0; n < N; ++n) {
+                const double2 v = chan[(int64_t)n * q.C + c];
+                a += v.x;
+                b += v.y;
+            }
+            dbeta[c] = (float)a;
+            dgamma[c] = (float)b;
+        }
+    if (r >= q.k || col >= q.cols) return;
+    float mu[V], rs[V], ga[V], be[V], s1[V], s2[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = (col * V + j) % q.C;
+        const int64_t g = (int64_t)blockIdx.z * q.G + c / q.cg;
+        mu[j] = mean[g];
+        rs[j] = rstd[g];
+        ga[j] = gamma[c];
+        be[j] = beta[c];
+        s1[j] = s12[g].x;
+        s2[j] = s12[g].y;
+    }
+    const int64_t at = (int64_t)blockIdx.z * q.S + (int64_t)col * V;
+    const T* x = X + at;
+    const T* dy = dY + at;
+    T* dx = dX + at;
+    auto out1 = [&](int j, T xw, T dw) {
+        const float xv = wide(xw), xhat = (xv - mu[j]) * rs[j];
+        const float dz = act_bwd<ACT>(wide(dw), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+        return rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]);
+    };
+    auto out = [&](const Vec<T, V>& u, const Vec<T, V>& d, int64_t i) {
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) narrow(o.v[j], out1(j, u.v[j], d.v[j]));
+        vstore<T, V>(dx + i * q.row, o);
+    };
+    const int64_t step = (int64_t)q.nb * q.k;
+    int64_t i = (int64_t)blockIdx.x * q.k + r;
+    for (; i + step < q.nrows; i += 2 * step) {
+        Vec<T, V> u[2], d[2];
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+            u[l] = vload<T, V>(x + (i + l * step) * q.row);
+            d[l] = vload<T, V>(dy + (i + l * step) * q.row);
+        }
+#pragma unroll
+        for (int l = 0; l < 2; ++l) out(u[l], d[l], i + l * step);
+    }
+    for (; i < q.nrows; i += step) out(vload<T, V>(x + i * q.row), vload<T, V>(dy + i * q.row), i);
+    if (blockIdx.x == 0 && r == 0) {
+        const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) narrow(dx[q.nrows * q.row + j], out1(j, x[q.nrows * q.row + j], dy[q.nrows * q.row + j]));
+    }
+}
+
+// ------------------------------------------------------------ small groups
+// A slice of `gs` whole groups (row = gs * cg values, one row per voxel) of
+// one sample held in one block's registers: nrows <= k * rows per thread.
+struct GnSlice {
+    int64_t S;       // values per sample
+    int nrows;       // voxels per sample
+    int C, G, cg;
+    int gs;          // groups of a slice
+    int cols;        // vectors of a slice's row
+    int k;           // rows in flight; k * cols <= threads
+};
+
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(GN_TS) void gn_small_kernel(const T* __restrict__ X, GnSlice q,
+                                                         const float* __restrict__ gamma,
+                                                         const float* __restrict__ beta, float eps, float slope,
+                                                         T* __restrict__ Y, float* __restrict__ mean,
+                                                         float* __restrict__ rstd)
+{
+    extern __shared__ double sh[];
+    const int t = (int)threadIdx.x, r = t / q.cols, col = t % q.cols, n = (int)blockIdx.y;
+    const int W = q.gs * q.cg, c0 = (int)blockIdx.x * W, g0 = (int)blockIdx.x * q.gs;
+    float2* stat = reinterpret_cast<float2*>(sh + q.k * W);      // [gs] mean, rstd; then [gs] sums of x
+    const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
+    const double M = (double)q.nrows * q.cg;
+    Vec<T, V> u[GN_ROWS_F];
+    double s[V] = {}, ss[V] = {};
+    const bool on = r < q.k;
+#pragma unroll
+    for (int l = 0; l < GN_ROWS_F; ++l) {
+        const int i = r + l * q.k;
+        if (on && i < q.nrows) u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
+    }
+#pragma unroll
+    for (int l = 0; l < GN_ROWS_F; ++l)
+        if (on && r + l * q.k < q.nrows)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const double d = (double)wide(u[l].v[j]);
+                s[j] += d;
+                ss[j] = fma(d, d, ss[j]);
+            }
+    int parts = sum_rows<V>(s, sh, q.k, q.cols);
+    for (int g = t >> 6; g < q.gs; g += (int)blockDim.x >> 6) {
+        const double a = group_total(sh, parts, W, 0, g, q.cg, W, W);
+        if ((t & 63) == 0) sh[q.k * W + q.gs + g] = a;
+    }
+    parts = sum_rows<V>(ss, sh, q.k, q.cols);
+    for (int g = t >> 6; g < q.gs; g += (int)blockDim.x >> 6) {
+        const double a = group_total(sh, parts, W, 0, g, q.cg, W, W);
+        if ((t & 63) == 0) {
+            const float2 m = moments(sh[q.k * W + q.gs + g], a, M, eps);
+            stat[g] = m;
+            mean[(int64_t)n * q.G + g0 + g] = m.x;
+            rstd[(int64_t)n * q.G + g0 + g] = m.y;
+        }
+    }
+    __syncthreads();
+    if (!on) return;
+    float mu[V], sc[V], be[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = col * V + j;
+        const float2 m = stat[c / q.cg];
+        mu[j] = m.x;
+        sc[j] = m.y * gamma[c0 + c];
+        be[j] = beta[c0 + c];
+    }
+#pragma unroll
+    for (int l = 0; l < GN_ROWS_F; ++l) {
+        const int i = r + l * q.k;
+        if (i >= q.nrows) continue;
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            narrow(o.v[j], act_fwd<ACT>(fmaf(wide(u[l].v[j]) - mu[j], sc[j], be[j]), slope));
+        vstore<T, V>(Y + at + (int64_t)i * q.C, o);
+    }
+}
+
+// The backward of a slice: the samples one after another in one block, so
+// that dgamma and dbeta need no second launch.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(GN_TS) void gn_bwd_small_kernel(const T* __restrict__ X, const T* __restrict__ dY,
+                                                             GnSlice q, int N, const float* __restrict__ gamma,
+                                                             const float* __restrict__ beta,
+                                                             const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd, float slope,
+                                                             T* __restrict__ dX, float* __restrict__ dgamma,
+                                                             float* __restrict__ dbeta)
+{
+    extern __shared__ double sh[];
+    const int t = (int)threadIdx.x, T_ = (int)blockDim.x, r = t / q.cols, col = t % q.cols;
+    const int W = q.gs * q.cg, c0 = (int)blockIdx.x * W, g0 = (int)blockIdx.x * q.gs;
+    double* cha = sh + q.k * W;              // [W] channel sums of dz, then of dz xhat
+    double* chb = cha + W;
+    double* tota = chb + W;                  // [W] the same over the samples
+    double* totb = tota + W;
+    float2* s12 = reinterpret_cast<float2*>(totb + W);
+    const double M = (double)q.nrows * q.cg;
+    const bool on = r < q.k;
+    for (int c = t; c < W; c += T_) tota[c] = totb[c] = 0.0;
+    float ga[V] = {}, be[V] = {};
+    if (on)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            ga[j] = gamma[c0 + col * V + j];
+            be[j] = beta[c0 + col * V + j];
+        }
+    for (int n = 0; n < N; ++n) {
+        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
+        Vec<T, V> u[GN_ROWS_B], d[GN_ROWS_B];
+        float mu[V] = {}, rs[V] = {};
+#pragma unroll
+        for (int l = 0; l < GN_ROWS_B; ++l) {
+            const int i = r + l * q.k;
+            if (on && i < q.nrows) {
+                u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
+                d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
+            }
+        }
+        if (on)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int64_t g = (int64_t)n * q.G + g0 + (col * V + j) / q.cg;
+                mu[j] = mean[g];
+                rs[j] = rstd[g];
+            }
+        double a[V] = {}, b[V] = {};
+#pragma unroll
+        for (int l = 0; l < GN_ROWS_B; ++l)
+            if (on && r + l * q.k < q.nrows)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+                    const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+                    a[j] += (double)dz;
+                    b[j] += (double)(dz * xhat);
+                }
+        int parts = sum_rows<V>(a, sh, q.k, q.cols);
+        for (int c = t; c < W; c += T_) {
+            double v = 0.0;
+            for (int i = 0; i < parts; ++i) v += sh[i * W + c];
+            cha[c] = v;
+            tota[c] += v;
+        }
+        parts = sum_rows<V>(b, sh, q.k, q.cols);
+        for (int c = t; c < W; c += T_) {
+            double v = 0.0;
+            for (int i = 0; i < parts; ++i) v += sh[i * W + c];
+            chb[c] = v;
+            totb[c] += v;
+        }
+        __syncthreads();
+        for (int g = t >> 6; g < q.gs; g += T_ >> 6) {
+            double s1 = 0.0, s2 = 0.0;
+            for (int i = t & 63; i < q.cg; i += 64) {
+                const double gm = (double)gamma[c0 + g * q.cg + i];
+                s1 += gm * cha[g * q.cg + i];
+                s2 += gm * chb[g * q.cg + i];
+            }
+            s1 = wave_sum(s1);
+            s2 = wave_sum(s2);
+            if ((t & 63) == 0) s12[g] = make_float2((float)(s1 / M), (float)(s2 / M));
+        }
+        __syncthreads();
+        if (on) {
+            float s1[V], s2[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float2 v = s12[(col * V + j) / q.cg];
+                s1[j] = v.x;
+                s2[j] = v.y;
+            }
+#pragma unroll
+            for (int l = 0; l < GN_ROWS_B; ++l) {
+                const int i = r + l * q.k;
+                if (i >= q.nrows) continue;
+                Vec<T, V> o;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+                    const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+                    narrow(o.v[j], rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
+                }
+                vstore<T, V>(dX + at + (int64_t)i * q.C, o);
+            }
+        }
+    }
+    for (int c = t; c < W; c += T_) {
+        dbeta[c0 + c] = (float)tota[c];
+        dgamma[c0 + c] = (float)totb[c];
+    }
+}
+
+// -------------------------------------------------------------------- plans
+int up64(int v) { return (v + 63) / 64 * 64; }
+size_t up256b(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <typename T> constexpr int vec_of() { return 16 / (int)sizeof(T); }
+
+template <typename T> GnGeom gn_geom(const cf_dims& x, int G)
+{
+    constexpr int V = vec_of<T>();
+    GnGeom q{};
+    q.C = (int)x.c;
+    q.G = G;
+    q.cg = q.C / G;
+    q.S = x.d * x.h * x.w * x.c;
+    q.row = (int)std::lcm((int64_t)V, x.c);
+    q.cols = q.row / V;
+    q.chunks = (q.cols + GN_T - 1) / GN_T;
+    q.cc = (q.cols + q.chunks - 1) / q.chunks;
+    q.k = GN_T / q.cc;
+    q.nrows = q.S / q.row;
+    // enough blocks to fill the chip, at least four rows per thread
+    const int64_t want = (q.nrows + 4 * q.k - 1) / (4 * q.k);
+    int64_t most = GN_BLOCKS / (x.n * q.chunks);
+    if (most < 1) most = 1;
+    q.nb = (int)(want < 1 ? 1 : want < most ? want : most);
+    return q;
+}
+
+// The slice plan of a shape, or cols = 0 where a group does not fit one block.
+// `held` vectors per thread, `arrays` doubles per channel beside the sums in
+// LDS (4 in the backward).
+template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int held, int arrays)
+{
+    GnSlice q{};
+    const int64_t vox = x.d * x.h * x.w;
+    const int threads = V == 8 ? GN_T : GN_TS;
+    q.C = (int)x.c;
+    q.G = G;
+    q.cg = q.C / G;
+    q.S = vox * x.c;
+    if (vox > (int64_t)threads * held || q.C % V) return q;
+    q.nrows = (int)vox;
+    // whole vectors, and 64 bytes of a voxel where the registers allow it
+    for (int gs = 1; gs <= G; ++gs) {
+        const int W = gs * q.cg;
+        if (G % gs || W % V) continue;
+        const int cols = W / V;
+        if (cols > threads) break;
+        const int k = (int)std::min<int64_t>(vox, threads / cols);
+        if ((vox + k - 1) / k > held) break;
+        if (((size_t)(k + arrays) * W + 2 * gs) * sizeof(double) > GN_LDS) break;
+        q.gs = gs;
+        q.cols = cols;
+        q.k = k;
+        if (W * esize >= 64) break;
+    }
+    return q;
+}
+
+// Samples that one block of the small backward takes in turn.
+constexpr int GN_SMALL_N = 4;
+
+template <typename T> GnSlice fwd_slice(const cf_dims& x, int G, int* V)
+{
+    constexpr int v = vec_of<T>();
+    *V = v;
+    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_ROWS_F, 0);
+    if (q.cols) return q;
+    *V = 1;
+    return gn_slice<1>(x, G, (int)sizeof(T), GN_ROWS_F, 0);
+}
+template <typename T> GnSlice bwd_slice(const cf_dims& x, int G, int* V)
+{
+    constexpr int v = vec_of<T>();
+    *V = v;
+    if (x.n > GN_SMALL_N) return GnSlice{};
+    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_ROWS_B, 4);
+    if (q.cols) return q;
+    *V = 1;
+    return gn_slice<1>(x, G, (int)sizeof(T), GN_ROWS_B, 4);
+}
+
+template <typename T, int V, int ACT>
+hipError_t run_small_fwd(const GnSlice& q, int64_t N, const T* X, const float* gamma, const float* beta, float eps,
+                         float slope, T* Y, float* mean, float* rstd, hipStream_t s)
+{
+    const size_t lds = ((size_t)q.k * q.gs * q.cg + 2 * q.gs) * sizeof(double);
+    hipLaunchKernelGGL((gn_small_kernel<T, V, ACT>), dim3((unsigned)(q.G / q.gs), (unsigned)N),
+                       dim3((unsigned)up64(q.k * q.cols)), lds, s, X, q, gamma, beta, eps, slope, Y, mean, rstd);
+    return hipGetLastError();
+}
+
+template <typename T, int V, int ACT>
+hipError_t run_small_bwd(const GnSlice& q, int64_t N, const T* X, const T* dY, const float* gamma, const float* beta,
+                         const float* mean, const float* rstd, float slope, T* dX, float* dgamma, float* dbeta,
+                         hipStream_t s)
+{
+    const size_t lds = ((size_t)(q.k + 4) * q.gs * q.cg + q.gs) * sizeof(double);
+    hipLaunchKernelGGL((gn_bwd_small_kernel<T, V, ACT>), dim3((unsigned)(q.G / q.gs)),
+                       dim3((unsigned)up64(q.k * q.cols)), lds, s, X, dY, q, (int)N, gamma, beta, mean, rstd, slope,
+                       dX, dgamma, dbeta);
+    return hipGetLastError();
+}
+
+template <typename T, int ACT>
+hipError_t run_fwd(const T* X, const float* gamma, const float* beta, float eps, float slope, T* Y, float* mean,
+                   float* rstd, const cf_dims& x, int G, void* ws, hipStream_t s)
+{
+    constexpr int V = vec_of<T>();
+    int v;
+    const GnSlice sl = fwd_slice<T>(x, G, &v);
+    if (sl.cols)
+        return v == 1 ? run_small_fwd<T, 1, ACT>(sl, x.n, X, gamma, beta, eps, slope, Y, mean, rstd, s)
+                      : run_small_fwd<T, V, ACT>(sl, x.n, X, gamma, beta, eps, slope, Y, mean, rstd, s);
+    const GnGeom q = gn_geom<T>(x, G);
+    const dim3 grid((unsigned)q.nb, (unsigned)q.chunks, (unsigned)x.n), block((unsigned)up64(q.k * q.cc));
+    double2* part = (double2*)ws;
+    hipLaunchKernelGGL((gn_stats_kernel<T, V>), grid, block, (size_t)q.k * q.cc * V * sizeof(double), s, X, q, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gn_apply_kernel<T, V, ACT>), grid, block, (size_t)G * sizeof(float2), s, X, q,
+                       q.nb * q.chunks, (const double2*)part, gamma, beta, eps, slope, Y, mean, rstd);
+    return hipGetLastError();
+}
+
+template <typename T, int ACT>
+hipError_t run_bwd(const T* X, const T* dY, const float* gamma, const float* beta, const float* mean,
+                   const float* rstd, float slope, T* dX, float* dgamma, float* dbeta, const cf_dims& x, int G,
+                   void* ws, hipStream_t s)
+{
+    constexpr int V = vec_of<T>();
+    int v;
+    const GnSlice sl = bwd_slice<T>(x, G, &v);
+    if (sl.cols)
+        return v == 1 ? run_small_bwd<T, 1, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, s)
+                      : run_small_bwd<T, V, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, s);
+    const GnGeom q = gn_geom<T>(x, G);
+    const int npart = q.nb * q.chunks;
+    char* p = (char*)ws;
+    double2* part = (double2*)p;
+    p += up256b((size_t)x.n * npart * q.C * sizeof(double2));
+    double2* chan = (double2*)p;
+    p += up256b((size_t)x.n * q.C * sizeof(double2));
+    float2* s12 = (float2*)p;
+    const dim3 grid((unsigned)q.nb, (unsigned)q.chunks, (unsigned)x.n), block((unsigned)up64(q.k * q.cc));
+    hipLaunchKernelGGL((gn_bwd_sums_kernel<T, V, ACT>), grid, block, (size_t)q.k * q.cc * V * sizeof(double), s, X, dY,
+                       q, gamma, beta, mean, rstd, slope, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(gn_bwd_join_kernel, dim3((unsigned)G, (unsigned)x.n), dim3(GN_TJ), 0, s, q, npart,
+                       (const double2*)part, gamma, chan, s12);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((gn_bwd_apply_kernel<T, V, ACT>), grid, block, 0, s, X, dY, q, (int)x.n, gamma, beta, mean,
+                       rstd, slope, (const double2*)chan, (const float2*)s12, dX, dgamma, dbeta);
+    return hipGetLastError();
+}
+
+template <typename T> size_t ws_bytes(const cf_dims& x, int G, bool bwd)
+{
+    int v;
+    if ((bwd ? bwd_slice<T>(x, G, &v) : fwd_slice<T>(x, G, &v)).cols) return 0;
+    const GnGeom q = gn_geom<T>(x, G);
+    const size_t npart = (size_t)x.n * q.nb * q.chunks;
+    if (!bwd) return up256b(npart * G * sizeof(double2));
+    return up256b(npart * q.C * sizeof(double2)) + up256b((size_t)x.n * q.C * sizeof(double2)) +
+           up256b((size_t)x.n * G * sizeof(float2));
+}
+
+}  // namespace
+
+size_t gn_ws_bytes(cf_dtype dt, const cf_dims& x, int G, bool bwd)
+{
+    return dt == CF_F32 ? ws_bytes<float>(x, G, bwd) : ws_bytes<uint16_t>(x, G, bwd);
+}
+
+template <typename T>
+hipError_t launch_gn_fwd(const T* X, const float* gamma, const float* beta, float eps, cf_act act, float slope, T* Y,
+                         float* mean, float* rstd, const cf_dims& x, int G, void* ws, hipStream_t s)
+{
+    return act == CF_ACT_SILU
+               ? run_fwd<T, CF_ACT_SILU>(X, gamma, beta, eps, slope, Y, mean, rstd, x, G, ws, s)
+               : run_fwd<T, CF_ACT_LRELU>(X, gamma, beta, eps, slope, Y, mean, rstd, x, G, ws, s);
+}
+
+template <typename T>
+hipError_t launch_gn_bwd(const T* X, const T* dY, const float* gamma, const float* beta, const float* mean,
+                         const float* rstd, cf_act act, float slope, T* dX, float* dgamma, float* dbeta,
+                         const cf_dims& x, int G, void* ws, hipStream_t s)
+{
+    return act == CF_ACT_SILU ? run_bwd<T, CF_ACT_SILU>(X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, x,
+                                                        G, ws, s)
+                              : run_bwd<T, CF_ACT_LRELU>(X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, x,
+                                                         G, ws, s);
+}
+
+template hipError_t launch_gn_fwd<float>(const float*, const float*, const float*, float, cf_act, float, float*,
+                                         float*, float*, const cf_dims&, int, void*, hipStream_t);
+template hipError_t launch_gn_fwd<uint16_t>(const uint16_t*, const float*, const float*, float, cf_act, float,
+                                            uint16_t*, float*, float*, const cf_dims&, int, void*, hipStream_t);
+template hipError_t launch_gn_bwd<float>(const float*, const float*, const float*, const float*, const float*,
+                                         const float*, cf_act, float, float*, float*, float*, const cf_dims&, int,
+                                         void*, hipStream_t);
+template hipError_t launch_gn_bwd<uint16_t>(const uint16_t*, const uint16_t*, const float*, const float*,
+                                            const float*, const float*, cf_act, float, uint16_t*, float*, float*,
+                                            const cf_dims&, int, void*, hipStream_t);
+
+}  // namespace cf

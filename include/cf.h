@@ -336,6 +336,45 @@ cf_status cf_batchnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
                            const float* mean, const float* invstd, void* dX, float* dgamma, float* dbeta,
                            void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------- group norm with activation */
+
+/* Activation applied to the normalised values. */
+typedef enum {
+    CF_ACT_LRELU = 0,  /* z > 0 ? z : slope * z, slope >= 0 (1 = none) */
+    CF_ACT_SILU = 1    /* z / (1 + exp(-z)); slope is ignored */
+} cf_act;
+
+/* Workspace bytes for cf_groupnorm_fwd (backward = 0) or cf_groupnorm_bwd
+ * (backward != 0); 0 is possible.  Returns 0 also for invalid arguments. */
+size_t cf_groupnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t groups, int32_t backward);
+
+/* Group normalisation with an activation: a stand-in for batch norm after a
+ * convolution ([OY] Sec. IV) that needs no statistics of other samples, so
+ * it also serves one volume per GPU.  For each sample n and each of `groups`
+ * groups of cg = x.c / groups neighbouring channels, over M = d h w cg values:
+ *   mean = sum X / M, var = sum (X - mean)^2 / M (biased)
+ *   rstd = 1 / sqrt(var + eps);  Y = act((X - mean) * rstd * gamma_c + beta_c)
+ *   X, Y [x.n, x.d, x.h, x.w, x.c] (dtype); gamma, beta [x.c] fp32;
+ *   mean, rstd [x.n, groups] fp32, outputs for the backward.
+ * x.c must be a multiple of groups (else CF_ERR_INVALID) and at most 4096,
+ * x.n at most 65535 (else CF_ERR_UNSUPPORTED); eps positive and finite.
+ * Statistics are summed in fp64 in a fixed order: results are reproducible
+ * bit for bit. */
+cf_status cf_groupnorm_fwd(cf_dtype dtype, cf_dims x, const void* X, int32_t groups, const float* gamma,
+                           const float* beta, float eps, cf_act act, float slope, void* Y, float* mean,
+                           float* rstd, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Backward of cf_groupnorm_fwd from its mean and rstd.  With xhat =
+ * (X - mean) rstd, z = xhat gamma + beta and dz = dY act'(z) (the leaky
+ * ReLU's derivative is slope at z <= 0):
+ *   dbeta_c = sum dz;  dgamma_c = sum dz xhat     (over n, d, h, w; fp32)
+ *   dX = rstd (gamma dz - s1 - xhat s2), s1 and s2 the group's sums of
+ *   gamma dz and gamma dz xhat divided by M       (dtype) */
+cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void* dY, int32_t groups,
+                           const float* gamma, const float* beta, const float* mean, const float* rstd, cf_act act,
+                           float slope, void* dX, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
 /* --------------------------------------------------------- training step */
 
 /* Caller-owned second stream for cf_train_step.  The blocks' weight

@@ -499,6 +499,50 @@ def batchnorm_bwd(x, dy, gamma, mean, invstd):
     return dx.reshape(x.shape), dgamma, dbeta
 
 
+# --------------------------------------------------------------- group norm
+def _act(z, act, slope):
+    """The activation and its derivative at z: "lrelu" or "silu"."""
+    if act == "silu":
+        s = np.where(z >= 0, 1.0 / (1.0 + np.exp(-np.abs(z))), np.exp(-np.abs(z)) / (1.0 + np.exp(-np.abs(z))))
+        return z * s, s + z * s * (1.0 - s)
+    return np.where(z > 0, z, slope * z), np.where(z > 0, 1.0, slope)
+
+
+def groupnorm_fwd(x, groups, gamma, beta, eps, act, slope):
+    """Group normalisation of NDHWC x with an activation: for each sample and
+    group of C / groups neighbouring channels, mean and biased variance over
+    the group's values, xhat = (x - mean) / sqrt(var + eps),
+    y = act(gamma xhat + beta).  Returns (y, mean, rstd) with mean and rstd
+    [N, groups]."""
+    x = _f64(x)
+    N, C = x.shape[0], x.shape[-1]
+    t = x.reshape(N, -1, groups, C // groups)
+    mean = t.mean(axis=(1, 3))
+    c = t - mean[:, None, :, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=(1, 3)) + eps)
+    z = (c * rstd[:, None, :, None]).reshape(N, -1, C) * _f64(gamma) + _f64(beta)
+    return _act(z, act, slope)[0].reshape(x.shape), mean, rstd
+
+
+def groupnorm_bwd(x, dy, groups, gamma, beta, mean, rstd, act, slope):
+    """Backward of groupnorm_fwd through the statistics:
+        dz = dy act'(z);  dbeta = sum dz;  dgamma = sum dz xhat
+        dx = rstd (gamma dz - mean_group(gamma dz) - xhat mean_group(gamma dz xhat)).
+    Returns (dx, dgamma, dbeta)."""
+    x, dy, gamma, beta = _f64(x), _f64(dy), _f64(gamma), _f64(beta)
+    N, C = x.shape[0], x.shape[-1]
+    sh = (N, -1, groups, C // groups)
+    mean, rstd = _f64(mean)[:, None, :, None], _f64(rstd)[:, None, :, None]
+    ga, be = gamma.reshape(groups, -1), beta.reshape(groups, -1)
+    xhat = (x.reshape(sh) - mean) * rstd
+    dz = dy.reshape(sh) * _act(xhat * ga + be, act, slope)[1]
+    dbeta = dz.sum(axis=(0, 1)).reshape(C)
+    dgamma = (dz * xhat).sum(axis=(0, 1)).reshape(C)
+    u = ga * dz
+    dx = rstd * (u - u.mean(axis=(1, 3), keepdims=True) - xhat * (u * xhat).mean(axis=(1, 3), keepdims=True))
+    return dx.reshape(x.shape), dgamma, dbeta
+
+
 # ------------------------------------------------- general network step
 def net_param_shapes(cin, layers, dense, batch_norm, dense_bias, in_size):
     """Parameter shapes in the order the step takes them: per conv layer W
