@@ -56,6 +56,7 @@ CF_MAX_DENSE = 4
 CF_POOL_MAX, CF_POOL_AVG, CF_POOL_NONE = 0, 1, 2
 CF_OPT_SGD, CF_OPT_ADAM_LARC = 0, 1
 CF_ACT_LRELU, CF_ACT_SILU = 0, 1
+CF_MUON_SCALE_ASPECT, CF_MUON_SCALE_RMS = 0, 1
 
 
 class cf_net_desc(ctypes.Structure):
@@ -71,7 +72,18 @@ class cf_optimizer(ctypes.Structure):
                 ("t", ctypes.c_int64)]
 
 
+class cf_newton_schulz_params(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class cf_muon_params(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("scale", ctypes.c_int32), ("ns", cf_newton_schulz_params)]
+
+
 _P = ctypes.c_void_p
+_PI64 = ctypes.POINTER(ctypes.c_int64)
 _SIG = {
     "cf_abi_version": ([], ctypes.c_int32),
     "cf_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -109,6 +121,12 @@ _SIG = {
                           ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "cf_groupnorm_bwd": ([ctypes.c_int, cf_dims, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int,
                           ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_newton_schulz_workspace_size": ([ctypes.c_int, ctypes.c_int32, _PI64, _PI64], ctypes.c_size_t),
+    "cf_newton_schulz": ([ctypes.POINTER(cf_newton_schulz_params), ctypes.c_int, ctypes.c_int32, _PI64, _PI64,
+                          ctypes.POINTER(_P), ctypes.POINTER(_P), _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_muon_workspace_size": ([ctypes.POINTER(cf_muon_params), ctypes.c_int32, _PI64, _PI64], ctypes.c_size_t),
+    "cf_muon": ([ctypes.POINTER(cf_muon_params), ctypes.c_int32, _PI64, _PI64, ctypes.POINTER(_P),
+                 ctypes.POINTER(_P), ctypes.POINTER(_P), _P, ctypes.c_size_t, _P], ctypes.c_int),
     "cf_net_param_count": ([ctypes.POINTER(cf_net_desc), ctypes.POINTER(ctypes.c_int64)], ctypes.c_int32),
     "cf_net_train_step_workspace_size": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32], ctypes.c_size_t),
     "cf_net_train_step": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.POINTER(_P),
@@ -452,6 +470,71 @@ def cf_adam_larc(hp, t, params, grads, m, v, lr_out=None, ws=None, stream=None):
     ws = _ws(int(lib().cf_adam_larc_workspace_size(k, n)), params[0].device, ws)
     check(lib().cf_adam_larc(ctypes.byref(hp), int(t), k, n, arr(params), arr(grads), arr(m), arr(v), _ptr(lr_out),
                              _ptr(ws), _wsbytes(ws), _stream(stream)))
+
+
+# ------------------------------------------------- Newton-Schulz and Muon
+def newton_schulz_params(steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7):
+    return cf_newton_schulz_params(int(steps), float(a), float(b), float(c), float(eps))
+
+
+def muon_params(lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=CF_MUON_SCALE_ASPECT, ns=None):
+    return cf_muon_params(float(lr), float(momentum), int(bool(nesterov)), float(weight_decay), int(scale),
+                          newton_schulz_params() if ns is None else ns)
+
+
+def _mat_sizes(mats):
+    """(rows, cols) arrays of weights taken as matrices: all but the last
+    dimension are rows (a conv weight [3,3,3,cin,cout] is [27 cin, cout])."""
+    k = len(mats)
+    rows, cols = (ctypes.c_int64 * k)(), (ctypes.c_int64 * k)()
+    for i, t in enumerate(mats):
+        if t.dim() < 2:
+            raise ValueError("matrix %d has fewer than two dimensions" % i)
+        cols[i] = t.shape[-1]
+        rows[i] = t.numel() // max(1, t.shape[-1])
+    return rows, cols
+
+
+def _pointers(ts):
+    return (_P * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
+    """The nearly orthogonal factor of each matrix (all fp32 or all bf16, two
+    dimensions or more, the last one the columns) -> list of tensors like
+    them."""
+    if not mats:
+        raise ValueError("no matrices")
+    dt = dtype_code(mats[0].dtype)
+    out = [torch.empty_like(t) for t in mats] if out is None else out
+    if len(out) != len(mats):
+        raise ValueError("%d outputs for %d matrices" % (len(out), len(mats)))
+    for i, (t, o) in enumerate(zip(mats, out)):
+        _packed("matrix %d" % i, t, mats[0].dtype)
+        _packed("output %d" % i, o, t.dtype, t.shape)
+    rows, cols = _mat_sizes(mats)
+    ws = _ws(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
+    check(lib().cf_newton_schulz(ctypes.byref(ns), dt, len(mats), rows, cols, _pointers(mats), _pointers(out),
+                                 _ptr(ws), _wsbytes(ws), _stream(stream)))
+    _record(stream, ws, *out)
+    return out
+
+
+def cf_muon(hp, params, grads, m, ws=None, stream=None):
+    """One Muon update of the fp32 weights `params` (two dimensions or more)
+    in place from `grads`, with momenta m (same shapes, updated in place)."""
+    k = len(params)
+    if not k or len(grads) != k or len(m) != k:
+        raise ValueError("params, grads and m must be lists of one length, not empty")
+    for i in range(k):
+        _packed("param %d" % i, params[i], torch.float32)
+        _packed("gradient %d" % i, grads[i], torch.float32, params[i].shape)
+        _packed("momentum %d" % i, m[i], torch.float32, params[i].shape)
+    rows, cols = _mat_sizes(params)
+    ws = _ws(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
+    check(lib().cf_muon(ctypes.byref(hp), k, rows, cols, _pointers(params), _pointers(grads), _pointers(m), _ptr(ws),
+                        _wsbytes(ws), _stream(stream)))
+    _record(stream, ws)
 
 
 # --------------------------------------------------------------- batch norm

@@ -871,6 +871,123 @@ cf_status cf_adam_larc(const cf_adam_larc_params* hp, int64_t t, int32_t ntensor
     return CF_OK;
 }
 
+// ------------------------------------------ Newton-Schulz products and Muon
+static cf_status check_ns(const cf_newton_schulz_params* ns, const char* fn)
+{
+    if (!ns) return fail(CF_ERR_INVALID, "%s: null parameters", fn);
+    if (ns->steps < 1 || ns->steps > 32) return fail(CF_ERR_INVALID, "%s: steps must be 1..32", fn);
+    if (!isfinite(ns->a) || !isfinite(ns->b) || !isfinite(ns->c))
+        return fail(CF_ERR_INVALID, "%s: coefficients must be finite", fn);
+    if (!(ns->eps > 0.f) || !(ns->eps < INFINITY)) return fail(CF_ERR_INVALID, "%s: eps must be positive and finite", fn);
+    return CF_OK;
+}
+
+static cf_status check_mats(int32_t nmat, const int64_t* rows, const int64_t* cols, const char* fn)
+{
+    if (nmat < 1 || nmat > CF_MAX_OPT_TENSORS)
+        return fail(CF_ERR_INVALID, "%s: nmat must be 1..%d (got %d)", fn, CF_MAX_OPT_TENSORS, nmat);
+    if (!rows || !cols) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
+    for (int i = 0; i < nmat; ++i) {
+        if (rows[i] < 1 || cols[i] < 1 || rows[i] > kMaxDim || cols[i] > kMaxDim)
+            return fail(CF_ERR_INVALID, "%s: rows or cols of matrix %d out of range", fn, i);
+        if ((rows[i] < cols[i] ? rows[i] : cols[i]) > 16384 || rows[i] * cols[i] > ((int64_t)1 << 36))
+            return fail(CF_ERR_UNSUPPORTED, "%s: matrix %d: the shorter side is at most 16384, the elements 2^36", fn, i);
+    }
+    return CF_OK;
+}
+
+static NsShapes ns_shapes(int32_t nmat, const int64_t* rows, const int64_t* cols)
+{
+    NsShapes l{};
+    l.count = nmat;
+    for (int i = 0; i < nmat; ++i) {
+        const bool tall = rows[i] > cols[i];
+        l.m[i] = (int)(tall ? cols[i] : rows[i]);
+        l.n[i] = (int)(tall ? rows[i] : cols[i]);
+        if (tall) l.tall |= 1u << i;
+    }
+    return l;
+}
+
+static NsCoef ns_coef(const cf_newton_schulz_params& p) { return NsCoef{p.steps, p.a, p.b, p.c, p.eps}; }
+
+size_t cf_newton_schulz_workspace_size(cf_dtype dtype, int32_t nmat, const int64_t* rows, const int64_t* cols)
+{
+    const char* fn = "cf_newton_schulz_workspace_size";
+    if (check_dtype(dtype) != CF_OK || check_mats(nmat, rows, cols, fn) != CF_OK) return 0;
+    return ns_ws_bytes(ns_shapes(nmat, rows, cols));
+}
+
+cf_status cf_newton_schulz(const cf_newton_schulz_params* ns, cf_dtype dtype, int32_t nmat, const int64_t* rows,
+                           const int64_t* cols, const void* const* x, void* const* out, void* ws, size_t ws_bytes,
+                           hipStream_t stream)
+{
+    const char* fn = "cf_newton_schulz";
+    cf_status st = check_dtype(dtype);
+    if (st != CF_OK) return st;
+    if ((st = check_ns(ns, fn)) != CF_OK || (st = check_mats(nmat, rows, cols, fn)) != CF_OK) return st;
+    if (!x || !out) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
+    for (int i = 0; i < nmat; ++i)
+        if (!x[i] || !out[i] || !al16(x[i]) || !al16(out[i]))
+            return fail(CF_ERR_INVALID, "%s: matrix %d has a null or misaligned pointer", fn, i);
+    const NsShapes l = ns_shapes(nmat, rows, cols);
+    const size_t need = ns_ws_bytes(l);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    CF_TRY_HIP(dtype == CF_F32 ? launch_newton_schulz<float>(l, ns_coef(*ns), x, out, ws, stream)
+                               : launch_newton_schulz<uint16_t>(l, ns_coef(*ns), x, out, ws, stream),
+               "newton-schulz");
+    return CF_OK;
+}
+
+static cf_status check_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols,
+                            const char* fn)
+{
+    if (!hp) return fail(CF_ERR_INVALID, "%s: null parameters", fn);
+    cf_status st = check_ns(&hp->ns, fn);
+    if (st != CF_OK) return st;
+    if (!isfinite(hp->lr)) return fail(CF_ERR_INVALID, "%s: lr must be finite", fn);
+    if (!(hp->momentum >= 0.f && hp->momentum < 1.f)) return fail(CF_ERR_INVALID, "%s: momentum must be in [0, 1)", fn);
+    if (!(hp->weight_decay >= 0.f && hp->weight_decay < INFINITY))
+        return fail(CF_ERR_INVALID, "%s: weight_decay must be >= 0 and finite", fn);
+    if (hp->scale != CF_MUON_SCALE_ASPECT && hp->scale != CF_MUON_SCALE_RMS)
+        return fail(CF_ERR_INVALID, "%s: unknown scale %d", fn, hp->scale);
+    return check_mats(nmat, rows, cols, fn);
+}
+
+size_t cf_muon_workspace_size(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols)
+{
+    if (check_muon(hp, nmat, rows, cols, "cf_muon_workspace_size") != CF_OK) return 0;
+    return muon_ws_bytes(ns_shapes(nmat, rows, cols), hp->nesterov != 0);
+}
+
+cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols, float* const* w,
+                  const float* const* g, float* const* m, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const char* fn = "cf_muon";
+    cf_status st = check_muon(hp, nmat, rows, cols, fn);
+    if (st != CF_OK) return st;
+    if (!w || !g || !m) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
+    for (int i = 0; i < nmat; ++i)
+        if (!w[i] || !g[i] || !m[i] || !al16(w[i]) || !al16(g[i]) || !al16(m[i]))
+            return fail(CF_ERR_INVALID, "%s: matrix %d has a null or misaligned pointer", fn, i);
+    const NsShapes l = ns_shapes(nmat, rows, cols);
+    const size_t need = muon_ws_bytes(l, hp->nesterov != 0);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    MuonArgs a{};
+    a.momentum = hp->momentum;
+    a.nesterov = hp->nesterov != 0;
+    a.keep = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
+    for (int i = 0; i < nmat; ++i) {
+        const double r = (double)rows[i], c = (double)cols[i];
+        const double f = hp->scale == CF_MUON_SCALE_ASPECT ? sqrt(c > r ? c / r : 1.0) : 0.2 * sqrt(c > r ? c : r);
+        a.rate[i] = (float)((double)hp->lr * f);
+    }
+    CF_TRY_HIP(launch_muon(l, ns_coef(hp->ns), a, w, g, m, ws, stream), "muon");
+    return CF_OK;
+}
+
 // ------------------------------------------------------------- batch norm
 static cf_status check_bn(cf_dtype dtype, const cf_dims& x, const char* fn)
 {

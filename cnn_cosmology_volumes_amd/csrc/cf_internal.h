@@ -328,4 +328,30 @@ hipError_t launch_gn_bwd(const T* X, const T* dY, const float* gamma, const floa
                          const float* rstd, cf_act act, float slope, T* dX, float* dgamma, float* dbeta,
                          const cf_dims& x, int groups, void* ws, hipStream_t s);
 
+// Newton-Schulz orthogonalisation and Muon (k_muon.hip) of a list of row-major
+// matrices; m and n are a matrix's short and long side, bit i of `tall` says
+// that matrix i has more rows than columns.
+struct NsShapes {
+    int count;
+    int m[CF_MAX_OPT_TENSORS], n[CF_MAX_OPT_TENSORS];
+    uint32_t tall;
+};
+struct NsCoef {
+    int steps;
+    float a, b, c, eps;
+};
+struct MuonArgs {
+    float momentum;
+    bool nesterov;
+    float keep;                         // 1 - lr weight_decay
+    float rate[CF_MAX_OPT_TENSORS];     // lr times the matrix's scale
+};
+size_t ns_ws_bytes(const NsShapes& l);
+size_t muon_ws_bytes(const NsShapes& l, bool nesterov);
+template <typename T>
+hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* const* x, void* const* out, void* ws,
+                                hipStream_t s);
+hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, float* const* w, const float* const* g,
+                       float* const* m, void* ws, hipStream_t s);
+
 }  // namespace cf

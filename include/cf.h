@@ -308,6 +308,64 @@ cf_status cf_adam_larc(const cf_adam_larc_params* hp, int64_t t, int32_t ntensor
                        float* const* w, const float* const* g, float* const* m, float* const* v,
                        float* lr_out, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------- Newton-Schulz products and Muon */
+
+/* Coefficients of the quintic Newton-Schulz iteration; 1 <= steps <= 32,
+ * finite a, b, c, finite eps > 0.  (3.4445, -4.7750, 2.0315), 5 steps and eps
+ * 1e-7 bring every singular value from about 0.005 to 1 of the normalised
+ * matrix near 1. */
+typedef struct {
+    int32_t steps;
+    float a, b, c;
+    float eps;
+} cf_newton_schulz_params;
+
+/* Workspace bytes for cf_newton_schulz over matrices of these sizes (HOST
+ * arrays; dtype as there).  Returns 0 for invalid arguments. */
+size_t cf_newton_schulz_workspace_size(cf_dtype dtype, int32_t nmat, const int64_t* rows, const int64_t* cols);
+
+/* The nearly orthogonal factor of each of nmat (1..CF_MAX_OPT_TENSORS)
+ * row-major matrices x[i] [rows[i]][cols[i]] (dtype), any sizes from 1 x 1:
+ *   X = x / (|x|_F + eps)
+ *   steps times, with A = X X^T:  X <- a X + (b A + c A A) X
+ *   out[i] = X (dtype)
+ * (rows > cols: the same on the transpose).  rows, cols, x and out are HOST
+ * arrays; x and out entries are DEVICE pointers and must not overlap.  The
+ * shorter side must be at most 16384 and a matrix at most 2^36 elements (else
+ * CF_ERR_UNSUPPORTED).  Products of fp32 accuracy or better throughout, also
+ * for CF_BF16, whose results are rounded once.  Sums are added in a fixed
+ * order: results are reproducible bit for bit. */
+cf_status cf_newton_schulz(const cf_newton_schulz_params* ns, cf_dtype dtype, int32_t nmat, const int64_t* rows,
+                           const int64_t* cols, const void* const* x, void* const* out, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* How cf_muon scales a matrix's orthogonalised update. */
+typedef enum {
+    CF_MUON_SCALE_ASPECT = 0,   /* sqrt(max(1, cols / rows)): weights are [in][out] */
+    CF_MUON_SCALE_RMS = 1       /* 0.2 sqrt(max(rows, cols)): the rms of an Adam update */
+} cf_muon_scale;
+
+typedef struct {
+    float lr;                   /* finite */
+    float momentum;             /* mu in [0, 1) */
+    int32_t nesterov;           /* != 0: the update direction is g + mu m */
+    float weight_decay;         /* >= 0 */
+    int32_t scale;              /* cf_muon_scale */
+    cf_newton_schulz_params ns;
+} cf_muon_params;
+
+/* Workspace bytes for cf_muon. */
+size_t cf_muon_workspace_size(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols);
+
+/* One Muon update of nmat fp32 weight matrices in place.  Conv weights
+ * [3,3,3,cin,cout] are matrices [27 cin][cout], dense weights [in][out].
+ *   m <- mu m + g;  u = g + mu m (nesterov) or m
+ *   w <- w (1 - lr weight_decay) - lr scale(rows, cols) NewtonSchulz(u)
+ * rows, cols, w, g, m are HOST arrays; w, g, m entries are DEVICE pointers
+ * (m starts at zero).  Sizes as for cf_newton_schulz. */
+cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols, float* const* w,
+                  const float* const* g, float* const* m, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------ batch norm */
 
 /* Workspace bytes for cf_batchnorm_fwd / cf_batchnorm_bwd on x. */

@@ -464,6 +464,30 @@ def adam_larc_step(w, g, m, v, t, lr, beta1, beta2, eps, trust):
     return w - lr_l * u, m, v, lr_l
 
 
+# ------------------------------------------------------- Newton-Schulz, Muon
+def newton_schulz(x, steps, a, b, c, eps):
+    """X = x / (|x|_F + eps), then `steps` times with A = X X^T (the product
+    of the shorter side): X <- a X + (b A + c A A) X."""
+    x = _f64(x)
+    t = x.T if x.shape[0] > x.shape[1] else x
+    t = t / (np.sqrt(np.sum(t * t)) + eps)
+    for _ in range(steps):
+        g = t @ t.T
+        t = a * t + (b * g + c * (g @ g)) @ t
+    return t.T if x.shape[0] > x.shape[1] else t
+
+
+def muon_step(w, g, m, lr, momentum, nesterov, weight_decay, scale, ns):
+    """One Muon update of a matrix [rows, cols]; scale "aspect" or "rms", ns
+    the arguments of newton_schulz after x.  Returns (w, m)."""
+    w, g, m = _f64(w), _f64(g), _f64(m)
+    m = momentum * m + g
+    u = g + momentum * m if nesterov else m
+    rows, cols = w.shape
+    f = np.sqrt(max(1.0, cols / rows)) if scale == "aspect" else 0.2 * np.sqrt(max(rows, cols))
+    return w * (1.0 - lr * weight_decay) - lr * f * newton_schulz(u, *ns), m
+
+
 # --------------------------------------------------------------- batch norm
 def batchnorm_fwd(x, gamma, beta, eps):
     """Training-mode batch normalisation of NDHWC x over (N, D, H, W) per
