@@ -351,6 +351,15 @@ size_t muon_ws_bytes(const NsShapes& l, bool nesterov);
 template <typename T>
 hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* const* x, void* const* out, void* ws,
                                 hipStream_t s);
+// One large matrix by split fp16 products (k_ns_split.hip), where the
+// coefficients allow it; out, or w <- w keep - rate o.
+bool ns_split_size(int m, int n);
+bool ns_split_coef(const NsCoef& c);
+size_t ns_split_ws_bytes(int m, int n);
+template <typename T>
+hipError_t launch_ns_split(int m, int n, bool tall, const NsCoef& c, const T* x, T* out, void* ws, hipStream_t s);
+hipError_t launch_ns_split_apply(int m, int n, bool tall, const NsCoef& c, const float* x, float* w, float keep,
+                                 float rate, void* ws, hipStream_t s);
 hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, float* const* w, const float* const* g,
                        float* const* m, void* ws, hipStream_t s);
 

@@ -585,19 +585,69 @@ hipError_t ns_final(const NsShapes& l, const NsPlan& p, const void* const* u, in
 
 }  // namespace
 
-size_t ns_ws_bytes(const NsShapes& l) { return up256b((size_t)ns_plan(l).doubles * sizeof(double)); }
+namespace {
+
+// The matrices of a list that take the fp64 launches together, and those that
+// take split products one after another.
+struct NsParts {
+    NsShapes f64;
+    int f64_at[CF_MAX_OPT_TENSORS];      // their places in the list
+    int split[CF_MAX_OPT_TENSORS], splits;
+};
+NsParts ns_parts(const NsShapes& l, bool allow_split)
+{
+    NsParts p{};
+    for (int i = 0; i < l.count; ++i) {
+        if (allow_split && ns_split_size(l.m[i], l.n[i])) {
+            p.split[p.splits++] = i;
+            continue;
+        }
+        const int k = p.f64.count++;
+        p.f64.m[k] = l.m[i];
+        p.f64.n[k] = l.n[i];
+        p.f64.tall |= (l.tall >> i & 1u) << k;
+        p.f64_at[k] = i;
+    }
+    return p;
+}
+
+size_t ns_f64_ws_bytes(const NsShapes& l) { return l.count ? up256b((size_t)ns_plan(l).doubles * sizeof(double)) : 0; }
+
+}  // namespace
+
+// The sizes alone fix the workspace: the larger of what any coefficients need.
+size_t ns_ws_bytes(const NsShapes& l)
+{
+    size_t b = ns_f64_ws_bytes(l);
+    const NsParts p = ns_parts(l, true);
+    b = std::max(b, ns_f64_ws_bytes(p.f64));
+    for (int i = 0; i < p.splits; ++i) b = std::max(b, ns_split_ws_bytes(l.m[p.split[i]], l.n[p.split[i]]));
+    return b;
+}
 
 template <typename T>
 hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* const* x, void* const* out, void* ws,
                                 hipStream_t s)
 {
-    const NsPlan p = ns_plan(l);
-    int q = 0;
-    hipError_t e = ns_iterate<T>(l, p, x, c, (double*)ws, &q, s);
-    if (e != hipSuccess) return e;
+    const NsParts p = ns_parts(l, ns_split_coef(c));
+    hipError_t e;
+    for (int i = 0; i < p.splits; ++i) {
+        const int k = p.split[i];
+        if ((e = launch_ns_split<T>(l.m[k], l.n[k], l.tall >> k & 1, c, (const T*)x[k], (T*)out[k], ws, s)) !=
+            hipSuccess)
+            return e;
+    }
+    if (!p.f64.count) return hipSuccess;
+    const void* u[CF_MAX_OPT_TENSORS];
     StoreArgs f{};
-    for (int i = 0; i < l.count; ++i) f.out[i] = out[i];
-    return ns_final<T>(l, p, x, q, f, (const double*)ws, s);
+    for (int i = 0; i < p.f64.count; ++i) {
+        u[i] = x[p.f64_at[i]];
+        f.out[i] = out[p.f64_at[i]];
+    }
+    const NsPlan pl = ns_plan(p.f64);
+    int q = 0;
+    if ((e = ns_iterate<T>(p.f64, pl, u, c, (double*)ws, &q, s)) != hipSuccess) return e;
+    return ns_final<T>(p.f64, pl, u, q, f, (const double*)ws, s);
 }
 
 size_t muon_ws_bytes(const NsShapes& l, bool nesterov)
@@ -612,8 +662,7 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
                        float* const* m, void* ws, hipStream_t s)
 {
     MomentumArgs a{};
-    ApplyArgs f{};
-    const void* u[CF_MAX_OPT_TENSORS];
+    const float* u[CF_MAX_OPT_TENSORS];
     char* at = (char*)ws + ns_ws_bytes(l);
     a.count = l.count;
     for (int i = 0; i < l.count; ++i) {
@@ -623,22 +672,35 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
         u[i] = m[i];
         if (h.nesterov) {
             a.u[i] = (float*)at;
-            u[i] = at;
+            u[i] = a.u[i];
             at += up256b((size_t)a.n[i] * sizeof(float));
         }
         a.start[i + 1] = a.start[i] + (int)((a.n[i] + MU_CHUNK - 1) / MU_CHUNK);
-        f.w[i] = w[i];
-        f.rate[i] = h.rate[i];
     }
-    f.keep = h.keep;
     hipLaunchKernelGGL(muon_momentum_kernel, dim3((unsigned)a.start[l.count]), dim3(NS_T), 0, s, a, h.momentum,
                        (int)h.nesterov);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const NsPlan p = ns_plan(l);
+    const NsParts p = ns_parts(l, ns_split_coef(c));
+    for (int i = 0; i < p.splits; ++i) {
+        const int k = p.split[i];
+        if ((e = launch_ns_split_apply(l.m[k], l.n[k], l.tall >> k & 1, c, u[k], w[k], h.keep, h.rate[k], ws, s)) !=
+            hipSuccess)
+            return e;
+    }
+    if (!p.f64.count) return hipSuccess;
+    const void* v[CF_MAX_OPT_TENSORS];
+    ApplyArgs f{};
+    f.keep = h.keep;
+    for (int i = 0; i < p.f64.count; ++i) {
+        v[i] = u[p.f64_at[i]];
+        f.w[i] = w[p.f64_at[i]];
+        f.rate[i] = h.rate[p.f64_at[i]];
+    }
+    const NsPlan pl = ns_plan(p.f64);
     int q = 0;
-    if ((e = ns_iterate<float>(l, p, u, c, (double*)ws, &q, s)) != hipSuccess) return e;
-    return ns_final<float>(l, p, u, q, f, (const double*)ws, s);
+    if ((e = ns_iterate<float>(p.f64, pl, v, c, (double*)ws, &q, s)) != hipSuccess) return e;
+    return ns_final<float>(p.f64, pl, v, q, f, (const double*)ws, s);
 }
 
 template hipError_t launch_newton_schulz<float>(const NsShapes&, const NsCoef&, const void* const*, void* const*,
