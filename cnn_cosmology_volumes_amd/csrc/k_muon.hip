@@ -598,7 +598,7 @@ NsParts ns_parts(const NsShapes& l, bool allow_split)
 {
     NsParts p{};
     for (int i = 0; i < l.count; ++i) {
-        if (allow_split && ns_split_size(l.m[i], l.n[i])) {
+        if (allow_split && ns_split_size(l.m[i])) {
             p.split[p.splits++] = i;
             continue;
         }

@@ -24,13 +24,19 @@
 // the end are readable and hold anything: they reach only results that are not
 // written.
 //
-// Work split: a launch has one block per CU, and the (tile, piece of the
-// reduction) units in tile order are cut into equal ranges, one for each block,
-// since the number of tiles seldom fills the chip evenly (136 tiles of a
-// symmetric 4096 x 4096 product for 256 CUs).  A block that holds all of a
-// tile's reduction writes its result; others write fp32 sums that a joining
-// launch adds in the order of the blocks.  No atomics and no waiting between
-// blocks: results are reproducible bit for bit.
+// Work split: tiles of 64 x 64, a block each, where they are few (the block's
+// waves share the reduction), else of 128 or 256 (sp_tile gives the rule).
+// There a launch has one block per CU, and the (tile, piece of the reduction)
+// units in tile order are cut into equal ranges, one for each block, since the
+// number of tiles seldom fills the chip evenly (136 tiles of a symmetric
+// 4096 x 4096 product for 256 CUs).  A block that holds all of a tile's
+// reduction writes its result; others write fp32 sums that a joining launch
+// adds in the order of the blocks.  No atomics and no waiting between blocks:
+// results are reproducible bit for bit.
+//
+// What bounds it: 4096 x 4096 takes 3943 us, of it 339 for each P X (1.21
+// PFLOP/s of fp16 products; a library fp16 product of that size reaches 1.26)
+// with the matrix cores busy 77% of the cycles at 1.46 GHz: the chip's power.
 #include "cf_internal.h"
 
 #include <algorithm>
@@ -42,8 +48,7 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int SP_TILE = 256;      // edge of an output tile
-constexpr int SP_T = 512;         // threads: 2 x 4 waves of 128 x 64
+constexpr int SP_TILE = 256;      // largest edge of an output tile
 constexpr int SP_K = 32;          // reduction values of a piece
 constexpr int SP_GRID = 256;      // blocks of a product, one per CU
 constexpr int SP_SB = 36;         // LDS row stride of a 32 x 32 block, floats
@@ -65,10 +70,10 @@ struct SpProduct {
     const uint16_t* p;      // [rows of C] and
     const uint16_t* r;      // [columns of C] operands, pieces(k) lines a row
     int kb;                 // pieces of the reduction
-    int mt, nt;             // tiles
+    int tile, mt, nt;       // edge of a tile, tiles
     int sym;
-    int last;               // the reduction of tile row i ends with pieces 8 i .. 8 i + 7: a I is in P, and
-                            // the sum of the small terms is rounded at its own size
+    int last;               // a tile's reduction ends with its own rows' pieces: a I is in P, and the sum of
+                            // the small terms is rounded at its own size
     int m, n;
     float f, g, diag;
     const uint16_t* s;
@@ -199,122 +204,347 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
 }
 
 // ------------------------------------------------------------------ product
-// A stage of one piece: 256 lines of p, then 256 of r.  The 16-byte chunk c of
-// row r's line lies at slot c ^ (r / 2 & 7): sixteen rows read at one chunk
-// fall on all banks.
-constexpr int SP_STAGE = 2 * SP_TILE * 8;      // 16-byte chunks
+// Two shapes of a block:
+//   256: 8 waves of 128 x 64, two stages of a piece in LDS (128 KB);
+//   128: 4 waves of 64 x 64, four stages (128 KB): a piece takes a quarter of
+//        the time there, less than a load's latency.
+template <int TILE> struct SpShape {
+    static constexpr int WAVES = TILE == 256 ? 8 : 4;
+    static constexpr int WC = WAVES / 2;            // waves side by side
+    static constexpr int MI = TILE / 64;            // a wave's 32 x 32 blocks: rows,
+    static constexpr int NJ = TILE / WC / 32;       // columns
+    static constexpr int STAGES = TILE == 256 ? 2 : 4;
+    static constexpr int CHUNKS = 2 * TILE * 8;     // 16-byte chunks of a stage
+};
 
-__device__ __forceinline__ void sp_load(uint4* stage, const uint16_t* p, const uint16_t* r, int64_t ld, int piece)
+// Raw 32-bit words from p on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t sp_rsrc(const void* p)
 {
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int q = wave * 4 + i % 4;      // eight rows of the panel
-        const int row = q * 8 + lane / 8, chunk = (lane & 7) ^ ((row >> 1) & 7);
-        const uint16_t* src = (i < 4 ? p : r) + row * ld + (int64_t)piece * 64 + chunk * 8;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                         (__attribute__((address_space(3))) void*)(stage + (i / 4) * (SP_TILE * 8) + q * 64),
-                                         16, 0, 0);
-    }
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0xffffffffu, 0x00020000);
 }
 
-__device__ __forceinline__ void sp_multiply(const uint4* stage, f32x16 (&acc)[4][2])
+// A stage: TILE lines of p, then TILE of r.  The 16-byte chunk c of row r's
+// line lies at slot c ^ (r / 2 & 7): sixteen rows read at one chunk fall on all
+// banks.
+//
+// Starts the loads of a piece; a wave's instruction takes eight rows' lines.
+// src: this wave's first row of p and of r at that piece, off: the lane's
+// offset in bytes from there, for an even and an odd group of eight rows.
+template <int TILE>
+__device__ __forceinline__ void sp_load(uint4* stage, const char* const (&src)[2], const uint32_t (&off)[2], int64_t ld)
 {
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                sp_rsrc(src[o]), (__attribute__((address_space(3))) void*)(stage + o * (TILE * 8) + (wave * 4 + i) * 64),
+                16, off[i & 1], i * 8 * (uint32_t)ld, 0, 0);
+}
+constexpr int SP_LOADS = 8;      // instructions of sp_load
+
+// One half (16 values) of a piece for a wave's part of the tile.
+template <int TILE> struct SpFrag {
+    f16x8 ah[SpShape<TILE>::MI], al[SpShape<TILE>::MI], bh[SpShape<TILE>::NJ], bl[SpShape<TILE>::NJ];
+};
+template <int TILE> __device__ __forceinline__ void sp_read(SpFrag<TILE>& f, const uint4* stage, int half)
+{
+    using S = SpShape<TILE>;
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int wi = (wave >> 2) * 128, wj = (wave & 3) * 64;
+    const int wi = wave / S::WC * S::MI * 32, wj = wave % S::WC * S::NJ * 32;
     const int swz = (lane >> 1) & 7;
+    const int ch = (half * 2 + lane / 32) ^ swz, cl = (4 + half * 2 + lane / 32) ^ swz;
     const f16x8* A = reinterpret_cast<const f16x8*>(stage) + (wi + lane % 32) * 8;
-    const f16x8* B = reinterpret_cast<const f16x8*>(stage) + (SP_TILE + wj + lane % 32) * 8;
+    const f16x8* B = reinterpret_cast<const f16x8*>(stage) + (TILE + wj + lane % 32) * 8;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int ch = (s * 2 + lane / 32) ^ swz, cl = (4 + s * 2 + lane / 32) ^ swz;
-        f16x8 ah[4], al[4], bh[2], bl[2];
+    for (int j = 0; j < S::NJ; ++j) {
+        f.bh[j] = B[j * 256 + ch];
+        f.bl[j] = B[j * 256 + cl];
+    }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bh[j] = B[j * 256 + ch];
-            bl[j] = B[j * 256 + cl];
-        }
+    for (int i = 0; i < S::MI; ++i) {
+        f.ah[i] = A[i * 256 + ch];
+        f.al[i] = A[i * 256 + cl];
+    }
+}
+template <int TILE>
+__device__ __forceinline__ void sp_multiply(const SpFrag<TILE>& f, f32x16 (&acc)[SpShape<TILE>::MI][SpShape<TILE>::NJ])
+{
+    using S = SpShape<TILE>;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ah[i] = A[i * 256 + ch];
-            al[i] = A[i * 256 + cl];
-        }
+    for (int i = 0; i < S::MI; ++i)
 #pragma unroll
         for (int x = 0; x < 3; ++x)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < S::NJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x == 2 ? f.al[i] : f.ah[i], x == 1 ? f.bl[j] : f.bh[j],
+                                                                  acc[i][j], 0, 0, 0);
+}
+// The LDS reads of the next half, and the loads of a piece, among the matrix
+// instructions of this one.
+template <int TILE, bool LOADS> __device__ __forceinline__ void sp_interleave()
+{
+    using S = SpShape<TILE>;
+    constexpr int reads = 2 * (S::MI + S::NJ);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x == 2 ? al[i] : ah[i], x == 1 ? bl[j] : bh[j],
-                                                                      acc[i][j], 0, 0, 0);
+    for (int i = 0; i < reads; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (LOADS && i < SP_LOADS) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(0x008, 3 * S::MI * S::NJ - reads, 0);
 }
 
-// Barrier after which every wave's loads into LDS have landed.
-__device__ __forceinline__ void sp_landed()
+// Barrier after which every wave's loads into LDS have landed but for the
+// newest AHEAD pieces', and its LDS reads are done.
+template <int AHEAD> __device__ __forceinline__ void sp_landed()
 {
-    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt 0
-    __syncthreads();
+    asm volatile("" ::: "memory");
+    constexpr int n = AHEAD * SP_LOADS;                                      // vmcnt: bits 0-3 and 14-15;
+    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);          // lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
-template <int MODE, typename T, typename F>
-__global__ __launch_bounds__(SP_T, 2) void sp_product_kernel(SpProduct q, SpFinal<T, F> fin)
+template <int TILE, int MODE, typename T, typename F>
+__global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(SpProduct q, SpFinal<T, F> fin)
 {
-    __shared__ uint4 s0[SP_STAGE];
-    __shared__ uint4 s1[SP_STAGE];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    using S = SpShape<TILE>;
+    // (arrays of their own: loads into one do not hold up reads of another)
+    __shared__ uint4 s0[S::CHUNKS];
+    __shared__ uint4 s1[S::CHUNKS];
+    __shared__ uint4 s2[S::STAGES > 2 ? S::CHUNKS : 1];
+    __shared__ uint4 s3[S::STAGES > 2 ? S::CHUNKS : 1];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int b = (int)xcd_remap(blockIdx.x, (uint32_t)q.grid);
-    const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)q.kb * 64;
+    const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)q.kb * 128;      // bytes of a row
+    uint32_t off[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        off[i] = (uint32_t)(lane / 8 * ld) + ((uint32_t)(lane & 7) ^ (uint32_t)(i * 4 + lane / 16)) * 16;
     int64_t u = sp_first(q, b);
     for (int seg = 0; u < u1; seg = 1) {
         const int t = (int)(u / q.kb), k0 = (int)(u - (int64_t)t * q.kb);
         const int len = (int)min((int64_t)(q.kb - k0), u1 - u);
         int ti, tj;
         sp_tile_at(q, t, ti, tj);
-        const uint16_t* p = q.p + (int64_t)ti * SP_TILE * ld;
-        const uint16_t* r = q.r + (int64_t)tj * SP_TILE * ld;
-        int piece = k0 + (q.last ? (ti + 1) * (SP_TILE / SP_K) : 0);
-        piece %= q.kb;
-        f32x16 acc[4][2] = {};
-        auto next = [&] { piece = piece + 1 == q.kb ? 0 : piece + 1; };
-        sp_load(s0, p, r, ld, piece);
-        for (int i = 0; i < len; i += 2) {
-            sp_landed();
-            next();
-            if (i + 1 < len) sp_load(s1, p, r, ld, piece);
-            sp_multiply(s0, acc);
-            if (i + 1 < len) {
-                sp_landed();
-                next();
-                if (i + 2 < len) sp_load(s0, p, r, ld, piece);
-                sp_multiply(s1, acc);
+        int piece = (k0 + (q.last ? (ti + 1) * (TILE / SP_K) : 0)) % q.kb;
+        const char* src[2] = {(const char*)q.p + ((int64_t)ti * TILE + wave * 32) * ld + (int64_t)piece * 128,
+                              (const char*)q.r + ((int64_t)tj * TILE + wave * 32) * ld + (int64_t)piece * 128};
+        f32x16 acc[S::MI][S::NJ] = {};
+        int left = len;      // pieces whose loads have not begun
+        // (past the last piece it is loaded again and not used: the waits count on a load every time)
+        auto load = [&](uint4* stage) {
+            sp_load<TILE>(stage, src, off, ld);
+            const bool wrap = piece + 1 == q.kb, more = --left > 0;
+            const int64_t step = more ? 128 - (wrap ? ld : 0) : 0;
+            piece = wrap ? 0 : piece + 1;
+            src[0] += step;
+            src[1] += step;
+        };
+        // The reads of a half are in flight while the half before it is multiplied, across the barrier too.
+        SpFrag<TILE> f0, f1;
+        load(s0);
+        load(s1);
+        if (S::STAGES > 2) {
+            load(s2);
+            load(s3);
+        }
+        sp_landed<S::STAGES - 1>();
+        sp_read<TILE>(f0, s0, 0);
+        auto piece_of = [&](uint4* cur, uint4* nxt) {
+            sp_read<TILE>(f1, cur, 1);
+            sp_multiply<TILE>(f0, acc);
+            sp_interleave<TILE, false>();
+            sp_landed<S::STAGES - 2>();
+            load(cur);
+            sp_read<TILE>(f0, nxt, 0);      // (past the last piece: read and not used)
+            sp_multiply<TILE>(f1, acc);
+            sp_interleave<TILE, true>();
+        };
+        for (int i = 0; i < len / S::STAGES; ++i) {
+            piece_of(s0, s1);
+            if constexpr (S::STAGES == 2) {
+                piece_of(s1, s0);
+            } else {
+                piece_of(s1, s2);
+                piece_of(s2, s3);
+                piece_of(s3, s0);
             }
         }
-        const int wi = (wave >> 2) * 4, wj = (wave & 3) * 2;
-        __syncthreads();
+        if (const int rest = len % S::STAGES) {
+            piece_of(s0, s1);
+            if (rest > 1) piece_of(s1, s2);
+            if (rest > 2) piece_of(s2, s3);
+        }
+        constexpr int E = TILE / 32;
+        const int wi = wave / S::WC * S::MI, wj = wave % S::WC * S::NJ;
+        sp_landed<0>();
         if (len == q.kb) {
             float* sh = reinterpret_cast<float*>(s0) + wave * (32 * SP_SB);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    sp_block<MODE>(acc[i][j], sh, q, fin, ti * 8 + wi + i, tj * 8 + wj + j);
+                for (int j = 0; j < S::NJ; ++j)
+                    sp_block<MODE>(acc[i][j], sh, q, fin, ti * E + wi + i, tj * E + wj + j);
             __syncthreads();
         } else {
             // [block of 32 x 32][quarter of a lane's registers][lane]
-            float4* out = reinterpret_cast<float4*>(q.part + ((int64_t)b * 2 + seg) * SP_PART);
+            float4* out = reinterpret_cast<float4*>(q.part + ((int64_t)b * 2 + seg) * (TILE * TILE));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < S::NJ; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        out[(((wi + i) * 8 + wj + j) * 4 + v) * 64 + lane] =
+                        out[(((wi + i) * E + wj + j) * 4 + v) * 64 + lane] =
                             make_float4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
                                         acc[i][j][4 * v + 3]);
         }
         u += len;
     }
+}
+
+// A block takes a 64 x 64 tile with its whole reduction: the four waves each
+// take every fourth piece for all of the tile, from stages of their own, so
+// that no wave waits for another until the end, when the four sums are added in
+// order and each wave writes a quarter of the tile.
+constexpr int SP_SMALL = 64;
+constexpr int SP_LINES = 2 * SP_SMALL * 8;      // 16-byte chunks of a wave's stage
+
+__device__ __forceinline__ void sp_small_load(uint4* stage, const char* const (&src)[2], const uint32_t (&off)[2],
+                                              int64_t ld)
+{
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int i = 0; i < SP_SMALL / 8; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                sp_rsrc(src[o]), (__attribute__((address_space(3))) void*)(stage + o * (SP_SMALL * 8) + i * 64), 16,
+                off[i & 1], i * 8 * (uint32_t)ld, 0, 0);
+}
+
+struct SpPiece {
+    f16x8 ah[2][2], al[2][2], bh[2][2], bl[2][2];      // [half][32 rows or columns]
+};
+__device__ __forceinline__ void sp_small_read(SpPiece& f, const uint4* stage)
+{
+    const int lane = (int)threadIdx.x & 63, swz = (lane >> 1) & 7;
+    const f16x8* A = reinterpret_cast<const f16x8*>(stage) + (lane % 32) * 8;
+    const f16x8* B = A + SP_SMALL * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int ch = (h * 2 + lane / 32) ^ swz, cl = (4 + h * 2 + lane / 32) ^ swz;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f.ah[h][i] = A[i * 256 + ch];
+            f.al[h][i] = A[i * 256 + cl];
+            f.bh[h][i] = B[i * 256 + ch];
+            f.bl[h][i] = B[i * 256 + cl];
+        }
+    }
+}
+__device__ __forceinline__ void sp_small_multiply(const SpPiece& f, f32x16 (&acc)[2][2])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x == 2 ? f.al[h][i] : f.ah[h][i],
+                                                                      x == 1 ? f.bl[h][j] : f.bh[h][j], acc[i][j], 0, 0, 0);
+}
+
+template <int MODE, typename T, typename F>
+__global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F> fin)
+{
+    __shared__ uint4 sa[4 * SP_LINES];
+    __shared__ uint4 sb[4 * SP_LINES];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    int ti, tj;
+    sp_tile_at(q, (int)xcd_remap(blockIdx.x, gridDim.x), ti, tj);
+    const int64_t ld = (int64_t)q.kb * 128;
+    uint32_t off[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        off[i] = (uint32_t)(lane / 8 * ld) + ((uint32_t)(lane & 7) ^ (uint32_t)(i * 4 + lane / 16)) * 16;
+    f32x16 acc[2][2] = {};
+    if (wave < q.kb) {
+        uint4* const A = sa + wave * SP_LINES;
+        uint4* const B = sb + wave * SP_LINES;
+        const int count = (q.kb - wave + 3) / 4;
+        const char* src[2] = {(const char*)q.p + (int64_t)ti * SP_SMALL * ld + wave * 128,
+                              (const char*)q.r + (int64_t)tj * SP_SMALL * ld + wave * 128};
+        int left = count;
+        // (past the last piece it is loaded again and not used: the waits count on a load every time)
+        auto load = [&](uint4* stage) {
+            sp_small_load(stage, src, off, ld);
+            if (--left > 0) {
+                src[0] += 512;
+                src[1] += 512;
+            }
+        };
+        // the older of the two pieces under way has landed
+        auto landed = [] {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x4f70);      // vmcnt 16
+            asm volatile("" ::: "memory");
+        };
+        // this wave's LDS reads are done
+        auto have_read = [] {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt 0
+            asm volatile("" ::: "memory");
+        };
+        SpPiece f0, f1;
+        load(A);
+        load(B);
+        landed();
+        sp_small_read(f0, A);
+        auto piece_of = [&](const SpPiece& now, SpPiece& then, uint4* cur, uint4* nxt) {
+            have_read();
+            load(cur);
+            landed();
+            sp_small_read(then, nxt);
+            sp_small_multiply(now, acc);
+        };
+        for (int i = 0; i < count / 2; ++i) {
+            piece_of(f0, f1, A, B);
+            piece_of(f1, f0, B, A);
+        }
+        if (count & 1) piece_of(f0, f1, A, B);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);      // vmcnt 0, lgkmcnt 0: nothing lands from here on
+    asm volatile("" ::: "memory");
+    __syncthreads();
+    // [wave][quarter of the tile][quarter of a lane's registers][lane]
+    float4* sum = reinterpret_cast<float4*>(sa);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sum[((wave * 4 + i * 2 + j) * 4 + v) * 64 + lane] = make_float4(
+                    acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]);
+    __syncthreads();
+    f32x16 total = {};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float4 x = sum[((w * 4 + wave) * 4 + v) * 64 + lane];
+            total[4 * v] += x.x;
+            total[4 * v + 1] += x.y;
+            total[4 * v + 2] += x.z;
+            total[4 * v + 3] += x.w;
+        }
+    sp_block<MODE>(total, reinterpret_cast<float*>(sb) + wave * (32 * SP_SB), q, fin, ti * 2 + wave / 2, tj * 2 + wave % 2);
 }
 
 // Adds the partial sums of the tiles that several blocks share.  A wave takes
@@ -324,7 +554,8 @@ __global__ __launch_bounds__(256) void sp_join_kernel(SpProduct q, SpFinal<T, F>
 {
     __shared__ float shared[4][32 * SP_SB];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int t = (int)blockIdx.x / 16, blk = (int)blockIdx.x % 16 * 4 + wave;
+    const int edge = q.tile / 32, per = edge * edge / 4;      // blocks of this launch per tile
+    const int t = (int)blockIdx.x / per, blk = (int)blockIdx.x % per * 4 + wave;
     const int64_t units = (int64_t)sp_tiles(q) * q.kb, ua = (int64_t)t * q.kb, ub = ua + q.kb - 1;
     // the block that holds unit u: the largest b with first(b) <= u
     auto holder = [&](int64_t u) {
@@ -335,34 +566,102 @@ __global__ __launch_bounds__(256) void sp_join_kernel(SpProduct q, SpFinal<T, F>
     };
     const int ba = holder(ua), bb = holder(ub);
     if (ba == bb) return;
+    // (the tile's first block may have begun in an earlier tile: its sums of this one are in its second place)
     f32x16 acc = {};
-    for (int b = ba; b <= bb; ++b) {
-        const int seg = sp_first(q, b) / q.kb == t ? 0 : 1;
-        const float4* in = reinterpret_cast<const float4*>(q.part + ((int64_t)b * 2 + seg) * SP_PART) + blk * 256 + lane;
+    auto at = [&](int b) {
+        const int seg = b == ba && sp_first(q, b) < ua ? 1 : 0;
+        return reinterpret_cast<const float4*>(q.part + ((int64_t)b * 2 + seg) * q.tile * q.tile) + blk * 256 + lane;
+    };
+    auto add = [&](const float4 (&w)[4]) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const float4 w = in[v * 64];
-            acc[4 * v] += w.x;
-            acc[4 * v + 1] += w.y;
-            acc[4 * v + 2] += w.z;
-            acc[4 * v + 3] += w.w;
+            acc[4 * v] += w[v].x;
+            acc[4 * v + 1] += w[v].y;
+            acc[4 * v + 2] += w[v].z;
+            acc[4 * v + 3] += w[v].w;
         }
+    };
+    int b = ba;
+    for (; b + 3 <= bb; b += 4) {      // four blocks' loads in flight
+        float4 w[4][4];
+#pragma unroll
+        for (int l = 0; l < 4; ++l)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) w[l][v] = at(b + l)[v * 64];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) add(w[l]);
+    }
+    for (; b <= bb; ++b) {
+        float4 w[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) w[v] = at(b)[v * 64];
+        add(w);
     }
     int ti, tj;
     sp_tile_at(q, t, ti, tj);
-    sp_block<MODE>(acc, shared[wave], q, fin, ti * 8 + blk / 8, tj * 8 + blk % 8);
+    sp_block<MODE>(acc, shared[wave], q, fin, ti * edge + blk / edge, tj * edge + blk % edge);
+}
+
+// Blocks of a product with tiles of edge 128 or 256 that share their
+// reductions: one for each CU, but no more than 16 for a tile (the joining
+// launch adds a tile's partial sums one after another).
+int sp_grid(int64_t tiles, int kb)
+{
+    return (int)std::min<int64_t>(std::min<int64_t>(SP_GRID, 16 * tiles), (tiles * kb + 1) / 2);
+}
+bool sp_joins(int64_t tiles, int kb, int grid) { return tiles * kb % grid != 0 || tiles * kb / grid % kb != 0; }
+
+// The tile whose estimated time is least, in microseconds from timings of
+// 512..4096 square and of long products: 64 takes 4.5 + 0.24 a piece for each
+// round of a block per CU, and its launch writes the result itself; 128 takes
+// 0.85 a piece and 12, 256 2.75 a piece and 16, and where blocks share tiles
+// the joining launch adds 12 or 20.  Times of P X (64, 128, 256): m = n = 1024
+// 14, 26, 38 us; 2048: 77, 57, 76; 4096: 499, 406, 348.
+int sp_tile(SpProduct q)
+{
+    double best = 0.0;
+    int pick = 0;
+    for (int tile : {64, 128, 256}) {
+        q.mt = (q.m + tile - 1) / tile;
+        q.nt = (q.n + tile - 1) / tile;
+        const int64_t t = sp_tiles(q);
+        double us;
+        if (tile == SP_SMALL) {
+            us = (double)((t + SP_GRID - 1) / SP_GRID) * (4.5 + 0.24 * q.kb);
+        } else {
+            const int grid = sp_grid(t, q.kb);
+            const bool joins = sp_joins(t, q.kb, grid);
+            const double pieces = (double)((t * q.kb + grid - 1) / grid);
+            us = tile == 128 ? 0.85 * pieces + (joins ? 24 : 12) : 2.75 * pieces + (joins ? 36 : 16);
+        }
+        if (!pick || us < best) {
+            pick = tile;
+            best = us;
+        }
+    }
+    return pick;
 }
 
 template <int MODE, typename T = float, typename F = SpNone>
 hipError_t sp_run(SpProduct q, const SpFinal<T, F>& fin, hipStream_t s)
 {
-    const int64_t units = (int64_t)sp_tiles(q) * q.kb;
-    q.grid = (int)std::min<int64_t>(SP_GRID, (units + 1) / 2);
-    hipLaunchKernelGGL((sp_product_kernel<MODE, T, F>), dim3((unsigned)q.grid), dim3(SP_T), 0, s, q, fin);
+    q.tile = sp_tile(q);
+    q.mt = (q.m + q.tile - 1) / q.tile;
+    q.nt = (q.n + q.tile - 1) / q.tile;
+    const int64_t tiles = sp_tiles(q);
+    if (q.tile == SP_SMALL) {
+        hipLaunchKernelGGL((sp_small_kernel<MODE, T, F>), dim3((unsigned)tiles), dim3(256), 0, s, q, fin);
+        return hipGetLastError();
+    }
+    q.grid = sp_grid(tiles, q.kb);
+    if (q.tile == 256)
+        hipLaunchKernelGGL((sp_product_kernel<256, MODE, T, F>), dim3((unsigned)q.grid), dim3(512), 0, s, q, fin);
+    else
+        hipLaunchKernelGGL((sp_product_kernel<128, MODE, T, F>), dim3((unsigned)q.grid), dim3(256), 0, s, q, fin);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (units % q.grid == 0 && units / q.grid % q.kb == 0) return e;      // whole tiles everywhere
-    hipLaunchKernelGGL((sp_join_kernel<MODE, T, F>), dim3((unsigned)sp_tiles(q) * 16), dim3(256), 0, s, q, fin);
+    if (e != hipSuccess || !sp_joins(tiles, q.kb, q.grid)) return e;
+    const int edge = q.tile / 32;
+    hipLaunchKernelGGL((sp_join_kernel<MODE, T, F>), dim3((unsigned)(tiles * edge * edge / 4)), dim3(256), 0, s, q, fin);
     return hipGetLastError();
 }
 
@@ -523,13 +822,11 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
                        (float)sx, q, (int)tall);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
-    const int mt = (m + SP_TILE - 1) / SP_TILE, nt = (n + SP_TILE - 1) / SP_TILE;
     const SpFinal<float, SpNone> none{};
     for (int k = 0; k < c.steps; ++k) {
         const double sa = sp_scale(1.01 * bd.x[k] * bd.x[k]), sp = sp_scale(1.01 * bd.p[k]);
         q.p = q.r = X;
         q.kb = pieces(n);
-        q.mt = q.nt = mt;
         q.sym = 1;
         q.last = 0;
         q.m = q.n = m;
@@ -545,7 +842,6 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
         if ((e = sp_run<SP_POLY>(q, none, s)) != hipSuccess) return e;
         q.p = P;
         q.r = XT[k & 1];
-        q.nt = nt;
         q.sym = 0;
         q.last = 1;
         q.n = n;
@@ -567,9 +863,11 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
 
 }  // namespace
 
-constexpr int SP_MIN = 512;
+// Shorter sides from which these products beat the fp64 path's on the short side: 333 x 1001 takes 152 us here and
+// 214 there, 256 x 6912 238 and 190.
+constexpr int SP_MIN = 320;
 
-bool ns_split_size(int m, int n) { return m >= SP_MIN; }
+bool ns_split_size(int m) { return m >= SP_MIN; }
 bool ns_split_coef(const NsCoef& c) { return ns_bounds(c).fits; }
 size_t ns_split_ws_bytes(int m, int n) { return sp_layout(m, n).bytes; }
 
