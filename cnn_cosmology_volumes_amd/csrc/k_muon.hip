@@ -25,11 +25,13 @@
 #include "cf_internal.h"
 
 #include <algorithm>
+#include <climits>
 
 namespace cf {
 namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int NS_T = 256;       // threads per block, 4 waves
 constexpr int NS_TILE = 64;     // edge of an output tile of U U^T and of Q U
@@ -41,11 +43,22 @@ constexpr int NS_SK = NS_K + 1;       // LDS row stride of a [64][k] panel
 int up(int v, int m) { return (v + m - 1) / m * m; }
 size_t up256b(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// The matrix whose range of blocks holds block b.
-__device__ __forceinline__ int find(const int* start, int count, int b)
+// First blocks of a launch's matrices; past the last one, past any block.
+struct Starts {
+    int at[CF_MAX_OPT_TENSORS];
+    void set(int i, int first) { at[i] = first; }
+    void clear()
+    {
+        for (int& v : at) v = INT_MAX;
+    }
+};
+// The matrix whose range of blocks holds block b: every entry is read at once,
+// a search would wait for one load after another.
+__device__ __forceinline__ int find(const Starts& s, int b)
 {
     int i = 0;
-    while (i + 1 < count && b >= start[i + 1]) ++i;
+#pragma unroll
+    for (int k = 1; k < CF_MAX_OPT_TENSORS; ++k) i += b >= s.at[k] ? 1 : 0;
     return i;
 }
 
@@ -109,8 +122,7 @@ template <bool TALL> __device__ __forceinline__ void panel_store(const float (&v
 constexpr int NS_PANEL = NS_K * NS_SP > NS_TILE * NS_SK ? NS_K * NS_SP : NS_TILE * NS_SK;
 
 struct GramArgs {
-    int count;
-    int start[CF_MAX_OPT_TENSORS + 1];        // first block of each matrix
+    Starts start;
     const void* u[CF_MAX_OPT_TENSORS];
     int m[CF_MAX_OPT_TENSORS], n[CF_MAX_OPT_TENSORS];
     int kc[CF_MAX_OPT_TENSORS];               // reduction indices per split
@@ -190,7 +202,7 @@ template <typename T> __global__ __launch_bounds__(NS_T) void ns_gram_kernel(Gra
 {
     __shared__ float sh[2 * NS_PANEL];
     __shared__ double red[4];
-    const int i = find(g.start, g.count, (int)blockIdx.x), b = (int)blockIdx.x - g.start[i];
+    const int i = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[i];
     const T* U = (const T*)g.u[i];
     if (g.tall >> i & 1) gram_tile<true>(U, g.m[i], g.n[i], g.kc[i], g.splits[i], b, ws + g.part[i], sh, red);
     else gram_tile<false>(U, g.m[i], g.n[i], g.kc[i], g.splits[i], b, ws + g.part[i], sh, red);
@@ -198,43 +210,57 @@ template <typename T> __global__ __launch_bounds__(NS_T) void ns_gram_kernel(Gra
 
 // ------------------------------------------------- A_0 from the partial sums
 struct SquareArgs {
-    int count;
-    int start[CF_MAX_OPT_TENSORS + 1];
+    Starts start;
     int m[CF_MAX_OPT_TENSORS];
     int splits[CF_MAX_OPT_TENSORS];
     int64_t part[CF_MAX_OPT_TENSORS];     // doubles from the workspace's start
     int64_t sq[CF_MAX_OPT_TENSORS];       // the five m x m buffers, each ld x ld
 };
+// Rows, and values of a row, of an m x m fp64 buffer.
 __host__ __device__ inline int ns_ld(int m) { return (m + NS_TILE - 1) / NS_TILE * NS_TILE; }
+__host__ __device__ inline int64_t ns_size(int m) { return (int64_t)ns_ld(m) * ns_ld(m); }
+// Values from one row to the next of the bf16 planes that Q ends in (they take
+// the place of a buffer).  With rows of a power of two their columns would
+// share few memory channels: the product with U took 28 us in place of 17 for
+// 6912 x 256.
+__host__ __device__ inline int ns_plane_ld(int m) { return ns_ld(m) + 16; }
+__host__ __device__ inline int64_t ns_plane(int m) { return (int64_t)ns_ld(m) * ns_plane_ld(m); }
 
-// Block = 16 rows of a tile pair: sums the splits in order, scales by s^2 and
-// writes the element and its mirror; block 0 of a matrix also stores s.
-constexpr int NS_JR = 16;
+// Block = one row of a tile pair: four groups of threads each sum every fourth
+// split, then the groups are added in order; scales by s^2 and writes the
+// element and its mirror.  Block 0 of a matrix also stores s.
 __global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, double* ws, double* scale)
 {
-    __shared__ double red[4];
-    const int q = find(g.start, g.count, (int)blockIdx.x), b = (int)blockIdx.x - g.start[q];
+    __shared__ double red[4], group[4][NS_TILE];
+    const int q = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[q];
     const int m = g.m[q], splits = g.splits[q], ld = ns_ld(m), nt = ld / NS_TILE, pairs = nt * (nt + 1) / 2;
     const double* part = ws + g.part[q];
+    const int p = b / NS_TILE, i = b % NS_TILE, j = (int)threadIdx.x % NS_TILE, w = (int)threadIdx.x / NS_TILE;
+    const double* in = part + (int64_t)p * (NS_TILE * NS_TILE) + i * NS_TILE + j;
+    const int64_t step = (int64_t)pairs * (NS_TILE * NS_TILE);
+    double v = 0.0;
+    int k = w;
+    for (; k + 28 < splits; k += 32) {
+        double x[8];
+#pragma unroll
+        for (int l = 0; l < 8; ++l) x[l] = in[(k + 4 * l) * step];
+#pragma unroll
+        for (int l = 0; l < 8; ++l) v += x[l];
+    }
+    for (; k < splits; k += 4) v += in[k * step];
+    group[w][j] = v;
     double tr = 0.0;
-    for (int i = (int)threadIdx.x; i < splits * nt; i += NS_T)
-        tr += part[(int64_t)splits * pairs * (NS_TILE * NS_TILE) + i];
-    const double s = 1.0 / (sqrt(block_sum(tr, red)) + (double)eps);
+    for (int e = (int)threadIdx.x; e < splits * nt; e += NS_T) tr += part[(int64_t)splits * pairs * (NS_TILE * NS_TILE) + e];
+    const double s = 1.0 / (sqrt(block_sum(tr, red)) + (double)eps);      // (its barriers cover `group` too)
     if (b == 0 && threadIdx.x == 0) scale[q] = s;
-    const int p = b / (NS_TILE / NS_JR), r0 = b % (NS_TILE / NS_JR) * NS_JR;
     int ti, tj;
     tile_pair(p, nt, ti, tj);
+    if (w != 0 || (ti == tj && i > j)) return;
+    v = (((group[0][j] + group[1][j]) + group[2][j]) + group[3][j]) * (s * s);
     double* A = ws + g.sq[q];
-    for (int e = (int)threadIdx.x; e < NS_JR * NS_TILE; e += NS_T) {
-        const int i = r0 + e / NS_TILE, j = e % NS_TILE;
-        if (ti == tj && i > j) continue;
-        double v = 0.0;
-        for (int k = 0; k < splits; ++k) v += part[((int64_t)k * pairs + p) * (NS_TILE * NS_TILE) + i * NS_TILE + j];
-        v *= s * s;
-        const int64_t I = ti * NS_TILE + i, J = tj * NS_TILE + j;
-        A[I * ld + J] = v;
-        A[J * ld + I] = v;
-    }
+    const int64_t I = ti * NS_TILE + i, J = tj * NS_TILE + j;
+    A[I * ld + J] = v;
+    A[J * ld + I] = v;
 }
 
 // ------------------------------------------------------ m x m symmetric rounds
@@ -243,6 +269,7 @@ __global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, 
 struct Product {
     int x, y, d;         // buffer indices
     int poly;
+    int last;            // D as three bf16 planes for the product with U
 };
 struct RoundArgs {
     SquareArgs s;
@@ -251,21 +278,35 @@ struct RoundArgs {
     float a, b, c;
 };
 
+// v = hi + mid + lo, each the bf16 nearest to what is left, up to 2^-24 of v;
+// planes of `size` elements.
+__device__ __forceinline__ void put_planes(uint16_t* p, int64_t size, int64_t i, double v)
+{
+    const uint16_t hi = f2bf((float)v);
+    const double r = v - (double)bf2f(hi);
+    const uint16_t mid = f2bf((float)r);
+    p[i] = hi;
+    p[size + i] = mid;
+    p[2 * size + i] = f2bf((float)(r - (double)bf2f(mid)));
+}
+
 // Block = one (16 TS)^2 tile of the upper triangle; its four waves take every
 // fourth 16-deep piece of the reduction and are joined through LDS in order.
 // A lane's 16-byte loads cover k = 4 (lane / 16) + 0..3 of a piece: the order
 // of k within a piece is the same for both operands.
+constexpr int ns_unroll(int ts) { return ts == 1 ? 4 : 2; }      // 64 registers of operands in flight
+
 template <int TS>
 __global__ __launch_bounds__(NS_T) void ns_round_kernel(RoundArgs g, double* ws)
 {
     constexpr int E = 16 * TS;
     __shared__ double sh[4][E * (E + 1)];
-    const int q = find(g.s.start, g.s.count, (int)blockIdx.x), b = (int)blockIdx.x - g.s.start[q];
+    const int q = find(g.s.start, (int)blockIdx.x), b = (int)blockIdx.x - g.s.start.at[q];
     const int m = g.s.m[q], ld = ns_ld(m), nt = (m + E - 1) / E, pairs = nt * (nt + 1) / 2;
     const Product pr = g.p[b / pairs];
     int ti, tj;
     tile_pair(b % pairs, nt, ti, tj);
-    const int64_t sz = (int64_t)ld * ld;
+    const int64_t sz = ns_size(m);
     const double* X = ws + g.s.sq[q] + pr.x * sz;
     const double* Y = ws + g.s.sq[q] + pr.y * sz;
     double* D = ws + g.s.sq[q] + pr.d * sz;
@@ -274,7 +315,7 @@ __global__ __launch_bounds__(NS_T) void ns_round_kernel(RoundArgs g, double* ws)
     const double* x = X + (int64_t)ti * E * ld + at;
     const double* y = Y + (int64_t)tj * E * ld + at;
     f64x4 acc[TS][TS] = {};
-#pragma unroll 2
+#pragma unroll ns_unroll(TS)
     for (int k = wave * 16; k < m; k += 64) {
         f64x4 u[TS], v[TS];
 #pragma unroll
@@ -311,7 +352,9 @@ __global__ __launch_bounds__(NS_T) void ns_round_kernel(RoundArgs g, double* ws)
                 v = (double)g.c * v + (double)g.b * Y[(int64_t)I * ld + J];
                 if (I == J && I < m) v += (double)g.a;
             }
-            if (I < ld && J < ld) D[(int64_t)I * ld + J] = v;
+            if (I >= ld || J >= ld) continue;
+            if (pr.last) put_planes((uint16_t*)D, ns_plane(m), (int64_t)I * ns_plane_ld(m) + J, v);
+            else D[(int64_t)I * ld + J] = v;
         }
 }
 
@@ -326,101 +369,357 @@ struct ApplyArgs {                      // w <- w keep - rate o
     float keep;
 };
 struct FinalArgs {
-    int count;
-    int start[CF_MAX_OPT_TENSORS + 1];
+    Starts start;
     const void* u[CF_MAX_OPT_TENSORS];
     int m[CF_MAX_OPT_TENSORS], n[CF_MAX_OPT_TENSORS];
     uint32_t tall;
     int64_t q[CF_MAX_OPT_TENSORS];      // the Q buffer, doubles from the workspace's start
 };
 
-template <typename T> __device__ __forceinline__ void finish(const StoreArgs& a, int q, int64_t i, float o)
+// Done in three passes over a tile's elements: loads, results, stores.  The
+// compiler may not move a load past a store, and a wait for a load between
+// stores would wait for the stores too.
+__device__ __forceinline__ float before(const StoreArgs&, int, int64_t) { return 0.f; }
+__device__ __forceinline__ float before(const ApplyArgs& a, int q, int64_t i) { return a.w[q][i]; }
+__device__ __forceinline__ float result(const StoreArgs&, int, float o, float) { return o; }
+__device__ __forceinline__ float result(const ApplyArgs& a, int q, float o, float w) { return fmaf(-a.rate[q], o, w * a.keep); }
+template <typename T> __device__ __forceinline__ void finish(const StoreArgs& a, int q, int64_t i, float v)
 {
-    Elem<T>::store((T*)a.out[q], i, o);
+    Elem<T>::store((T*)a.out[q], i, v);
 }
-template <typename T> __device__ __forceinline__ void finish(const ApplyArgs& a, int q, int64_t i, float o)
-{
-    float* w = a.w[q] + i;
-    *w = fmaf(-a.rate[q], o, *w * a.keep);
-}
+template <typename T> __device__ __forceinline__ void finish(const ApplyArgs& a, int q, int64_t i, float v) { a.w[q][i] = v; }
+// Keeps a result's computation before the stores.
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 
-// Block = a 64 (short side) x 64 (long side) tile of s Q U on the fp32 matrix
-// cores.  Both operands are staged [64][k] or [k][64] as U lies in memory; Q,
-// symmetric, is staged as it is read.  The lanes that hold neighbouring
+// Block = a 64 (short side) x 64 (long side) tile of s Q U on the bf16 matrix
+// cores, with both operands as hi + mid + lo (Q's planes from the last round, U
+// split as it is staged; 24 bits, an fp32 value whole) and the six products
+// above 2^-24: fp32's accuracy and range at 2.7 times its matrix rate.  A stage
+// is 64 deep, for there are few: its loads, in flight while the stage before it
+// is multiplied, are what takes the time.  The lanes that hold neighbouring
 // outputs run along the matrix's rows in memory: short-side indices are the
 // matrix core's columns for a tall matrix and its rows for a wide one.
+constexpr int NF_K = 64;
+constexpr int NF_ROW = NF_K + 8;                 // LDS row stride: 16 rows of an operand fall on all banks
+constexpr int NF_PLANE = NS_TILE * NF_ROW;
+
 template <bool TALL, typename T, typename F>
-__device__ void final_tile(const T* U, const double* Q, double s, int m, int n, int b, const F& f, int q, float* sh)
+__device__ void final_tile(const T* U, const uint16_t* Q, double s, int m, int n, int b, const F& f, int q, uint16_t* sh)
 {
-    const int ld = ns_ld(m), nt = (m + NS_TILE - 1) / NS_TILE;
-    const int i0 = b % nt * NS_TILE, c0 = b / nt * NS_TILE;     // short, long
-    float* A = sh;                       // Q: [64 short][k]
-    float* B = sh + NS_PANEL;            // U: [64 long][k] for a tall matrix, [k][64 long] for a wide one
+    const int ld = ns_plane_ld(m), across = (m + 63) / 64;
     const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int ws = (wave >> 1) * 32, wl = (wave & 1) * 32;      // this wave's quadrant: short, long
-    f32x4 acc[2][2] = {};
-    float va[NS_PV], vb[NS_PV];
+    const int i0 = b % across * 64, j0 = b / across * 64;      // short, long
+    const int64_t size = ns_plane(m);
+    uint16_t* const su = sh;                                   // [3][64 long][64 k]
+    uint16_t* const sq = sh + 3 * NF_PLANE;                    // [3][64 short][64 k]
+    // a thread stages twice 8 values of k of one row of each
+    const int row = TALL ? t / 4 : t % 64, k8 = TALL ? t % 4 * 8 : t / 64 * 8;
+    const int j = min(j0 + row, n - 1);
+    const uint16_t* qp = Q + (int64_t)(i0 + t / 4) * ld + t % 4 * 8;
+    T u[2][8];
+    bf16x8 p[2][3];
     auto load = [&](int k0) {
 #pragma unroll
-        for (int r = 0; r < NS_PV; ++r) {
-            const int i = t / NS_K + r * (NS_T / NS_K), k = k0 + t % NS_K;
-            // (beyond m the buffers hold anything)
-            va[r] = i0 + i < m && k < m ? (float)(Q[(int64_t)(i0 + i) * ld + k] * s) : 0.f;
-        }
-        if (TALL) panel_load<false>(vb, U, n, m, c0, k0, m);
-        else panel_load<true>(vb, U, n, m, c0, k0, m);
-    };
-    load(0);
-    for (int k0 = 0; k0 < m; k0 += NS_K) {
-        __syncthreads();
-        panel_store<false>(va, A);
-        panel_store<!TALL>(vb, B);
-        __syncthreads();
-        if (k0 + NS_K < m) load(k0 + NS_K);
+        for (int x = 0; x < 2; ++x) {
+            const int k = k0 + x * 32 + k8;
+            if (k0 + NF_K <= m) {
+                if (TALL) {
+                    __builtin_memcpy(u[x], U + (int64_t)j * m + k, sizeof(u[x]));
+                } else {
 #pragma unroll
-        for (int st = 0; st < NS_K / 4; ++st) {
-            float a[2], c[2];
+                    for (int e = 0; e < 8; ++e) u[x][e] = U[(int64_t)(k + e) * n + j];
+                }
+            } else {
+                asm volatile("");      // not joined with the wide loads above
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int kk = st * 4 + lane / 16, i = ws + r * 16 + lane % 16, j = wl + r * 16 + lane % 16;
-                a[r] = A[i * NS_SK + kk];
-                c[r] = B[TALL ? j * NS_SK + kk : kk * NS_SP + j];
+                for (int e = 0; e < 8; ++e) {
+                    const int c = min(k + e, m - 1);
+                    u[x][e] = U[TALL ? (int64_t)j * m + c : (int64_t)c * n + j];
+                }
+                asm volatile("");
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int e = 0; e < 3; ++e) p[x][e] = *reinterpret_cast<const bf16x8*>(qp + e * size + k0 + x * 32);
+        }
+    };
+    auto store = [&](int k0) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+        for (int x = 0; x < 2; ++x) {
+            bf16x8 d[3];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = k0 + x * 32 + k8 + e < m ? (float)((double)elem(u[x], e) * s) : 0.f;
+                d[0][e] = (__bf16)v;
+                const float v1 = v - (float)d[0][e];
+                d[1][e] = (__bf16)v1;
+                d[2][e] = (__bf16)(v1 - (float)d[1][e]);
+            }
+            // (Q's columns are zeros up to a multiple of 16 above m, and hold anything after it)
+            if (k0 + x * 32 + t % 4 * 8 >= m)
+#pragma unroll
+                for (int e = 0; e < 3; ++e) p[x][e] = bf16x8{};
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                *reinterpret_cast<bf16x8*>(su + e * NF_PLANE + row * NF_ROW + x * 32 + k8) = d[e];
+                *reinterpret_cast<bf16x8*>(sq + e * NF_PLANE + t / 4 * NF_ROW + x * 32 + t % 4 * 8) = p[x][e];
+            }
+        }
+    };
+    const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;      // this wave's quadrant: short, long
+    const bf16x8* a = reinterpret_cast<const bf16x8*>(sq + (wi + lane % 32) * NF_ROW + lane / 32 * 8);
+    const bf16x8* c = reinterpret_cast<const bf16x8*>(su + (wj + lane % 32) * NF_ROW + lane / 32 * 8);
+    f32x16 acc = {}, small = {};
+    // the stages in a round that starts elsewhere for the next block: all blocks at one k would read rows that lie
+    // 4 m bytes apart, from a part of the memory channels
+    const int stages = (m + NF_K - 1) / NF_K;
+    int k0 = (b / across + b) % stages * NF_K;
+    load(k0);
+    for (int i = 0; i < stages; ++i) {
+        __syncthreads();
+        store(k0);
+        __syncthreads();
+        k0 = k0 + NF_K < m ? k0 + NF_K : 0;
+        if (i + 1 < stages) load(k0);
+#pragma unroll
+        for (int k = 0; k < NF_K / 16; ++k) {
+            bf16x8 x[3], y[3];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                x[e] = a[(e * NF_PLANE + k * 16) / 8];
+                y[e] = c[(e * NF_PLANE + k * 16) / 8];
+            }
+#pragma unroll
+            for (int z = 0; z < 6; ++z) {
+                    // (e, o): 02 00 11 01 20 10: three of the second order in one chain, three larger in the other
+                    const int o = z % 2 == 0 ? 2 : z == 1 ? 0 : 1, e = z == 0 || z == 1 || z == 3 ? 0 : z == 4 ? 2 : 1;
+                    f32x16& sum = o == 2 ? small : acc;
                     // rows from the first operand, columns (lanes) from the second
-                    acc[x][y] = TALL ? __builtin_amdgcn_mfma_f32_16x16x4f32(c[y], a[x], acc[x][y], 0, 0, 0)
-                                     : __builtin_amdgcn_mfma_f32_16x16x4f32(a[x], c[y], acc[x][y], 0, 0, 0);
+                    sum = TALL ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(y[o - e], x[e], sum, 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[e], y[o - e], sum, 0, 0, 0);
+                }
         }
     }
+    // register v of a lane: row 8 (v / 4) + 4 (lane / 32) + v % 4, column lane % 32
+    auto place = [&](int v) {
+        const int r = 8 * (v / 4) + 4 * (lane / 32) + v % 4, l = lane % 32;
+        const int I = i0 + wi + (TALL ? l : r), J = j0 + wj + (TALL ? r : l);
+        return I < m && J < n ? TALL ? (int64_t)J * m + I : (int64_t)I * n + J : (int64_t)-1;
+    };
+    float w[16];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int v = 0; v < 16; ++v) w[v] = before(f, q, max(place(v), (int64_t)0));
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+    for (int v = 0; v < 16; ++v) {
+        w[v] = result(f, q, acc[v] + small[v], w[v]);
+        settle(w[v]);
+    }
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int row = 4 * (lane / 16) + v, col = lane % 16;
-                const int i = i0 + ws + x * 16 + (TALL ? col : row), j = c0 + wl + y * 16 + (TALL ? row : col);
-                if (i < m && j < n) finish<T>(f, q, TALL ? (int64_t)j * m + i : (int64_t)i * n + j, acc[x][y][v]);
-            }
+    for (int v = 0; v < 16; ++v) {
+        const int64_t at = place(v);
+        if (at >= 0) finish<T>(f, q, at, w[v]);
+    }
 }
 
 template <typename T, typename F>
 __global__ __launch_bounds__(NS_T) void ns_final_kernel(FinalArgs g, F f, const double* ws, const double* scale)
 {
-    __shared__ float sh[2 * NS_PANEL];
-    const int i = find(g.start, g.count, (int)blockIdx.x), b = (int)blockIdx.x - g.start[i];
+    __shared__ __attribute__((aligned(16))) uint16_t sh[6 * NF_PLANE];
+    const int i = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[i];
     const T* U = (const T*)g.u[i];
-    if (g.tall >> i & 1) final_tile<true>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
-    else final_tile<false>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
+    const uint16_t* Q = (const uint16_t*)(ws + g.q[i]);
+    if (g.tall >> i & 1) final_tile<true>(U, Q, scale[i], g.m[i], g.n[i], b, f, i, sh);
+    else final_tile<false>(U, Q, scale[i], g.m[i], g.n[i], b, f, i, sh);
+}
+
+// ----------------------------------------------- one block for a small matrix
+// The iteration of a matrix with m <= 64 in one block's LDS: three fp64 m x m
+// buffers, results held in registers until every wave has read.  WHOLE: also
+// U U^T and s Q U, from U in LDS; else A_0 comes from the joining launch and Q
+// goes to its planes.
+constexpr int NB_T = 1024;
+constexpr int NB_W = NB_T / 64;                  // waves
+constexpr int NB_M = 64;
+constexpr int NB_BUF = NB_M * (NB_M + 2);        // a row of LD = 16 t + 2 doubles: the 16 rows of an operand start an
+                                                 // odd number of 16-byte steps apart
+constexpr int NB_U = 10240;                      // floats of U
+__host__ __device__ inline int nb_ldu(int mp) { return mp + (mp % 32 == 0 ? 16 : 0); }      // 4 rows of 16: 64 banks
+bool ns_whole(int m, int n) { return m <= NB_M && (int64_t)nb_ldu(up(m, 16)) * up(n, 16) <= NB_U; }
+
+struct BlockArgs {
+    const void* u[CF_MAX_OPT_TENSORS];
+    int m[CF_MAX_OPT_TENSORS], n[CF_MAX_OPT_TENSORS];
+    uint32_t tall;
+    int64_t a[CF_MAX_OPT_TENSORS], q[CF_MAX_OPT_TENSORS];      // A_0 and Q's planes, doubles from the workspace's start
+    int steps;
+    float ca, cb, cc, eps;
+};
+
+template <bool WHOLE, typename T, typename F>
+__global__ __launch_bounds__(NB_T) void ns_block_kernel(BlockArgs g, F f, double* ws)
+{
+    __shared__ double A[NB_BUF], P[NB_BUF], Q[NB_BUF];
+    __shared__ double part[WHOLE ? 8 * 256 : 1], trace[4];
+    __shared__ float us[WHOLE ? NB_U : 1];
+    const int q = (int)blockIdx.x, m = g.m[q], n = g.n[q];
+    const int mp = (m + 15) / 16 * 16, LD = mp + 2, nt = mp / 16, pairs = nt * (nt + 1) / 2;
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int r = lane % 16, h = lane / 16;      // operands: row r, k = h; results: row 4 v + h, column r
+    const bool tall = g.tall >> q & 1;
+    double s = 0.0;
+
+    // a 16 x 16 tile of X Y, both symmetric
+    auto product = [&](const double* X, const double* Y, int p) {
+        int ti, tj;
+        tile_pair(p, nt, ti, tj);
+        const double* x = X + (ti * 16 + r) * LD + h;
+        const double* y = Y + (tj * 16 + r) * LD + h;
+        f64x4 a0 = {}, a1 = {};      // two chains: a matrix instruction waits for its own sum
+#pragma unroll 2
+        for (int k = 0; k < mp; k += 16) {
+            a0 = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k], y[k], a0, 0, 0, 0);
+            a1 = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + 4], y[k + 4], a1, 0, 0, 0);
+            a0 = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + 8], y[k + 8], a0, 0, 0, 0);
+            a1 = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k + 12], y[k + 12], a1, 0, 0, 0);
+        }
+        return a0 + a1;
+    };
+    // its upper part and mirror
+    auto put = [&](double* D, int p, const f64x4& x) {
+        int ti, tj;
+        tile_pair(p, nt, ti, tj);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int i = ti * 16 + 4 * v + h, j = tj * 16 + r;
+            if (i > j) continue;
+            D[i * LD + j] = x[v];
+            D[j * LD + i] = x[v];
+        }
+    };
+
+    if constexpr (WHOLE) {
+        const T* U = (const T*)g.u[q];
+        const int ldu = nb_ldu(mp), np = (n + 15) / 16 * 16;
+        for (int e = t; e < np * ldu; e += NB_T) us[e] = 0.f;
+        __syncthreads();
+        for (int e = t; e < n * m; e += NB_T) {
+            const int k = tall ? e / m : e % n, i = tall ? e % m : e / n;
+            us[k * ldu + i] = elem(U, e);
+        }
+        __syncthreads();
+        // few tiles: their reductions are cut into parts, one for each wave
+        const int parts = max(1, 8 / pairs);
+        for (int w = wave; w < parts * pairs; w += NB_W) {
+            int ti, tj;
+            tile_pair(w % pairs, nt, ti, tj);
+            f64x4 acc = {};
+            for (int k = w / pairs * 4 + h; k < np; k += 4 * parts)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)us[k * ldu + ti * 16 + r], (double)us[k * ldu + tj * 16 + r],
+                                                           acc, 0, 0, 0);
+            if (parts > 1) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) part[w * 256 + v * 64 + lane] = acc[v];
+            } else {
+                put(A, w, acc);
+            }
+        }
+        __syncthreads();
+        if (parts > 1) {
+            if (wave < pairs) {
+                f64x4 acc = {};
+                for (int x = 0; x < parts; ++x)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[v] += part[(x * pairs + wave) * 256 + v * 64 + lane];
+                put(A, wave, acc);
+            }
+            __syncthreads();
+        }
+        if (wave == 0) {
+            const double tr = wave_sum(lane < m ? A[lane * LD + lane] : 0.0);
+            if (lane == 0) trace[0] = tr;
+        }
+        __syncthreads();
+        s = 1.0 / (sqrt(trace[0]) + (double)g.eps);
+        for (int e = t; e < mp * mp; e += NB_T) A[e / mp * LD + e % mp] *= s * s;
+    } else {
+        const double* in = ws + g.a[q];
+        const int ld = ns_ld(m);
+        for (int e = t; e < mp * mp; e += NB_T) A[e / mp * LD + e % mp] = in[(int64_t)(e / mp) * ld + e % mp];
+    }
+    __syncthreads();
+    for (int k = 0; k < g.steps; ++k) {
+        const bool last = k + 1 == g.steps;
+        for (int p = wave; p < pairs; p += NB_W) {
+            f64x4 x = product(A, A, p);
+            int ti, tj;
+            tile_pair(p, nt, ti, tj);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = ti * 16 + 4 * v + h, j = tj * 16 + r;
+                x[v] = (double)g.cc * x[v] + (double)g.cb * A[i * LD + j] + (i == j && i < m ? (double)g.ca : 0.0);
+            }
+            put(P, p, x);
+            if (k == 0) put(Q, p, x);      // Q = P_0
+        }
+        __syncthreads();
+        // P A (but for the last step), P Q (but for the first): A and Q are replaced when all have read them
+        const int first = last ? pairs : 0, count = k == 0 ? pairs : 2 * pairs;
+        f64x4 x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int w = first + wave + NB_W * i;
+            if (w < count) x[i] = product(P, w < pairs ? A : Q, w < pairs ? w : w - pairs);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int w = first + wave + NB_W * i;
+            if (w < count) put(w < pairs ? A : Q, w < pairs ? w : w - pairs, x[i]);
+        }
+        __syncthreads();
+        if (last) break;
+        if (wave < pairs) x[0] = product(A, P, wave);
+        __syncthreads();
+        if (wave < pairs) put(A, wave, x[0]);
+        __syncthreads();
+    }
+    if constexpr (WHOLE) {
+        const int ldu = nb_ldu(mp), np = (n + 15) / 16 * 16;
+        for (int w = wave; w < np / 16 * nt; w += NB_W) {
+            const int i0 = w % nt * 16, j0 = w / nt * 16;      // short, long
+            f64x4 acc = {};
+            for (int k = 0; k < mp; k += 4) {
+                const double a = Q[(i0 + r) * LD + k + h], b = (double)us[(j0 + r) * ldu + k + h] * s;
+                acc = tall ? __builtin_amdgcn_mfma_f64_16x16x4f64(b, a, acc, 0, 0, 0)
+                           : __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, acc, 0, 0, 0);
+            }
+            int64_t at[4];
+            float x[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = i0 + (tall ? r : 4 * v + h), j = j0 + (tall ? 4 * v + h : r);
+                at[v] = i < m && j < n ? tall ? (int64_t)j * m + i : (int64_t)i * n + j : -1;
+                x[v] = before(f, q, max(at[v], (int64_t)0));
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                x[v] = result(f, q, (float)acc[v], x[v]);
+                settle(x[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (at[v] >= 0) finish<T>(f, q, at[v], x[v]);
+        }
+    } else {
+        const int ld = ns_plane_ld(m);
+        uint16_t* out = (uint16_t*)(ws + g.q[q]);
+        for (int e = t; e < mp * mp; e += NB_T)
+            put_planes(out, ns_plane(m), (int64_t)(e / mp) * ld + e % mp, Q[e / mp * LD + e % mp]);
+    }
 }
 
 // --------------------------------------------------------------- momentum
 struct MomentumArgs {
-    int count;
-    int start[CF_MAX_OPT_TENSORS + 1];
+    Starts start;
     int64_t n[CF_MAX_OPT_TENSORS];
     const float* g[CF_MAX_OPT_TENSORS];
     float* m[CF_MAX_OPT_TENSORS];
@@ -431,8 +730,8 @@ constexpr int MU_CHUNK = NS_T * MU_V * 4;
 
 __global__ __launch_bounds__(NS_T) void muon_momentum_kernel(MomentumArgs a, float mu, int nesterov)
 {
-    const int q = find(a.start, a.count, (int)blockIdx.x);
-    const int64_t n = a.n[q], base = (int64_t)((int)blockIdx.x - a.start[q]) * MU_CHUNK;
+    const int q = find(a.start, (int)blockIdx.x);
+    const int64_t n = a.n[q], base = (int64_t)((int)blockIdx.x - a.start.at[q]) * MU_CHUNK;
     const float* g = a.g[q];
     float* m = a.m[q];
     float* u = a.u[q];
@@ -482,110 +781,123 @@ NsPlan ns_plan(const NsShapes& l)
     kc = std::max<int64_t>(NS_KC_MIN, (kc + NS_K - 1) / NS_K * NS_K);
     int64_t at = CF_MAX_OPT_TENSORS;        // the scales come first
     for (int i = 0; i < l.count; ++i) {
-        const int64_t ld = ns_ld(l.m[i]), nt = ld / NS_TILE, pairs = nt * (nt + 1) / 2;
+        const int64_t nt = ns_ld(l.m[i]) / NS_TILE, pairs = nt * (nt + 1) / 2;
         p.kc[i] = (int)std::min<int64_t>(kc, up(l.n[i], NS_K));
         p.splits[i] = (l.n[i] + p.kc[i] - 1) / p.kc[i];
         p.part[i] = at;
         at += p.splits[i] * (pairs * NS_TILE * NS_TILE + nt);
         at = (at + 31) / 32 * 32;
         p.sq[i] = at;
-        at += 5 * ld * ld;
+        at += 5 * ns_size(l.m[i]);
     }
     p.doubles = at;
     return p;
 }
 
-// Runs U U^T to Q; *q receives the index of the buffer that holds Q.
-template <typename T>
-hipError_t ns_iterate(const NsShapes& l, const NsPlan& p, const void* const* u, const NsCoef& c, double* ws, int* q,
-                      hipStream_t s)
+// Everything of a list from U on.
+template <typename T, typename F>
+hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, const F& f, double* ws, hipStream_t s)
 {
+    const NsPlan p = ns_plan(l);
+    bool whole = true;
+    int maxm = 0;
+    BlockArgs k{};
+    k.tall = l.tall;
+    k.steps = c.steps;
+    k.ca = c.a;
+    k.cb = c.b;
+    k.cc = c.c;
+    k.eps = c.eps;
+    for (int i = 0; i < l.count; ++i) {
+        whole = whole && ns_whole(l.m[i], l.n[i]);
+        maxm = std::max(maxm, l.m[i]);
+        k.u[i] = u[i];
+        k.m[i] = l.m[i];
+        k.n[i] = l.n[i];
+        k.a[i] = p.sq[i];
+        k.q[i] = p.sq[i] + ns_size(l.m[i]);
+    }
+    if (whole) {
+        hipLaunchKernelGGL((ns_block_kernel<true, T, F>), dim3((unsigned)l.count), dim3(NB_T), 0, s, k, f, ws);
+        return hipGetLastError();
+    }
+
     GramArgs g{};
     SquareArgs sq{};
-    g.count = sq.count = l.count;
-    int maxm = 0;
+    FinalArgs a{};
+    g.start.clear();
+    sq.start.clear();
+    a.start.clear();
+    int grams = 0, joins = 0, finals = 0;
     for (int i = 0; i < l.count; ++i) {
         const int nt = ns_ld(l.m[i]) / NS_TILE, pairs = nt * (nt + 1) / 2;
-        g.u[i] = u[i];
-        g.m[i] = sq.m[i] = l.m[i];
-        g.n[i] = l.n[i];
+        g.u[i] = a.u[i] = u[i];
+        g.m[i] = sq.m[i] = a.m[i] = l.m[i];
+        g.n[i] = a.n[i] = l.n[i];
         g.kc[i] = p.kc[i];
         g.splits[i] = sq.splits[i] = p.splits[i];
         g.part[i] = sq.part[i] = p.part[i];
         sq.sq[i] = p.sq[i];
-        g.start[i + 1] = g.start[i] + p.splits[i] * pairs;
-        sq.start[i + 1] = sq.start[i] + pairs * (NS_TILE / NS_JR);
-        maxm = std::max(maxm, l.m[i]);
+        g.start.set(i, grams);
+        sq.start.set(i, joins);
+        a.start.set(i, finals);
+        grams += p.splits[i] * pairs;
+        joins += pairs * NS_TILE;
+        finals += nt * ((l.n[i] + 63) / 64);
     }
-    g.tall = l.tall;
-    hipLaunchKernelGGL(ns_gram_kernel<T>, dim3((unsigned)g.start[l.count]), dim3(NS_T), 0, s, g, ws);
+    g.tall = a.tall = l.tall;
+    hipLaunchKernelGGL(ns_gram_kernel<T>, dim3((unsigned)grams), dim3(NS_T), 0, s, g, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ns_join_kernel, dim3((unsigned)sq.start[l.count]), dim3(NS_T), 0, s, sq, c.eps, ws, ws);
+    hipLaunchKernelGGL(ns_join_kernel, dim3((unsigned)joins), dim3(NS_T), 0, s, sq, c.eps, ws, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
-    RoundArgs r{};
-    r.s = sq;
-    r.a = c.a;
-    r.b = c.b;
-    r.c = c.c;
-    // small matrices: many small tiles; large ones: tiles that read less
-    const int edge = maxm <= 256 ? 16 : 32;
-    auto round = [&](std::initializer_list<Product> ps) -> hipError_t {
-        r.np = 0;
-        for (const Product& x : ps) r.p[r.np++] = x;
-        r.s.start[0] = 0;
-        for (int i = 0; i < l.count; ++i) {
-            const int nt = (l.m[i] + edge - 1) / edge;
-            r.s.start[i + 1] = r.s.start[i] + r.np * (nt * (nt + 1) / 2);
-        }
-        const dim3 grid((unsigned)r.s.start[l.count]);
-        if (edge == 16) hipLaunchKernelGGL(ns_round_kernel<1>, grid, dim3(NS_T), 0, s, r, ws);
-        else hipLaunchKernelGGL(ns_round_kernel<2>, grid, dim3(NS_T), 0, s, r, ws);
-        return hipGetLastError();
-    };
     int A = 0, T_ = 1, P = 2, Q = 3, R = 4;      // buffers: A_k, P A, P_k, Q and a free one
-    for (int k = 0; k < c.steps; ++k) {
-        const bool last = k + 1 == c.steps;
-        if ((e = round({{A, A, P, 1}})) != hipSuccess) return e;
-        if (k == 0) {
-            std::swap(P, Q);                      // Q = P_0
-            if (!last && (e = round({{Q, A, T_, 0}})) != hipSuccess) return e;
-            if (!last && (e = round({{T_, Q, A, 0}})) != hipSuccess) return e;
-            continue;
+    if (maxm <= NB_M) {
+        hipLaunchKernelGGL((ns_block_kernel<false, T, F>), dim3((unsigned)l.count), dim3(NB_T), 0, s, k, f, ws);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        Q = 1;
+    } else {
+        RoundArgs r{};
+        r.s = sq;
+        r.a = c.a;
+        r.b = c.b;
+        r.c = c.c;
+        // small matrices: many small tiles; large ones: tiles that read less
+        const int edge = maxm <= 256 ? 16 : 32;
+        auto round = [&](std::initializer_list<Product> ps) -> hipError_t {
+            r.np = 0;
+            for (const Product& x : ps) r.p[r.np++] = x;
+            int blocks = 0;
+            for (int i = 0; i < l.count; ++i) {
+                const int nt = (l.m[i] + edge - 1) / edge;
+                r.s.start.set(i, blocks);
+                blocks += r.np * (nt * (nt + 1) / 2);
+            }
+            if (edge == 16) hipLaunchKernelGGL(ns_round_kernel<1>, dim3((unsigned)blocks), dim3(NS_T), 0, s, r, ws);
+            else hipLaunchKernelGGL(ns_round_kernel<2>, dim3((unsigned)blocks), dim3(NS_T), 0, s, r, ws);
+            return hipGetLastError();
+        };
+        for (int i = 0; i < c.steps; ++i) {
+            const bool last = i + 1 == c.steps;
+            if (i == 0) {
+                if ((e = round({{A, A, Q, 1, last}})) != hipSuccess) return e;      // Q = P_0
+                if (!last && (e = round({{Q, A, T_, 0, 0}})) != hipSuccess) return e;
+                if (!last && (e = round({{T_, Q, A, 0, 0}})) != hipSuccess) return e;
+                continue;
+            }
+            if ((e = round({{A, A, P, 1, 0}})) != hipSuccess) return e;
+            if (last) e = round({{P, Q, R, 0, 1}});
+            else e = round({{P, A, T_, 0, 0}, {P, Q, R, 0, 0}});
+            if (e != hipSuccess) return e;
+            std::swap(Q, R);
+            if (!last && (e = round({{T_, P, A, 0, 0}})) != hipSuccess) return e;
         }
-        if (last) e = round({{P, Q, R, 0}});
-        else e = round({{P, A, T_, 0}, {P, Q, R, 0}});
-        if (e != hipSuccess) return e;
-        std::swap(Q, R);
-        if (!last && (e = round({{T_, P, A, 0}})) != hipSuccess) return e;
     }
-    *q = Q;
-    return hipSuccess;
-}
-
-template <typename T, typename F>
-hipError_t ns_final(const NsShapes& l, const NsPlan& p, const void* const* u, int q, const F& f, const double* ws,
-                    hipStream_t s)
-{
-    FinalArgs a{};
-    a.count = l.count;
-    a.tall = l.tall;
-    for (int i = 0; i < l.count; ++i) {
-        const int64_t ld = ns_ld(l.m[i]);
-        a.u[i] = u[i];
-        a.m[i] = l.m[i];
-        a.n[i] = l.n[i];
-        a.q[i] = p.sq[i] + q * ld * ld;
-        a.start[i + 1] = a.start[i] + (int)(ld / NS_TILE) * ((l.n[i] + NS_TILE - 1) / NS_TILE);
-    }
-    hipLaunchKernelGGL((ns_final_kernel<T, F>), dim3((unsigned)a.start[l.count]), dim3(NS_T), 0, s, a, f, ws, ws);
+    for (int i = 0; i < l.count; ++i) a.q[i] = p.sq[i] + Q * ns_size(l.m[i]);
+    hipLaunchKernelGGL((ns_final_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
     return hipGetLastError();
 }
-
-}  // namespace
-
-namespace {
 
 // The matrices of a list that take the fp64 launches together, and those that
 // take split products one after another.
@@ -644,10 +956,7 @@ hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* 
         u[i] = x[p.f64_at[i]];
         f.out[i] = out[p.f64_at[i]];
     }
-    const NsPlan pl = ns_plan(p.f64);
-    int q = 0;
-    if ((e = ns_iterate<T>(p.f64, pl, u, c, (double*)ws, &q, s)) != hipSuccess) return e;
-    return ns_final<T>(p.f64, pl, u, q, f, (const double*)ws, s);
+    return ns_f64<T>(p.f64, u, c, f, (double*)ws, s);
 }
 
 size_t muon_ws_bytes(const NsShapes& l, bool nesterov)
@@ -664,8 +973,10 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
     MomentumArgs a{};
     const float* u[CF_MAX_OPT_TENSORS];
     char* at = (char*)ws + ns_ws_bytes(l);
-    a.count = l.count;
+    a.start.clear();
+    int blocks = 0;
     for (int i = 0; i < l.count; ++i) {
+        a.start.set(i, blocks);
         a.n[i] = (int64_t)l.m[i] * l.n[i];
         a.g[i] = g[i];
         a.m[i] = m[i];
@@ -675,9 +986,9 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
             u[i] = a.u[i];
             at += up256b((size_t)a.n[i] * sizeof(float));
         }
-        a.start[i + 1] = a.start[i] + (int)((a.n[i] + MU_CHUNK - 1) / MU_CHUNK);
+        blocks += (int)((a.n[i] + MU_CHUNK - 1) / MU_CHUNK);
     }
-    hipLaunchKernelGGL(muon_momentum_kernel, dim3((unsigned)a.start[l.count]), dim3(NS_T), 0, s, a, h.momentum,
+    hipLaunchKernelGGL(muon_momentum_kernel, dim3((unsigned)blocks), dim3(NS_T), 0, s, a, h.momentum,
                        (int)h.nesterov);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -697,10 +1008,7 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
         f.w[i] = w[p.f64_at[i]];
         f.rate[i] = h.rate[p.f64_at[i]];
     }
-    const NsPlan pl = ns_plan(p.f64);
-    int q = 0;
-    if ((e = ns_iterate<float>(p.f64, pl, v, c, (double*)ws, &q, s)) != hipSuccess) return e;
-    return ns_final<float>(p.f64, pl, v, q, f, (const double*)ws, s);
+    return ns_f64<float>(p.f64, v, c, f, (double*)ws, s);
 }
 
 template hipError_t launch_newton_schulz<float>(const NsShapes&, const NsCoef&, const void* const*, void* const*,

@@ -56,6 +56,9 @@ constexpr int SP_PART = SP_TILE * SP_TILE;      // floats of a tile's partial su
 
 size_t up256b(size_t b) { return (b + 255) & ~(size_t)255; }
 __host__ __device__ inline int pieces(int k) { return (k + SP_K - 1) / SP_K; }
+// Lines from one row to the next: an odd number, or the rows of a piece would
+// share few memory channels.
+__host__ __device__ inline int row_lines(int kb) { return kb | 1; }
 
 // ---------------------------------------------------------------- epilogues
 // What becomes of element (i, j) of the product C, i < m, j < n.
@@ -124,29 +127,34 @@ __device__ __forceinline__ void sp_put(const float* sh, bool flip, const SpProdu
 {
     const int lane = (int)threadIdx.x & 63, chunk = lane & 7, k8 = (chunk & 3) * 8;
     if (c0 >= kd * SP_K) return;
+    auto line = [&](int it) {
+        return ((int64_t)min(r0 + it * 8 + lane / 8, rows - 1) * row_lines(kd) + c0 / SP_K) * 64;
+    };
+    f16x8 hi[4], lo[4], o[4];
+    if (MODE == SP_POLY)
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            hi[it] = *reinterpret_cast<const f16x8*>(q.s + line(it) + k8);
+            lo[it] = *reinterpret_cast<const f16x8*>(q.s + line(it) + 32 + k8);
+        }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int r = it * 8 + lane / 8;
-        if (r0 + r >= rows) continue;
-        const int64_t line = ((int64_t)(r0 + r) * kd + c0 / SP_K) * 64;
-        f16x8 hi = {}, lo = {}, o;
-        if (MODE == SP_POLY) {
-            hi = *reinterpret_cast<const f16x8*>(q.s + line + k8);
-            lo = *reinterpret_cast<const f16x8*>(q.s + line + 32 + k8);
-        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float v = q.f * (flip ? sh[(k8 + j) * SP_SB + r] : sh[r * SP_SB + k8 + j]);
             if (MODE == SP_POLY) {
-                v = fmaf(q.g, (float)hi[j] + (float)lo[j], v);
+                v = fmaf(q.g, (float)hi[it][j] + (float)lo[it][j], v);
                 if (r0 + r == c0 + k8 + j) v += q.diag;
             }
             if (c0 + k8 + j >= cols) v = 0.f;
             const _Float16 h = (_Float16)v;
-            o[j] = chunk < 4 ? h : (_Float16)(v - (float)h);
+            o[it][j] = chunk < 4 ? h : (_Float16)(v - (float)h);
         }
-        *reinterpret_cast<f16x8*>(d + line + chunk * 8) = o;
     }
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+        if (r0 + it * 8 + lane / 8 < rows) *reinterpret_cast<f16x8*>(d + line(it) + chunk * 8) = o[it];
 }
 
 // The caller's row-major matrix, [m][n] or (tall) [n][m].
@@ -157,14 +165,18 @@ struct SpApply {
     float* w;
     float keep, rate;
 };
-template <typename T> __device__ __forceinline__ void sp_finish(const SpStore& a, int64_t i, float o)
+// Done in three passes over a block's elements: loads, results, stores.  The
+// compiler may not move a load past a store, and a wait for a load between
+// stores would wait for the stores too.
+__device__ __forceinline__ float sp_before(const SpStore&, int64_t) { return 0.f; }
+__device__ __forceinline__ float sp_before(const SpApply& a, int64_t i) { return a.w[i]; }
+__device__ __forceinline__ float sp_result(const SpStore&, float o, float) { return o; }
+__device__ __forceinline__ float sp_result(const SpApply& a, float o, float w) { return fmaf(-a.rate, o, w * a.keep); }
+template <typename T> __device__ __forceinline__ void sp_finish(const SpStore& a, int64_t i, float v)
 {
-    Elem<T>::store((T*)a.out, i, o);
+    Elem<T>::store((T*)a.out, i, v);
 }
-template <typename T> __device__ __forceinline__ void sp_finish(const SpApply& a, int64_t i, float o)
-{
-    a.w[i] = fmaf(-a.rate, o, a.w[i] * a.keep);
-}
+template <typename T> __device__ __forceinline__ void sp_finish(const SpApply& a, int64_t i, float v) { a.w[i] = v; }
 struct SpNone {};
 template <typename T, typename F> struct SpFinal {
     F f;
@@ -192,12 +204,22 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
     } else {
         const int c = lane % 32, x0 = fin.tall ? j0 : i0, y0 = fin.tall ? i0 : j0;
         const int rows = fin.tall ? q.n : q.m, cols = fin.tall ? q.m : q.n;
+        float w[16];
+#pragma unroll
+        for (int it = 0; it < 16; ++it) {
+            const int x = min(x0 + it * 2 + lane / 32, rows - 1), y = min(y0 + c, cols - 1);
+            w[it] = sp_before(fin.f, (int64_t)x * cols + y);
+        }
 #pragma unroll
         for (int it = 0; it < 16; ++it) {
             const int r = it * 2 + lane / 32;
-            if (x0 + r < rows && y0 + c < cols)
-                sp_finish<T>(fin.f, (int64_t)(x0 + r) * cols + y0 + c,
-                             q.f * (fin.tall ? sh[c * SP_SB + r] : sh[r * SP_SB + c]));
+            w[it] = sp_result(fin.f, q.f * (fin.tall ? sh[c * SP_SB + r] : sh[r * SP_SB + c]), w[it]);
+            asm volatile("" : "+v"(w[it]));      // computed before the stores
+        }
+#pragma unroll
+        for (int it = 0; it < 16; ++it) {
+            const int r = it * 2 + lane / 32;
+            if (x0 + r < rows && y0 + c < cols) sp_finish<T>(fin.f, (int64_t)(x0 + r) * cols + y0 + c, w[it]);
         }
     }
     sp_wave_sync();
@@ -318,7 +340,7 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
     __shared__ uint4 s3[S::STAGES > 2 ? S::CHUNKS : 1];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int b = (int)xcd_remap(blockIdx.x, (uint32_t)q.grid);
-    const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)q.kb * 128;      // bytes of a row
+    const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)row_lines(q.kb) * 128;      // bytes from row to row
     uint32_t off[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -338,7 +360,7 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
         auto load = [&](uint4* stage) {
             sp_load<TILE>(stage, src, off, ld);
             const bool wrap = piece + 1 == q.kb, more = --left > 0;
-            const int64_t step = more ? 128 - (wrap ? ld : 0) : 0;
+            const int64_t step = more ? 128 - (wrap ? (int64_t)q.kb * 128 : 0) : 0;
             piece = wrap ? 0 : piece + 1;
             src[0] += step;
             src[1] += step;
@@ -467,7 +489,7 @@ __global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int ti, tj;
     sp_tile_at(q, (int)xcd_remap(blockIdx.x, gridDim.x), ti, tj);
-    const int64_t ld = (int64_t)q.kb * 128;
+    const int64_t ld = (int64_t)row_lines(q.kb) * 128;
     uint32_t off[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -786,11 +808,11 @@ SpLayout sp_layout(int m, int n)
         return r;
     };
     l.norm = take(SP_NORM * sizeof(double));
-    l.x = take(rows(m) * pieces(n) * 128);
-    l.xt[0] = take(rows(n) * pieces(m) * 128);
-    l.xt[1] = take(rows(n) * pieces(m) * 128);
-    l.a = take(rows(m) * pieces(m) * 128);
-    l.p = take(rows(m) * pieces(m) * 128);
+    l.x = take(rows(m) * row_lines(pieces(n)) * 128);
+    l.xt[0] = take(rows(n) * row_lines(pieces(m)) * 128);
+    l.xt[1] = take(rows(n) * row_lines(pieces(m)) * 128);
+    l.a = take(rows(m) * row_lines(pieces(m)) * 128);
+    l.p = take(rows(m) * row_lines(pieces(m)) * 128);
     l.part = take((size_t)2 * SP_GRID * SP_PART * sizeof(float));
     l.bytes = at;
     return l;
