@@ -177,12 +177,19 @@ def dtype_code(t: torch.dtype) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# (torch.cuda.current_stream builds a Stream object, which takes longer than a small kernel's launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def dims(shape) -> cf_dims:
@@ -592,18 +599,16 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
                      stream=None):
     """Group norm of NDHWC X, then the activation -> (Y, mean [N, groups],
     rstd [N, groups])."""
-    dt = dtype_code(X.dtype)
-    N, C = int(X.shape[0]), int(X.shape[4])
+    dt, d, groups = dtype_code(X.dtype), dims(X.shape), int(groups)
     _packed("X", X)
-    _packed("gamma", gamma, torch.float32, (C,))
-    _packed("beta", beta, torch.float32, (C,))
+    _packed("gamma", gamma, torch.float32, (d.c,))
+    _packed("beta", beta, torch.float32, (d.c,))
     Y = torch.empty_like(X) if Y is None else Y
-    mean = torch.empty((N, int(groups)), dtype=torch.float32, device=X.device) if mean is None else mean
-    rstd = torch.empty((N, int(groups)), dtype=torch.float32, device=X.device) if rstd is None else rstd
-    ws = _ws(cf_groupnorm_workspace_size(dt, X.shape, groups, False), X.device, ws)
-    check(lib().cf_groupnorm_fwd(dt, dims(X.shape), _ptr(X), int(groups), _ptr(gamma), _ptr(beta), float(eps),
-                                 int(act), float(slope), _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws),
-                                 _stream(stream)))
+    mean = gamma.new_empty((d.n, groups)) if mean is None else mean
+    rstd = gamma.new_empty((d.n, groups)) if rstd is None else rstd
+    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
+    check(lib().cf_groupnorm_fwd(dt, d, _ptr(X), groups, _ptr(gamma), _ptr(beta), float(eps), int(act), float(slope),
+                                 _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), _stream(stream)))
     _record(stream, Y, mean, rstd, ws)
     return Y, mean, rstd
 
@@ -611,21 +616,19 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
 def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, slope=1.0, dX=None, ws=None,
                      stream=None):
     """-> (dX, dgamma, dbeta) from the forward's mean and rstd."""
-    dt = dtype_code(X.dtype)
-    N, C = int(X.shape[0]), int(X.shape[4])
+    dt, d, groups = dtype_code(X.dtype), dims(X.shape), int(groups)
     _packed("X", X)
     _packed("dY", dY, X.dtype, X.shape)
-    _packed("gamma", gamma, torch.float32, (C,))
-    _packed("beta", beta, torch.float32, (C,))
-    _packed("mean", mean, torch.float32, (N, int(groups)))
-    _packed("rstd", rstd, torch.float32, (N, int(groups)))
+    _packed("gamma", gamma, torch.float32, (d.c,))
+    _packed("beta", beta, torch.float32, (d.c,))
+    _packed("mean", mean, torch.float32, (d.n, groups))
+    _packed("rstd", rstd, torch.float32, (d.n, groups))
     dX = torch.empty_like(X) if dX is None else dX
-    dgamma = torch.empty((C,), dtype=torch.float32, device=X.device)
-    dbeta = torch.empty((C,), dtype=torch.float32, device=X.device)
-    ws = _ws(cf_groupnorm_workspace_size(dt, X.shape, groups, True), X.device, ws)
-    check(lib().cf_groupnorm_bwd(dt, dims(X.shape), _ptr(X), _ptr(dY), int(groups), _ptr(gamma), _ptr(beta),
-                                 _ptr(mean), _ptr(rstd), int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta),
-                                 _ptr(ws), _wsbytes(ws), _stream(stream)))
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
+    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
+    check(lib().cf_groupnorm_bwd(dt, d, _ptr(X), _ptr(dY), groups, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
+                                 int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws),
+                                 _stream(stream)))
     _record(stream, dX, dgamma, dbeta, ws)
     return dX, dgamma, dbeta
 

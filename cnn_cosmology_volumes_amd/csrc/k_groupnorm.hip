@@ -43,6 +43,7 @@ constexpr int GN_TS = 1024;      // most threads of a small-group block
 constexpr int GN_ROWS_F = 8;     // vectors per thread held by the small forward
 constexpr int GN_ROWS_B = 4;     // and by the small backward (of x and dy each)
 constexpr size_t GN_LDS = 65536; // most LDS of a small-group block
+constexpr int GN_SLICES = 64;    // blocks per sample from which slices of more groups are taken
 constexpr int GN_BLOCKS = 1024;  // streaming blocks per launch, about 4 per CU
 
 // V values of T as one 16-byte access (V = 1: one element).
@@ -84,43 +85,87 @@ struct GnGeom {
     int nb;          // blocks per sample and chunk
 };
 
-// First stage of a block's sums.  Thread t < k * cc holds in v[j] a partial
-// sum of row position t % cc * V + j, of W = cc * V positions.  Afterwards
-// sh[i * W + p] for i < the returned count hold position p's total in that
-// many parts.  sh: k * W doubles.
-template <int V>
-__device__ __forceinline__ int sum_rows(const double (&v)[V], double* sh, int k, int cc)
+// A block's sums.  Thread t < n = k * cc holds in v[j] a partial sum of row
+// position t % cc * V + j; 2^lh neighbouring positions that go to the same sum
+// are added first, leaving positions p of V >> lh planes a thread.  In LDS a
+// plane's values lie thread by thread, so that neighbouring lanes use
+// neighbouring banks.
+struct RowSums {
+    const double* sh;
+    int lg, n, cc, parts;      // log2 of the planes, values of a plane, vectors, partial sums left of a position
+    __device__ __forceinline__ double at(int p, int i) const
+    {
+        return sh[(p & ((1 << lg) - 1)) * n + i * cc + (p >> lg)];
+    }
+    // Position p's total.
+    __device__ __forceinline__ double total(int p) const
+    {
+        double a = 0.0;
+        for (int i = 0; i < parts; ++i) a += at(p, i);
+        return a;
+    }
+};
+
+template <int V> __device__ __forceinline__ void put_rows(const double (&v)[V], double* sh, int n, int lh)
 {
-    const int W = cc * V, t = (int)threadIdx.x, T = (int)blockDim.x;
-    const int parts = max(1, min(k, T / W));
-    __syncthreads();             // the previous sums have been read
-    if (t < k * cc) {
+    const int t = (int)threadIdx.x;
+    if (t >= n) return;
+    double w[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) sh[t * V + j] = v[j];
-    }
-    __syncthreads();
-    for (int e = t; e < parts * W; e += T) {
-        double a = sh[e];
-        for (int i = e + parts * W; i < k * W; i += parts * W) a += sh[i];
-        sh[e] = a;
-    }
+    for (int j = 0; j < V; ++j) w[j] = v[j];
+#pragma unroll
+    for (int l = 0; (1 << l) < V; ++l)
+        if (lh > l)
+#pragma unroll
+            for (int j = 0; j + (1 << l) < V; j += 2 << l) w[j] += w[j + (1 << l)];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if ((j & ((1 << lh) - 1)) == 0) sh[(j >> lh) * n + t] = w[j];
+}
+
+// Adds the k rows of each plane in levels, each with as many threads as it can
+// use, until at most 8 partial sums of a position are left; returns how many.
+__device__ __forceinline__ int fold_rows(double* sh, int planes, int k, int cc)
+{
+    const int t = (int)threadIdx.x, T = (int)blockDim.x, n = k * cc;
+    int parts = k;
+    do {
+        const int next = max(1, min((parts + 3) / 4, T / (planes * cc))), m = next * cc;
+        __syncthreads();
+        for (int e = t; e < planes * m; e += T) {
+            const int j = e / m, x = e - j * m;
+            double* q = sh + j * n + x;
+            double a = q[0];
+            for (int i = m; x + i < parts * cc; i += m) a += q[i];
+            q[0] = a;
+        }
+        parts = next;
+    } while (parts > 8);
     __syncthreads();
     return parts;
 }
 
-// Total over the row positions p0 <= p < p0 + W whose channel (p mod C) lies
-// in group g, from sum_rows' result; one wave, returned in every lane.
-__device__ __forceinline__ double group_total(const double* sh, int parts, int W, int p0, int g, int cg, int C,
-                                              int row)
+// Total over the positions p0 <= p < p0 + W of a row whose channel (p mod C)
+// lies in group g; one wave, returned in every lane.
+__device__ __forceinline__ double group_total(const RowSums& r, int W, int p0, int g, int cg, int C, int row)
 {
-    const int n = row / C * cg;
+    const int lane = (int)(threadIdx.x & 63);
+    int lc = 0;                                    // lanes: 2^lc channels x the partial sums
+    while (lc < 6 && (1 << lc) < cg) ++lc;
     double a = 0.0;
-    for (int e = (int)(threadIdx.x & 63); e < n * parts; e += 64) {
-        const int i = e / n, f = e - i * n;
-        const int p = f / cg * C + g * cg + f % cg - p0;
-        if (p >= 0 && p < W) a += sh[i * W + p];
-    }
+    for (int c0 = g * cg - p0; c0 < row - p0 && c0 < W; c0 += C)
+        for (int f = lane & ((1 << lc) - 1); f < cg; f += 1 << lc)
+            if (c0 + f >= 0 && c0 + f < W)
+                for (int i = lane >> lc; i < r.parts; i += 64 >> lc) a += r.at(c0 + f, i);
     return wave_sum(a);
+}
+
+// log2 of the positions of V neighbouring ones that always lie in one group.
+__host__ __device__ __forceinline__ int same_group(int cg, int V)
+{
+    int l = 0;
+    while ((2 << l) <= V && cg % (2 << l) == 0) ++l;
+    return l;
 }
 
 // Mean and 1 / sqrt(var + eps) from fp64 sums of x and x^2 over M values.
@@ -131,6 +176,22 @@ __device__ __forceinline__ float2 moments(double s, double ss, double M, float e
     if (var < 0.0) var = 0.0;
     return make_float2((float)mu, (float)(1.0 / sqrt(var + (double)eps)));
 }
+
+// The channel and group of neighbouring row positions, without a division
+// for each.
+struct Channel {
+    int c, g, r;      // channel, its group, its place in the group
+    __device__ __forceinline__ Channel(int position, int C, int cg) : c(position % C), g(c / cg), r(c - g * cg) {}
+    __device__ __forceinline__ void next(int C, int cg)
+    {
+        ++c;
+        if (++r == cg) {
+            r = 0;
+            ++g;
+        }
+        if (c == C) c = g = 0;
+    }
+};
 
 // ------------------------------------------------------------- activation
 template <int ACT> __device__ __forceinline__ float act_fwd(float z, float slope)
@@ -159,7 +220,7 @@ __device__ __forceinline__ float act_bwd(float dy, float x, float mu, float rs, 
 }
 
 // -------------------------------------------------------- streaming forward
-// Partial sums of x and x^2: part[n][block][chunk][group] = (sum, squares).
+// Partial sums of x and x^2: part[n][group][block][chunk] = (sum, squares).
 template <typename T, int V>
 __global__ __launch_bounds__(GN_T) void gn_stats_kernel(const T* __restrict__ X, GnGeom q, double2* __restrict__ part)
 {
@@ -196,17 +257,19 @@ __global__ __launch_bounds__(GN_T) void gn_stats_kernel(const T* __restrict__ X,
                 if (j < left) add1(j, x[q.nrows * q.row + j]);
         }
     }
-    const int p0 = (int)blockIdx.y * q.cc * V, W = q.cc * V;
-    double2* out = part + (((int64_t)blockIdx.z * q.nb + blockIdx.x) * q.chunks + blockIdx.y) * q.G;
-    int parts = sum_rows<V>(s, sh, q.k, q.cc);
+    const int lh = same_group(q.cg, V), nv = V >> lh, n = q.k * q.cc;
+    put_rows<V>(s, sh, n, lh);
+    put_rows<V>(ss, sh + nv * n, n, lh);
+    RowSums a{sh, 31 - __builtin_clz(nv), n, q.cc, fold_rows(sh, 2 * nv, q.k, q.cc)};
+    RowSums b = a;
+    b.sh += nv * n;
+    const int npart = q.nb * q.chunks;
+    double2* out = part + (int64_t)blockIdx.z * q.G * npart + (int64_t)blockIdx.x * q.chunks + blockIdx.y;
     for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
-        const double a = group_total(sh, parts, W, p0, g, q.cg, q.C, q.row);
-        if ((t & 63) == 0) out[g].x = a;
-    }
-    parts = sum_rows<V>(ss, sh, q.k, q.cc);
-    for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
-        const double a = group_total(sh, parts, W, p0, g, q.cg, q.C, q.row);
-        if ((t & 63) == 0) out[g].y = a;
+        const int W = q.cc * nv, p0 = (int)blockIdx.y * W;
+        const double x = group_total(a, W, p0, g, q.cg >> lh, q.C >> lh, q.row >> lh);
+        const double y = group_total(b, W, p0, g, q.cg >> lh, q.C >> lh, q.row >> lh);
+        if ((t & 63) == 0) out[(int64_t)g * npart] = make_double2(x, y);
     }
 }
 
@@ -222,11 +285,36 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
 {
     extern __shared__ float2 stat[];     // [G] mean, rstd
     const int t = (int)threadIdx.x, n = (int)blockIdx.z;
+    const int r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
+    const bool on = r < q.k && col < q.cols;
+    const int64_t at = (int64_t)n * q.S + (int64_t)col * V, step = (int64_t)q.nb * q.k;
+    const T* x = X + at;
+    T* y = Y + at;
+    // the first rows are on their way while the sums are added
+    Vec<T, V> u[4];
+    auto load = [&](int64_t i) {
+#pragma unroll
+        for (int l = 0; l < 4; ++l) u[l] = vload<T, V>(x + min(i + l * step, q.nrows - 1) * q.row);
+    };
+    int64_t i = (int64_t)blockIdx.x * q.k + r;
+    if (on && i < q.nrows) load(i);
     part += (int64_t)n * npart * q.G;
     for (int g = t >> 6; g < q.G; g += (int)blockDim.x >> 6) {
         double s = 0.0, ss = 0.0;
-        for (int b = t & 63; b < npart; b += 64) {
-            const double2 v = part[(int64_t)b * q.G + g];
+        const double2* in = part + (int64_t)g * npart;
+        int b = t & 63;
+        for (; b + 192 < npart; b += 256) {
+            double2 v[4];
+#pragma unroll
+            for (int l = 0; l < 4; ++l) v[l] = in[b + 64 * l];
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                s += v[l].x;
+                ss += v[l].y;
+            }
+        }
+        for (; b < npart; b += 64) {
+            const double2 v = in[b];
             s += v.x;
             ss += v.y;
         }
@@ -242,20 +330,17 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
         }
     }
     __syncthreads();
-    const int r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
-    if (r >= q.k || col >= q.cols) return;
+    if (!on) return;
     float mu[V], sc[V], be[V];
+    Channel ch(col * V, q.C, q.cg);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = (col * V + j) % q.C;
-        const float2 m = stat[c / q.cg];
+        const float2 m = stat[ch.g];
         mu[j] = m.x;
-        sc[j] = m.y * gamma[c];
-        be[j] = beta[c];
+        sc[j] = m.y * gamma[ch.c];
+        be[j] = beta[ch.c];
+        ch.next(q.C, q.cg);
     }
-    const int64_t at = (int64_t)n * q.S + (int64_t)col * V;
-    const T* x = X + at;
-    T* y = Y + at;
     auto out1 = [&](int j, T w) { return act_fwd<ACT>(fmaf(wide(w) - mu[j], sc[j], be[j]), slope); };
     auto out = [&](const Vec<T, V>& u, int64_t i) {
         Vec<T, V> o;
@@ -263,16 +348,17 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
         for (int j = 0; j < V; ++j) narrow(o.v[j], out1(j, u.v[j]));
         vstore<T, V>(y + i * q.row, o);
     };
-    const int64_t step = (int64_t)q.nb * q.k;
-    int64_t i = (int64_t)blockIdx.x * q.k + r;
     for (; i + 3 * step < q.nrows; i += 4 * step) {
-        Vec<T, V> u[4];
+        Vec<T, V> v[4];
 #pragma unroll
-        for (int l = 0; l < 4; ++l) u[l] = vload<T, V>(x + (i + l * step) * q.row);
+        for (int l = 0; l < 4; ++l) v[l] = u[l];
+        if (i + 4 * step < q.nrows) load(i + 4 * step);
 #pragma unroll
-        for (int l = 0; l < 4; ++l) out(u[l], i + l * step);
+        for (int l = 0; l < 4; ++l) out(v[l], i + l * step);
     }
-    for (; i < q.nrows; i += step) out(vload<T, V>(x + i * q.row), i);
+#pragma unroll
+    for (int l = 0; l < 3; ++l)
+        if (i + l * step < q.nrows) out(u[l], i + l * step);
     if (blockIdx.x == 0 && r == 0) {
         const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
 #pragma unroll
@@ -299,14 +385,15 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_sums_kernel(const T* __restrict__
     double a[V] = {}, b[V] = {};
     if (r < q.k && col < q.cols) {
         float mu[V], rs[V], ga[V], be[V];
+        Channel ch(col * V, q.C, q.cg);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = (col * V + j) % q.C;
-            const int64_t g = (int64_t)blockIdx.z * q.G + c / q.cg;
+            const int64_t g = (int64_t)blockIdx.z * q.G + ch.g;
             mu[j] = mean[g];
             rs[j] = rstd[g];
-            ga[j] = gamma[c];
-            be[j] = beta[c];
+            ga[j] = gamma[ch.c];
+            be[j] = beta[ch.c];
+            ch.next(q.C, q.cg);
         }
         auto add1 = [&](int j, T xw, T dw) {
             const float xv = wide(xw), xhat = (xv - mu[j]) * rs[j];
@@ -328,7 +415,7 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_sums_kernel(const T* __restrict__
 #pragma unroll
                 for (int j = 0; j < V; ++j) add1(j, u[l].v[j], d[l].v[j]);
         }
-        for (; i < q.nrows; i += step) {
+        if (i < q.nrows) {
             const Vec<T, V> u = vload<T, V>(x + i * q.row), d = vload<T, V>(dy + i * q.row);
 #pragma unroll
             for (int j = 0; j < V; ++j) add1(j, u.v[j], d.v[j]);
@@ -340,19 +427,22 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_sums_kernel(const T* __restrict__
                 if (j < left) add1(j, x[q.nrows * q.row + j], dy[q.nrows * q.row + j]);
         }
     }
-    const int p0 = (int)blockIdx.y * q.cc * V, W = q.cc * V;
+    const int n = q.k * q.cc, p0 = (int)blockIdx.y * q.cc * V, W = q.cc * V;
+    put_rows<V>(a, sh, n, 0);
+    put_rows<V>(b, sh + V * n, n, 0);
+    RowSums ra{sh, 31 - __builtin_clz(V), n, q.cc, fold_rows(sh, 2 * V, q.k, q.cc)};
+    RowSums rb = ra;
+    rb.sh += V * n;
     double2* out = part + (((int64_t)blockIdx.z * q.nb + blockIdx.x) * q.chunks + blockIdx.y) * q.C;
-    auto channel = [&](int c, int parts) {
-        double v = 0.0;
+    for (int c = t; c < q.C; c += (int)blockDim.x) {
+        double x = 0.0, y = 0.0;
         for (int p = c - p0; p < W && p < q.row - p0; p += q.C)
-            if (p >= 0)
-                for (int i = 0; i < parts; ++i) v += sh[i * W + p];
-        return v;
-    };
-    int parts = sum_rows<V>(a, sh, q.k, q.cc);
-    for (int c = t; c < q.C; c += (int)blockDim.x) out[c].x = channel(c, parts);
-    parts = sum_rows<V>(b, sh, q.k, q.cc);
-    for (int c = t; c < q.C; c += (int)blockDim.x) out[c].y = channel(c, parts);
+            if (p >= 0) {
+                x += ra.total(p);
+                y += rb.total(p);
+            }
+        out[c] = make_double2(x, y);
+    }
 }
 
 // One block per (group, sample): the blocks' partials to per-sample channel
@@ -371,12 +461,24 @@ __global__ __launch_bounds__(GN_TJ) void gn_bwd_join_kernel(GnGeom q, int npart,
         const int i = t % cw, way = t / cw, c = g * q.cg + c0 + i;
         const bool on = way < ways && c0 + i < q.cg;
         double a = 0.0, b = 0.0;
-        if (on)
-            for (int p = way; p < npart; p += ways) {
+        if (on) {
+            int p = way;
+            for (; p + 7 * ways < npart; p += 8 * ways) {      // eight loads in flight
+                double2 v[8];
+#pragma unroll
+                for (int l = 0; l < 8; ++l) v[l] = part[(int64_t)(p + l * ways) * q.C + c];
+#pragma unroll
+                for (int l = 0; l < 8; ++l) {
+                    a += v[l].x;
+                    b += v[l].y;
+                }
+            }
+            for (; p < npart; p += ways) {
                 const double2 v = part[(int64_t)p * q.C + c];
                 a += v.x;
                 b += v.y;
             }
+        }
         __syncthreads();
         la[t] = a;
         lb[t] = b;
@@ -433,22 +535,23 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_apply_kernel(const T* __restrict_
             dgamma[c] = (float)b;
         }
     if (r >= q.k || col >= q.cols) return;
-    float mu[V], rs[V], ga[V], be[V], s1[V], s2[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = (col * V + j) % q.C;
-        const int64_t g = (int64_t)blockIdx.z * q.G + c / q.cg;
-        mu[j] = mean[g];
-        rs[j] = rstd[g];
-        ga[j] = gamma[c];
-        be[j] = beta[c];
-        s1[j] = s12[g].x;
-        s2[j] = s12[g].y;
-    }
-    const int64_t at = (int64_t)blockIdx.z * q.S + (int64_t)col * V;
+    const int64_t at = (int64_t)blockIdx.z * q.S + (int64_t)col * V, step = (int64_t)q.nb * q.k;
     const T* x = X + at;
     const T* dy = dY + at;
     T* dx = dX + at;
+    float mu[V], rs[V], ga[V], be[V], s1[V], s2[V];
+    Channel ch(col * V, q.C, q.cg);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t g = (int64_t)blockIdx.z * q.G + ch.g;
+        mu[j] = mean[g];
+        rs[j] = rstd[g];
+        ga[j] = gamma[ch.c];
+        be[j] = beta[ch.c];
+        s1[j] = s12[g].x;
+        s2[j] = s12[g].y;
+        ch.next(q.C, q.cg);
+    }
     auto out1 = [&](int j, T xw, T dw) {
         const float xv = wide(xw), xhat = (xv - mu[j]) * rs[j];
         const float dz = act_bwd<ACT>(wide(dw), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
@@ -460,7 +563,6 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_apply_kernel(const T* __restrict_
         for (int j = 0; j < V; ++j) narrow(o.v[j], out1(j, u.v[j], d.v[j]));
         vstore<T, V>(dx + i * q.row, o);
     };
-    const int64_t step = (int64_t)q.nb * q.k;
     int64_t i = (int64_t)blockIdx.x * q.k + r;
     for (; i + step < q.nrows; i += 2 * step) {
         Vec<T, V> u[2], d[2];
@@ -472,7 +574,7 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_apply_kernel(const T* __restrict_
 #pragma unroll
         for (int l = 0; l < 2; ++l) out(u[l], d[l], i + l * step);
     }
-    for (; i < q.nrows; i += step) out(vload<T, V>(x + i * q.row), vload<T, V>(dy + i * q.row), i);
+    if (i < q.nrows) out(vload<T, V>(x + i * q.row), vload<T, V>(dy + i * q.row), i);
     if (blockIdx.x == 0 && r == 0) {
         const int64_t left = q.S - q.nrows * q.row - (int64_t)col * V;
 #pragma unroll
@@ -494,7 +596,7 @@ struct GnSlice {
 };
 
 template <typename T, int V, int ACT>
-__global__ __launch_bounds__(GN_TS) void gn_small_kernel(const T* __restrict__ X, GnSlice q,
+__global__ __launch_bounds__(V == 8 ? GN_T : GN_TS) void gn_small_kernel(const T* __restrict__ X, GnSlice q,
                                                          const float* __restrict__ gamma,
                                                          const float* __restrict__ beta, float eps, float slope,
                                                          T* __restrict__ Y, float* __restrict__ mean,
@@ -523,31 +625,44 @@ __global__ __launch_bounds__(GN_TS) void gn_small_kernel(const T* __restrict__ X
                 s[j] += d;
                 ss[j] = fma(d, d, ss[j]);
             }
-    int parts = sum_rows<V>(s, sh, q.k, q.cols);
-    for (int g = t >> 6; g < q.gs; g += (int)blockDim.x >> 6) {
-        const double a = group_total(sh, parts, W, 0, g, q.cg, W, W);
-        if ((t & 63) == 0) sh[q.k * W + q.gs + g] = a;
-    }
-    parts = sum_rows<V>(ss, sh, q.k, q.cols);
-    for (int g = t >> 6; g < q.gs; g += (int)blockDim.x >> 6) {
-        const double a = group_total(sh, parts, W, 0, g, q.cg, W, W);
-        if ((t & 63) == 0) {
-            const float2 m = moments(sh[q.k * W + q.gs + g], a, M, eps);
-            stat[g] = m;
-            mean[(int64_t)n * q.G + g0 + g] = m.x;
-            rstd[(int64_t)n * q.G + g0 + g] = m.y;
+    const int lh = same_group(q.cg, V), nv = V >> lh, threads = q.k * q.cols;
+    RowSums a{sh, 31 - __builtin_clz(nv), threads, q.cols, 0}, b = a;
+    auto groups = [&](const RowSums& r, auto done) {
+        for (int g = t >> 6; g < q.gs; g += (int)blockDim.x >> 6) {
+            const double v = group_total(r, W >> lh, 0, g, q.cg >> lh, W >> lh, W >> lh);
+            if ((t & 63) == 0) done(g, v);
         }
+    };
+    put_rows<V>(s, sh, threads, lh);
+    if (lh > 0) {      // both sums fit
+        put_rows<V>(ss, sh + nv * threads, threads, lh);
+        a.parts = b.parts = fold_rows(sh, 2 * nv, q.k, q.cols);
+        b.sh += nv * threads;
+        groups(a, [&](int g, double v) { sh[q.k * W + q.gs + g] = v; });
+    } else {
+        a.parts = fold_rows(sh, nv, q.k, q.cols);
+        groups(a, [&](int g, double v) { sh[q.k * W + q.gs + g] = v; });
+        __syncthreads();
+        put_rows<V>(ss, sh, threads, lh);
+        b.parts = fold_rows(sh, nv, q.k, q.cols);
     }
+    groups(b, [&](int g, double v) {
+        const float2 m = moments(sh[q.k * W + q.gs + g], v, M, eps);
+        stat[g] = m;
+        mean[(int64_t)n * q.G + g0 + g] = m.x;
+        rstd[(int64_t)n * q.G + g0 + g] = m.y;
+    });
     __syncthreads();
     if (!on) return;
     float mu[V], sc[V], be[V];
+    Channel ch(col * V, W, q.cg);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = col * V + j;
-        const float2 m = stat[c / q.cg];
+        const float2 m = stat[ch.g];
         mu[j] = m.x;
-        sc[j] = m.y * gamma[c0 + c];
-        be[j] = beta[c0 + c];
+        sc[j] = m.y * gamma[c0 + col * V + j];
+        be[j] = beta[c0 + col * V + j];
+        ch.next(W, q.cg);
     }
 #pragma unroll
     for (int l = 0; l < GN_ROWS_F; ++l) {
@@ -564,7 +679,7 @@ __global__ __launch_bounds__(GN_TS) void gn_small_kernel(const T* __restrict__ X
 // The backward of a slice: the samples one after another in one block, so
 // that dgamma and dbeta need no second launch.
 template <typename T, int V, int ACT>
-__global__ __launch_bounds__(GN_TS) void gn_bwd_small_kernel(const T* __restrict__ X, const T* __restrict__ dY,
+__global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict__ X, const T* __restrict__ dY,
                                                              GnSlice q, int N, const float* __restrict__ gamma,
                                                              const float* __restrict__ beta,
                                                              const float* __restrict__ mean,
@@ -590,47 +705,54 @@ __global__ __launch_bounds__(GN_TS) void gn_bwd_small_kernel(const T* __restrict
             ga[j] = gamma[c0 + col * V + j];
             be[j] = beta[c0 + col * V + j];
         }
-    for (int n = 0; n < N; ++n) {
-        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
+    struct Held {
         Vec<T, V> u[GN_ROWS_B], d[GN_ROWS_B];
-        float mu[V] = {}, rs[V] = {};
+        float mu[V], rs[V];
+    };
+    const Channel first(col * V, W, q.cg);
+    auto load = [&](Held& x, int n) {
+        if (!on) return;
+        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
 #pragma unroll
         for (int l = 0; l < GN_ROWS_B; ++l) {
-            const int i = r + l * q.k;
-            if (on && i < q.nrows) {
-                u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
-                d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
-            }
+            const int i = min(r + l * q.k, q.nrows - 1);
+            x.u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
+            x.d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
         }
-        if (on)
+        Channel ch = first;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int64_t g = (int64_t)n * q.G + g0 + (col * V + j) / q.cg;
-                mu[j] = mean[g];
-                rs[j] = rstd[g];
-            }
+        for (int j = 0; j < V; ++j) {
+            const int64_t g = (int64_t)n * q.G + g0 + ch.g;
+            x.mu[j] = mean[g];
+            x.rs[j] = rstd[g];
+            ch.next(W, q.cg);
+        }
+    };
+    RowSums rows{sh, 31 - __builtin_clz(V), q.k * q.cols, q.cols, 0};
+    auto sample = [&](const Held& x, int n) {
         double a[V] = {}, b[V] = {};
 #pragma unroll
         for (int l = 0; l < GN_ROWS_B; ++l)
             if (on && r + l * q.k < q.nrows)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
-                    const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+                    const float xv = wide(x.u[l].v[j]), xhat = (xv - x.mu[j]) * x.rs[j];
+                    const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, x.mu[j], x.rs[j], xhat, ga[j], be[j], slope);
                     a[j] += (double)dz;
                     b[j] += (double)(dz * xhat);
                 }
-        int parts = sum_rows<V>(a, sh, q.k, q.cols);
+        put_rows<V>(a, sh, q.k * q.cols, 0);
+        rows.parts = fold_rows(sh, V, q.k, q.cols);
         for (int c = t; c < W; c += T_) {
-            double v = 0.0;
-            for (int i = 0; i < parts; ++i) v += sh[i * W + c];
+            const double v = rows.total(c);
             cha[c] = v;
             tota[c] += v;
         }
-        parts = sum_rows<V>(b, sh, q.k, q.cols);
+        __syncthreads();
+        put_rows<V>(b, sh, q.k * q.cols, 0);
+        rows.parts = fold_rows(sh, V, q.k, q.cols);
         for (int c = t; c < W; c += T_) {
-            double v = 0.0;
-            for (int i = 0; i < parts; ++i) v += sh[i * W + c];
+            const double v = rows.total(c);
             chb[c] = v;
             totb[c] += v;
         }
@@ -647,28 +769,40 @@ __global__ __launch_bounds__(GN_TS) void gn_bwd_small_kernel(const T* __restrict
             if ((t & 63) == 0) s12[g] = make_float2((float)(s1 / M), (float)(s2 / M));
         }
         __syncthreads();
-        if (on) {
-            float s1[V], s2[V];
+        if (!on) return;
+        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
+        float s1[V], s2[V];
+        Channel ch = first;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 v = s12[ch.g];
+            s1[j] = v.x;
+            s2[j] = v.y;
+            ch.next(W, q.cg);
+        }
+#pragma unroll
+        for (int l = 0; l < GN_ROWS_B; ++l) {
+            const int i = r + l * q.k;
+            if (i >= q.nrows) continue;
+            Vec<T, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float2 v = s12[(col * V + j) / q.cg];
-                s1[j] = v.x;
-                s2[j] = v.y;
+                const float xv = wide(x.u[l].v[j]), xhat = (xv - x.mu[j]) * x.rs[j];
+                const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, x.mu[j], x.rs[j], xhat, ga[j], be[j], slope);
+                narrow(o.v[j], x.rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
             }
-#pragma unroll
-            for (int l = 0; l < GN_ROWS_B; ++l) {
-                const int i = r + l * q.k;
-                if (i >= q.nrows) continue;
-                Vec<T, V> o;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
-                    const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
-                    narrow(o.v[j], rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
-                }
-                vstore<T, V>(dX + at + (int64_t)i * q.C, o);
-            }
+            vstore<T, V>(dX + at + (int64_t)i * q.C, o);
         }
+    };
+    // the next sample's loads are in flight while this one is summed
+    Held x, y;
+    load(x, 0);
+    for (int n = 0; n < N; n += 2) {
+        if (n + 1 < N) load(y, n + 1);
+        sample(x, n);
+        if (n + 1 == N) break;
+        if (n + 2 < N) load(x, n + 2);
+        sample(y, n + 1);
     }
     for (int c = t; c < W; c += T_) {
         dbeta[c0 + c] = (float)tota[c];
@@ -707,18 +841,18 @@ template <typename T> GnGeom gn_geom(const cf_dims& x, int G)
 // The slice plan of a shape, or cols = 0 where a group does not fit one block.
 // `held` vectors per thread, `arrays` doubles per channel beside the sums in
 // LDS (4 in the backward).
-template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int held, int arrays)
+template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int threads, int held, int arrays)
 {
     GnSlice q{};
     const int64_t vox = x.d * x.h * x.w;
-    const int threads = V == 8 ? GN_T : GN_TS;
     q.C = (int)x.c;
     q.G = G;
     q.cg = q.C / G;
     q.S = vox * x.c;
     if (vox > (int64_t)threads * held || q.C % V) return q;
     q.nrows = (int)vox;
-    // whole vectors, and 64 bytes of a voxel where the registers allow it
+    // whole vectors, and 64 bytes of a voxel where the registers allow it and many blocks are left: what a block
+    // computes takes longer than what it reads
     for (int gs = 1; gs <= G; ++gs) {
         const int W = gs * q.cg;
         if (G % gs || W % V) continue;
@@ -730,7 +864,7 @@ template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int held, 
         q.gs = gs;
         q.cols = cols;
         q.k = k;
-        if (W * esize >= 64) break;
+        if (W * esize >= 64 || G / gs <= GN_SLICES) break;
     }
     return q;
 }
@@ -742,20 +876,20 @@ template <typename T> GnSlice fwd_slice(const cf_dims& x, int G, int* V)
 {
     constexpr int v = vec_of<T>();
     *V = v;
-    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_ROWS_F, 0);
+    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), v == 8 ? GN_T : GN_TS, GN_ROWS_F, 0);
     if (q.cols) return q;
     *V = 1;
-    return gn_slice<1>(x, G, (int)sizeof(T), GN_ROWS_F, 0);
+    return gn_slice<1>(x, G, (int)sizeof(T), GN_TS, GN_ROWS_F, 0);
 }
 template <typename T> GnSlice bwd_slice(const cf_dims& x, int G, int* V)
 {
     constexpr int v = vec_of<T>();
     *V = v;
     if (x.n > GN_SMALL_N) return GnSlice{};
-    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_ROWS_B, 4);
+    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 4);
     if (q.cols) return q;
     *V = 1;
-    return gn_slice<1>(x, G, (int)sizeof(T), GN_ROWS_B, 4);
+    return gn_slice<1>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 4);
 }
 
 template <typename T, int V, int ACT>
@@ -793,7 +927,8 @@ hipError_t run_fwd(const T* X, const float* gamma, const float* beta, float eps,
     const GnGeom q = gn_geom<T>(x, G);
     const dim3 grid((unsigned)q.nb, (unsigned)q.chunks, (unsigned)x.n), block((unsigned)up64(q.k * q.cc));
     double2* part = (double2*)ws;
-    hipLaunchKernelGGL((gn_stats_kernel<T, V>), grid, block, (size_t)q.k * q.cc * V * sizeof(double), s, X, q, part);
+    hipLaunchKernelGGL((gn_stats_kernel<T, V>), grid, block,
+                       (size_t)q.k * q.cc * (2 * V >> same_group(q.cg, V)) * sizeof(double), s, X, q, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gn_apply_kernel<T, V, ACT>), grid, block, (size_t)G * sizeof(float2), s, X, q,
@@ -821,7 +956,7 @@ hipError_t run_bwd(const T* X, const T* dY, const float* gamma, const float* bet
     p += up256b((size_t)x.n * q.C * sizeof(double2));
     float2* s12 = (float2*)p;
     const dim3 grid((unsigned)q.nb, (unsigned)q.chunks, (unsigned)x.n), block((unsigned)up64(q.k * q.cc));
-    hipLaunchKernelGGL((gn_bwd_sums_kernel<T, V, ACT>), grid, block, (size_t)q.k * q.cc * V * sizeof(double), s, X, dY,
+    hipLaunchKernelGGL((gn_bwd_sums_kernel<T, V, ACT>), grid, block, (size_t)q.k * q.cc * 2 * V * sizeof(double), s, X, dY,
                        q, gamma, beta, mean, rstd, slope, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
