@@ -43,6 +43,7 @@ constexpr int GN_TS = 1024;      // most threads of a small-group block
 constexpr int GN_ROWS_F = 8;     // vectors per thread held by the small forward
 constexpr int GN_ROWS_B = 4;     // and by the small backward (of x and dy each)
 constexpr size_t GN_LDS = 65536; // most LDS of a small-group block
+constexpr int GN_FEW = 192;      // streaming blocks that leave CUs idle
 constexpr int GN_SLICES = 64;    // blocks per sample from which slices of more groups are taken
 constexpr int GN_BLOCKS = 1024;  // streaming blocks per launch, about 4 per CU
 
@@ -830,8 +831,9 @@ template <typename T> GnGeom gn_geom(const cf_dims& x, int G)
     q.cc = (q.cols + q.chunks - 1) / q.chunks;
     q.k = GN_T / q.cc;
     q.nrows = q.S / q.row;
-    // enough blocks to fill the chip, at least four rows per thread
-    const int64_t want = (q.nrows + 4 * q.k - 1) / (4 * q.k);
+    // eight rows for each thread (a block's coefficients and sums cost as much), four where that leaves CUs idle
+    int64_t want = (q.nrows + 8 * q.k - 1) / (8 * q.k);
+    if (want * x.n * q.chunks < GN_FEW) want = (q.nrows + 4 * q.k - 1) / (4 * q.k);
     int64_t most = GN_BLOCKS / (x.n * q.chunks);
     if (most < 1) most = 1;
     q.nb = (int)(want < 1 ? 1 : want < most ? want : most);
