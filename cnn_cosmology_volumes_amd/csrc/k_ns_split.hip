@@ -50,7 +50,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int SP_TILE = 256;      // largest edge of an output tile
 constexpr int SP_K = 32;          // reduction values of a piece
-constexpr int SP_GRID = 256;      // blocks of a product, one per CU
+constexpr int SP_GRID = 256;      // blocks of a product whose tiles are shared, one per CU
 constexpr int SP_SB = 36;         // LDS row stride of a 32 x 32 block, floats
 constexpr int SP_PART = SP_TILE * SP_TILE;      // floats of a tile's partial sums
 
@@ -624,64 +624,62 @@ __global__ __launch_bounds__(256) void sp_join_kernel(SpProduct q, SpFinal<T, F>
     sp_block<MODE>(acc, shared[wave], q, fin, ti * edge + blk / edge, tj * edge + blk % edge);
 }
 
-// Blocks of a product with tiles of edge 128 or 256 that share their
-// reductions: one for each CU, but no more than 16 for a tile (the joining
-// launch adds a tile's partial sums one after another).
-int sp_grid(int64_t tiles, int kb)
-{
-    return (int)std::min<int64_t>(std::min<int64_t>(SP_GRID, 16 * tiles), (tiles * kb + 1) / 2);
-}
-bool sp_joins(int64_t tiles, int kb, int grid) { return tiles * kb % grid != 0 || tiles * kb / grid % kb != 0; }
-
-// The tile whose estimated time is least, in microseconds from timings of
-// 512..4096 square and of long products: 64 takes 4.5 + 0.24 a piece for each
-// round of a block per CU, and its launch writes the result itself; 128 takes
-// 0.85 a piece and 12, 256 2.75 a piece and 16, and where blocks share tiles
-// the joining launch adds 12 or 20.  Times of P X (64, 128, 256): m = n = 1024
-// 14, 26, 38 us; 2048: 77, 57, 76; 4096: 499, 406, 348.
-int sp_tile(SpProduct q)
+// Tiles and blocks of a product: those of least estimated time, in
+// microseconds from timings of 512..4096 square and of long products.
+//   64: 4.5 + 0.24 a piece for each round of a block per CU;
+//   128 and 256, a block for each tile: 12 + 0.65 (0.76 in several rounds),
+//   10 + 2.6 a piece and round;
+//   128 and 256, the units cut into equal ranges for one block per CU (but no
+//   more than 16 for a tile, whose partial sums the joining launch adds one
+//   after another): 19 + 0.95 a piece of a block and 24 a tile of one that has
+//   several, 28 + 2.9 a piece, the join among them.
+// Times of P X (64, 128, 256): m = n = 1024 14, 26, 38 us; 2048: 77, 54, 75;
+// 4096: 499, 390, 330.  X X^T with tiles of 128, whole and cut: 2048: 58, 45;
+// 2500: 58, 74.
+void sp_plan(SpProduct& q)
 {
     double best = 0.0;
-    int pick = 0;
+    SpProduct pick = q;
+    auto offer = [&](int grid, double us) {
+        if (best != 0.0 && us >= best) return;
+        best = us;
+        pick = q;
+        pick.grid = grid;
+    };
     for (int tile : {64, 128, 256}) {
+        q.tile = tile;
         q.mt = (q.m + tile - 1) / tile;
         q.nt = (q.n + tile - 1) / tile;
-        const int64_t t = sp_tiles(q);
-        double us;
+        const int64_t t = sp_tiles(q), units = t * q.kb;
+        const double whole = (double)((t + SP_GRID - 1) / SP_GRID) * q.kb;      // pieces of the busiest CU
         if (tile == SP_SMALL) {
-            us = (double)((t + SP_GRID - 1) / SP_GRID) * (4.5 + 0.24 * q.kb);
-        } else {
-            const int grid = sp_grid(t, q.kb);
-            const bool joins = sp_joins(t, q.kb, grid);
-            const double pieces = (double)((t * q.kb + grid - 1) / grid);
-            us = tile == 128 ? 0.85 * pieces + (joins ? 24 : 12) : 2.75 * pieces + (joins ? 36 : 16);
+            offer((int)t, (double)((t + SP_GRID - 1) / SP_GRID) * 4.5 + 0.24 * whole);
+            continue;
         }
-        if (!pick || us < best) {
-            pick = tile;
-            best = us;
-        }
+        offer((int)t, tile == 128 ? 12 + (t > SP_GRID ? 0.76 : 0.65) * whole : 10 + 2.6 * whole);
+        const int grid = (int)std::min<int64_t>(std::min<int64_t>(SP_GRID, 16 * t), (units + 1) / 2);
+        const double cut = (double)((units + grid - 1) / grid);
+        const double restarts = t > grid ? 24.0 * (double)t / grid : 0.0;
+        offer(grid, tile == 128 ? 19 + 0.95 * cut + restarts : 28 + 2.9 * cut);
     }
-    return pick;
+    q = pick;
 }
 
 template <int MODE, typename T = float, typename F = SpNone>
 hipError_t sp_run(SpProduct q, const SpFinal<T, F>& fin, hipStream_t s)
 {
-    q.tile = sp_tile(q);
-    q.mt = (q.m + q.tile - 1) / q.tile;
-    q.nt = (q.n + q.tile - 1) / q.tile;
-    const int64_t tiles = sp_tiles(q);
+    sp_plan(q);
+    const int64_t tiles = sp_tiles(q), units = tiles * q.kb;
     if (q.tile == SP_SMALL) {
-        hipLaunchKernelGGL((sp_small_kernel<MODE, T, F>), dim3((unsigned)tiles), dim3(256), 0, s, q, fin);
+        hipLaunchKernelGGL((sp_small_kernel<MODE, T, F>), dim3((unsigned)q.grid), dim3(256), 0, s, q, fin);
         return hipGetLastError();
     }
-    q.grid = sp_grid(tiles, q.kb);
     if (q.tile == 256)
         hipLaunchKernelGGL((sp_product_kernel<256, MODE, T, F>), dim3((unsigned)q.grid), dim3(512), 0, s, q, fin);
     else
         hipLaunchKernelGGL((sp_product_kernel<128, MODE, T, F>), dim3((unsigned)q.grid), dim3(256), 0, s, q, fin);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !sp_joins(tiles, q.kb, q.grid)) return e;
+    if (e != hipSuccess || (units % q.grid == 0 && units / q.grid % q.kb == 0)) return e;      // whole tiles everywhere
     const int edge = q.tile / 32;
     hipLaunchKernelGGL((sp_join_kernel<MODE, T, F>), dim3((unsigned)(tiles * edge * edge / 4)), dim3(256), 0, s, q, fin);
     return hipGetLastError();
