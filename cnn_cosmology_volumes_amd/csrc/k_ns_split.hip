@@ -467,18 +467,28 @@ __device__ __forceinline__ void sp_small_read(SpPiece& f, const uint4* stage)
         }
     }
 }
-__device__ __forceinline__ void sp_small_multiply(const SpPiece& f, f32x16 (&acc)[2][2])
+// One half's products, and 16 loads (mask 0x010) or LDS reads (0x100) among them.
+template <int OTHERS>
+__device__ __forceinline__ void sp_small_multiply(const SpPiece& f, int h, f32x16 (&acc)[2][2])
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int x = 0; x < 3; ++x)
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x == 2 ? f.al[h][i] : f.ah[h][i],
+                                                                  x == 1 ? f.bl[h][j] : f.bh[h][j], acc[i][j], 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x == 2 ? f.al[h][i] : f.ah[h][i],
-                                                                      x == 1 ? f.bl[h][j] : f.bh[h][j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(OTHERS, 2, 0);
+    }
+#pragma unroll
+    for (int i = 4; i < 12; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(OTHERS, 1, 0);
+    }
 }
 
 template <int MODE, typename T, typename F>
@@ -505,10 +515,9 @@ __global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F
         // (past the last piece it is loaded again and not used: the waits count on a load every time)
         auto load = [&](uint4* stage) {
             sp_small_load(stage, src, off, ld);
-            if (--left > 0) {
-                src[0] += 512;
-                src[1] += 512;
-            }
+            const int step = --left > 0 ? 512 : 0;
+            src[0] += step;
+            src[1] += step;
         };
         // the older of the two pieces under way has landed
         auto landed = [] {
@@ -530,9 +539,10 @@ __global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F
         auto piece_of = [&](const SpPiece& now, SpPiece& then, uint4* cur, uint4* nxt) {
             have_read();
             load(cur);
+            sp_small_multiply<0x010>(now, 0, acc);
             landed();
             sp_small_read(then, nxt);
-            sp_small_multiply(now, acc);
+            sp_small_multiply<0x100>(now, 1, acc);
         };
         for (int i = 0; i < count / 2; ++i) {
             piece_of(f0, f1, A, B);
