@@ -353,7 +353,7 @@ hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* 
                                 hipStream_t s);
 // One large matrix by split fp16 products (k_ns_split.hip), where the
 // coefficients allow it; out, or w <- w keep - rate o.
-bool ns_split_size(int m);
+bool ns_split_size(int m, int n);
 bool ns_split_coef(const NsCoef& c);
 size_t ns_split_ws_bytes(int m, int n);
 template <typename T>

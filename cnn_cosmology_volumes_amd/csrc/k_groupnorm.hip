@@ -30,6 +30,11 @@
 // reads every input once (gn_*_small); larger ones take a reducing launch and
 // an applying launch (with a short joining launch between them in the
 // backward).
+//
+// What bounds it: large samples, memory: 8 x 128^3 x 32 bf16 forward takes 603
+// us for 3.2 GB (x is read twice; 5.3 TB/s, a copy reaches 5.1), 8 x 64^3 x 64
+// backward 286 us for 1.34 GB.  A few MB, the latencies of two or three
+// dependent launches: 3 x 37 x 29 x 31 x 60 fp32 forward 20.6 us.
 #include "cf_internal.h"
 
 #include <algorithm>

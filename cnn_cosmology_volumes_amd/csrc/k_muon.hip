@@ -18,10 +18,18 @@
 // X are.  U U^T and the m x m products therefore run on the fp64 matrix cores
 // (products of fp32 values are exact in fp64); the result is then closer to
 // the exact one than fp32 products of X.  Only the last product, s Q U, is
-// fp32.
+// fp32, as products of three bf16 parts.
 //
 // Launches take a list of matrices; partial sums are added in a fixed order
 // and there are no atomics: results are reproducible bit for bit.
+//
+// What bounds it: the chain of launches.  256 x 256 takes 112 us in 17 of them
+// (a launch of this kind takes about 5 us with almost no work), the eight
+// matrices of the 128^3 benchmark network 196 us: momentum 14, U U^T 32 (fp64
+// matrix cores), its join 10, 14 rounds of 7.5, s Q U 32.  Shorter sides up to
+// 64 iterate in one block instead (108 x 32: 21 us, 70 by rounds), and large
+// matrices whose long side is not much longer take split products of X
+// (k_ns_split.hip).
 #include "cf_internal.h"
 
 #include <algorithm>
@@ -290,6 +298,11 @@ __device__ __forceinline__ void put_planes(uint16_t* p, int64_t size, int64_t i,
     p[2 * size + i] = f2bf((float)(r - (double)bf2f(mid)));
 }
 
+// Small matrices take tiles of 16, many of them, large ones tiles of 32, which
+// read less: a whole iteration of 400 x 400 takes 180 and 209 us, 448 x 448
+// 197 and 209, 500 x 500 259 and 242.
+constexpr int NS_EDGE_16 = 448;
+
 // Block = one (16 TS)^2 tile of the upper triangle; its four waves take every
 // fourth 16-deep piece of the reduction and are joined through LDS in order.
 // A lane's 16-byte loads cover k = 4 (lane / 16) + 0..3 of a piece: the order
@@ -533,7 +546,9 @@ __global__ __launch_bounds__(NS_T) void ns_final_kernel(FinalArgs g, F f, const 
 
 // ----------------------------------------------- one block for a small matrix
 // The iteration of a matrix with m <= 64 in one block's LDS: three fp64 m x m
-// buffers, results held in registers until every wave has read.  WHOLE: also
+// buffers, results held in registers until every wave has read.  64 x 512 takes
+// 42 us for 14 rounds' 65; the matrix cores are busy half of the time, the rest
+// is barriers and the uneven share of 10 tiles among 4 SIMDs.  WHOLE: also
 // U U^T and s Q U, from U in LDS; else A_0 comes from the joining launch and Q
 // goes to its planes.
 constexpr int NB_T = 1024;
@@ -863,8 +878,7 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
         r.a = c.a;
         r.b = c.b;
         r.c = c.c;
-        // small matrices: many small tiles; large ones: tiles that read less
-        const int edge = maxm <= 256 ? 16 : 32;
+        const int edge = maxm <= NS_EDGE_16 ? 16 : 32;
         auto round = [&](std::initializer_list<Product> ps) -> hipError_t {
             r.np = 0;
             for (const Product& x : ps) r.p[r.np++] = x;
@@ -909,8 +923,13 @@ struct NsParts {
 NsParts ns_parts(const NsShapes& l, bool allow_split)
 {
     NsParts p{};
+    // Matrices that share the rounds' launches: with two or more, those of moderate size join them rather than take
+    // 17 launches each (400 x 400 beside 256 x 6912: 264 us apart, 202 together).
+    int rounds = 0;
+    for (int i = 0; i < l.count; ++i)
+        rounds += ns_split_size(l.m[i], l.n[i]) ? l.m[i] <= NS_EDGE_16 : l.m[i] > NB_M;
     for (int i = 0; i < l.count; ++i) {
-        if (allow_split && ns_split_size(l.m[i])) {
+        if (allow_split && ns_split_size(l.m[i], l.n[i]) && !(rounds > 1 && l.m[i] <= NS_EDGE_16)) {
             p.split[p.splits++] = i;
             continue;
         }

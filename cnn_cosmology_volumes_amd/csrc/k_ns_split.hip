@@ -34,9 +34,11 @@
 // adds in the order of the blocks.  No atomics and no waiting between blocks:
 // results are reproducible bit for bit.
 //
-// What bounds it: 4096 x 4096 takes 3943 us, of it 339 for each P X (1.21
+// What bounds it: 4096 x 4096 takes 3850 us, of it 330 for each P X (1.25
 // PFLOP/s of fp16 products; a library fp16 product of that size reaches 1.26)
-// with the matrix cores busy 77% of the cycles at 1.46 GHz: the chip's power.
+// with the matrix cores busy 77% of the cycles at 1.5 GHz: the chip's power.
+// 2048 x 2048 takes 733 us, 56 for each P X (55% at 1.6 GHz) and 46 for each
+// symmetric product, 13 of them the joining launch.
 #include "cf_internal.h"
 
 #include <algorithm>
@@ -893,11 +895,11 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
 
 }  // namespace
 
-// Shorter sides from which these products beat the fp64 path's on the short side: 333 x 1001 takes 152 us here and
-// 214 there, 256 x 6912 238 and 190.
-constexpr int SP_MIN = 320;
-
-bool ns_split_size(int m) { return m >= SP_MIN; }
+// Where these products beat the fp64 path, whose time is 14 rounds of m x m
+// products and grows little with n (here, there, in microseconds): 300 x 300
+// 123, 124; 333 x 1001 149, 136; 400 x 400 135, 180; 400 x 4000 233, 203;
+// 500 x 3000 240, 266; 640 x 640 166, 286.
+bool ns_split_size(int m, int n) { return n <= 20 * ((int64_t)m - 290); }
 bool ns_split_coef(const NsCoef& c) { return ns_bounds(c).fits; }
 size_t ns_split_ws_bytes(int m, int n) { return sp_layout(m, n).bytes; }
 

@@ -1,8 +1,9 @@
 """Newton-Schulz and Muon at the sizes where the library changes its way of
 computing: one block (shorter side up to 64, with or without the whole matrix
-in LDS), fp64 rounds (up to 319), split fp16 products (from 320, with tiles of
-64, 128 and 256 and reductions cut over blocks), and coefficients that the
-split products do not take.
+in LDS), fp64 rounds (tiles of 16, and of 32 from 449), split fp16 products
+(from about 300 where the longer side is not much longer, with tiles of 64,
+128 and 256 and reductions cut over blocks), and coefficients that the split
+products do not take.
 
 The reference is the definition in float64.  Tolerance as in
 test_gpu_muon.py: |out - exact| <= 2^-22 K sum_k |a|^(steps - 1 - k) |X_k|,
@@ -52,7 +53,7 @@ def check(got, x, ns=NS):
 SHAPES = [(1, 1), (1, 640), (1, 641), (640, 16), (641, 16), (17, 208), (209, 17), (48, 208), (209, 48), (64, 64),
           (64, 128), (64, 129), (129, 64), (60, 3000), (5000, 33), (65, 65), (65, 4097), (128, 128), (2049, 192),
           (200, 319), (257, 255), (319, 319), (319, 640), (320, 320), (320, 9000), (7001, 333), (321, 352), (640, 511),
-          (768, 2000), (1300, 1290), (2000, 1025), (2300, 2900), (4090, 4000)]
+          (768, 2000), (448, 450), (449, 5001), (500, 4000), (7003, 600), (6000, 640), (1300, 1290), (2000, 1025), (2300, 2900), (4090, 4000)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
@@ -90,7 +91,8 @@ def test_coefficients_without_a_small_bound():
 
 
 LISTS = [[(108, 32), (16, 16), (3, 200)], [(64, 300), (40, 50)], [(300, 64), (64, 3), (128, 1000)],
-         [(2300, 2900), (108, 32), (64, 700), (300, 280), (500, 340)], [(330, 8000), (8000, 330)]]
+         [(2300, 2900), (108, 32), (64, 700), (300, 280), (500, 340)], [(330, 8000), (8000, 330)],
+         [(400, 410), (440, 430)], [(400, 410), (32, 40), (700, 650)]]
 
 
 @pytest.mark.parametrize("nesterov", [False, True])
