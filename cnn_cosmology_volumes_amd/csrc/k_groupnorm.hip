@@ -47,6 +47,7 @@ constexpr int GN_T = 512;        // most threads of a streaming block
 constexpr int GN_TS = 1024;      // most threads of a small-group block
 constexpr int GN_ROWS_F = 8;     // vectors per thread held by the small forward
 constexpr int GN_ROWS_B = 4;     // and by the small backward (of x and dy each)
+constexpr int GN_SMALL_N = 4;    // most samples that one block of the small backward takes in turn
 constexpr size_t GN_LDS = 65536; // most LDS of a small-group block
 constexpr int GN_FEW = 192;      // streaming blocks that leave CUs idle
 constexpr int GN_SLICES = 64;    // blocks per sample from which slices of more groups are taken
@@ -711,9 +712,9 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict_
             ga[j] = gamma[c0 + col * V + j];
             be[j] = beta[c0 + col * V + j];
         }
+    float2* stat = s12 + q.gs;               // [N][gs] mean, rstd
     struct Held {
         Vec<T, V> u[GN_ROWS_B], d[GN_ROWS_B];
-        float mu[V], rs[V];
     };
     const Channel first(col * V, W, q.cg);
     auto load = [&](Held& x, int n) {
@@ -725,25 +726,27 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict_
             x.u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
             x.d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
         }
-        Channel ch = first;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int64_t g = (int64_t)n * q.G + g0 + ch.g;
-            x.mu[j] = mean[g];
-            x.rs[j] = rstd[g];
-            ch.next(W, q.cg);
-        }
     };
     RowSums rows{sh, 31 - __builtin_clz(V), q.k * q.cols, q.cols, 0};
     auto sample = [&](const Held& x, int n) {
+        float mu[V] = {}, rs[V] = {};
+        if (on) {
+            Channel ch = first;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                mu[j] = stat[n * q.gs + ch.g].x;
+                rs[j] = stat[n * q.gs + ch.g].y;
+                ch.next(W, q.cg);
+            }
+        }
         double a[V] = {}, b[V] = {};
 #pragma unroll
         for (int l = 0; l < GN_ROWS_B; ++l)
             if (on && r + l * q.k < q.nrows)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xv = wide(x.u[l].v[j]), xhat = (xv - x.mu[j]) * x.rs[j];
-                    const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, x.mu[j], x.rs[j], xhat, ga[j], be[j], slope);
+                    const float xv = wide(x.u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+                    const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
                     a[j] += (double)dz;
                     b[j] += (double)(dz * xhat);
                 }
@@ -793,9 +796,9 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict_
             Vec<T, V> o;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xv = wide(x.u[l].v[j]), xhat = (xv - x.mu[j]) * x.rs[j];
-                const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, x.mu[j], x.rs[j], xhat, ga[j], be[j], slope);
-                narrow(o.v[j], x.rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
+                const float xv = wide(x.u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+                const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+                narrow(o.v[j], rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
             }
             vstore<T, V>(dX + at + (int64_t)i * q.C, o);
         }
@@ -803,6 +806,11 @@ __global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict_
     // the next sample's loads are in flight while this one is summed
     Held x, y;
     load(x, 0);
+    for (int e = t; e < N * q.gs; e += T_) {
+        const int64_t g = (int64_t)(e / q.gs) * q.G + g0 + e % q.gs;
+        stat[e] = make_float2(mean[g], rstd[g]);
+    }
+    __syncthreads();
     for (int n = 0; n < N; n += 2) {
         if (n + 1 < N) load(y, n + 1);
         sample(x, n);
@@ -867,7 +875,7 @@ template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int thread
         if (cols > threads) break;
         const int k = (int)std::min<int64_t>(vox, threads / cols);
         if ((vox + k - 1) / k > held) break;
-        if (((size_t)(k + arrays) * W + 2 * gs) * sizeof(double) > GN_LDS) break;
+        if (((size_t)(k + arrays) * W + (1 + GN_SMALL_N) * gs) * sizeof(double) > GN_LDS) break;
         q.gs = gs;
         q.cols = cols;
         q.k = k;
@@ -875,9 +883,6 @@ template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int thread
     }
     return q;
 }
-
-// Samples that one block of the small backward takes in turn.
-constexpr int GN_SMALL_N = 4;
 
 template <typename T> GnSlice fwd_slice(const cf_dims& x, int G, int* V)
 {
@@ -914,7 +919,7 @@ hipError_t run_small_bwd(const GnSlice& q, int64_t N, const T* X, const T* dY, c
                          const float* mean, const float* rstd, float slope, T* dX, float* dgamma, float* dbeta,
                          hipStream_t s)
 {
-    const size_t lds = ((size_t)(q.k + 4) * q.gs * q.cg + q.gs) * sizeof(double);
+    const size_t lds = ((size_t)(q.k + 4) * q.gs * q.cg + (1 + N) * q.gs) * sizeof(double);
     hipLaunchKernelGGL((gn_bwd_small_kernel<T, V, ACT>), dim3((unsigned)(q.G / q.gs)),
                        dim3((unsigned)up64(q.k * q.cols)), lds, s, X, dY, q, (int)N, gamma, beta, mean, rstd, slope,
                        dX, dgamma, dbeta);
