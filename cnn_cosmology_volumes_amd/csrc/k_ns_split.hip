@@ -123,8 +123,10 @@ __device__ __forceinline__ void sp_wave_sync()
 
 // Writes the 32 x 32 block in LDS (rows of SP_SB floats; flip: its transpose)
 // to rows r0.. and piece c0 / 32 of d.  Eight lanes write a row's line.
+// SP_POLY adds S, and leaves the sums in LDS for the mirror; else the block is
+// multiplied by f.
 template <int MODE>
-__device__ __forceinline__ void sp_put(const float* sh, bool flip, const SpProduct& q, uint16_t* d, int kd, int r0,
+__device__ __forceinline__ void sp_put(float* sh, bool flip, float f, const SpProduct& q, uint16_t* d, int kd, int r0,
                                        int c0, int rows, int cols)
 {
     const int lane = (int)threadIdx.x & 63, chunk = lane & 7, k8 = (chunk & 3) * 8;
@@ -133,6 +135,7 @@ __device__ __forceinline__ void sp_put(const float* sh, bool flip, const SpProdu
         return ((int64_t)min(r0 + it * 8 + lane / 8, rows - 1) * row_lines(kd) + c0 / SP_K) * 64;
     };
     f16x8 hi[4], lo[4], o[4];
+    float sums[4][8];
     if (MODE == SP_POLY)
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -144,10 +147,11 @@ __device__ __forceinline__ void sp_put(const float* sh, bool flip, const SpProdu
         const int r = it * 8 + lane / 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float v = q.f * (flip ? sh[(k8 + j) * SP_SB + r] : sh[r * SP_SB + k8 + j]);
+            float v = f * (flip ? sh[(k8 + j) * SP_SB + r] : sh[r * SP_SB + k8 + j]);
             if (MODE == SP_POLY) {
                 v = fmaf(q.g, (float)hi[it][j] + (float)lo[it][j], v);
                 if (r0 + r == c0 + k8 + j) v += q.diag;
+                sums[it][j] = v;
             }
             if (c0 + k8 + j >= cols) v = 0.f;
             const _Float16 h = (_Float16)v;
@@ -157,6 +161,11 @@ __device__ __forceinline__ void sp_put(const float* sh, bool flip, const SpProdu
 #pragma unroll
     for (int it = 0; it < 4; ++it)
         if (r0 + it * 8 + lane / 8 < rows) *reinterpret_cast<f16x8*>(d + line(it) + chunk * 8) = o[it];
+    if (MODE == SP_POLY && chunk < 4)
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sh[(it * 8 + lane / 8) * SP_SB + k8 + j] = sums[it][j];
 }
 
 // The caller's row-major matrix, [m][n] or (tall) [n][m].
@@ -198,11 +207,15 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
     for (int r = 0; r < 16; ++r) sh[(8 * (r / 4) + 4 * (lane / 32) + r % 4) * SP_SB + lane % 32] = acc[r];
     sp_wave_sync();
     if constexpr (MODE == SP_GRAM || MODE == SP_POLY) {
-        sp_put<MODE>(sh, false, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
-        if (bi < bj) sp_put<MODE>(sh, true, q, q.d, pieces(q.n), j0, i0, q.m, q.n);
+        sp_put<MODE>(sh, false, q.f, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
+        if (bi < bj) {
+            // (S is symmetric: the mirror's sums are the same)
+            if (MODE == SP_POLY) sp_wave_sync();
+            sp_put<SP_GRAM>(sh, true, MODE == SP_POLY ? 1.f : q.f, q, q.d, pieces(q.n), j0, i0, q.m, q.n);
+        }
     } else if constexpr (MODE == SP_BOTH) {
-        sp_put<MODE>(sh, false, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
-        sp_put<MODE>(sh, true, q, q.dt, pieces(q.m), j0, i0, q.n, q.m);
+        sp_put<MODE>(sh, false, q.f, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
+        sp_put<MODE>(sh, true, q.f, q, q.dt, pieces(q.m), j0, i0, q.n, q.m);
     } else {
         const int c = lane % 32, x0 = fin.tall ? j0 : i0, y0 = fin.tall ? i0 : j0;
         const int rows = fin.tall ? q.n : q.m, cols = fin.tall ? q.m : q.n;
@@ -716,14 +729,25 @@ template <typename T> __global__ __launch_bounds__(256) void sp_norm_kernel(cons
     constexpr int V = 16 / (int)sizeof(T);
     double a = 0.0;
     const int64_t vecs = n / V;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vecs; i += SP_NORM * 256) {
-        T v[V];
-        __builtin_memcpy(v, u + i * V, 16);
+    auto add = [&](const T* v) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const double d = (double)Elem<T>::load(v, j);
             a = fma(d, d, a);
         }
+    };
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (; i + 3 * SP_NORM * 256 < vecs; i += 4 * SP_NORM * 256) {      // four loads in flight
+        T v[4][V];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) __builtin_memcpy(v[l], u + (i + l * SP_NORM * 256) * V, 16);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) add(v[l]);
+    }
+    for (; i < vecs; i += SP_NORM * 256) {
+        T v[V];
+        __builtin_memcpy(v, u + i * V, 16);
+        add(v);
     }
     if (blockIdx.x == 0 && (int64_t)threadIdx.x < n - vecs * V) {
         const double d = (double)Elem<T>::load(u, vecs * V + threadIdx.x);
@@ -758,8 +782,8 @@ __global__ __launch_bounds__(256) void sp_split_kernel(const T* u, int rows, int
         sh[r * SP_SB + c] = v;
     }
     sp_wave_sync();
-    sp_put<SP_BOTH>(sh, false, q, tall ? q.dt : q.d, bc, r0, c0, rows, cols);
-    sp_put<SP_BOTH>(sh, true, q, tall ? q.d : q.dt, pieces(rows), c0, r0, cols, rows);
+    sp_put<SP_BOTH>(sh, false, 1.f, q, tall ? q.dt : q.d, bc, r0, c0, rows, cols);
+    sp_put<SP_BOTH>(sh, true, 1.f, q, tall ? q.d : q.dt, pieces(rows), c0, r0, cols, rows);
 }
 
 // -------------------------------------------------------------------- plan
@@ -846,7 +870,6 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
     hipLaunchKernelGGL(sp_norm_kernel<T>, dim3(SP_NORM), dim3(256), 0, s, u, (int64_t)m * n, norm);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    q.f = 1.f;
     q.d = X;
     q.dt = XT[0];
     const int64_t blocks = ((int64_t)pieces(rows) * pieces(cols) + 3) / 4;
