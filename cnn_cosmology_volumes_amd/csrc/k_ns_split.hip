@@ -918,11 +918,12 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
 
 }  // namespace
 
-// Where these products beat the fp64 path, whose time is 14 rounds of m x m
-// products and grows little with n (here, there, in microseconds): 300 x 300
-// 123, 124; 333 x 1001 149, 136; 400 x 400 135, 180; 400 x 4000 233, 203;
-// 500 x 3000 240, 266; 640 x 640 166, 286.
-bool ns_split_size(int m, int n) { return n <= 20 * ((int64_t)m - 290); }
+// Where these products beat the fp64 path, whose 14 rounds of m x m products
+// cost as m^2 to m^3 while n costs it little (here, there, in microseconds):
+// 320 x 320 125, 129 and x 640 134, 130; 360 x 1440 168, 170 and x 2880 224,
+// 181; 512 x 4096 261, 273 and x 12288 421, 354; 768 x 18432 810, 846 and
+// x 24576 1180, 968; 1024 x 16384 1071, 1425; 2048 x 65536 11714, 15895.
+bool ns_split_size(int m, int n) { return 16 * (int64_t)n <= (int64_t)m * (m - 300); }
 bool ns_split_coef(const NsCoef& c) { return ns_bounds(c).fits; }
 size_t ns_split_ws_bytes(int m, int n) { return sp_layout(m, n).bytes; }
 
