@@ -27,7 +27,8 @@
 // bit.
 //
 // Groups small enough for one block's registers take a single launch that
-// reads every input once (gn_*_small); larger ones take a reducing launch and
+// reads every input once (gn_*_small; the backward of samples that share no
+// block adds one that joins dgamma and dbeta); larger ones take a reducing launch and
 // an applying launch (with a short joining launch between them in the
 // backward).
 //
@@ -47,10 +48,9 @@ constexpr int GN_T = 512;        // most threads of a streaming block
 constexpr int GN_TS = 1024;      // most threads of a small-group block
 constexpr int GN_ROWS_F = 8;     // vectors per thread held by the small forward
 constexpr int GN_ROWS_B = 4;     // and by the small backward (of x and dy each)
-constexpr int GN_SMALL_N = 4;    // most samples that one block of the small backward takes in turn
 constexpr size_t GN_LDS = 65536; // most LDS of a small-group block
 constexpr int GN_FEW = 192;      // streaming blocks that leave CUs idle
-constexpr int GN_SLICES = 64;    // blocks per sample from which slices of more groups are taken
+constexpr int GN_SLICES = 256;   // blocks from which slices of more groups are taken
 constexpr int GN_BLOCKS = 1024;  // streaming blocks per launch, about 4 per CU
 
 // V values of T as one 16-byte access (V = 1: one element).
@@ -113,9 +113,9 @@ struct RowSums {
     }
 };
 
-template <int V> __device__ __forceinline__ void put_rows(const double (&v)[V], double* sh, int n, int lh)
+template <int V> __device__ __forceinline__ void put_rows(const double (&v)[V], double* sh, int n, int lh,
+                                                             int t = (int)threadIdx.x)
 {
-    const int t = (int)threadIdx.x;
     if (t >= n) return;
     double w[V];
 #pragma unroll
@@ -599,7 +599,8 @@ struct GnSlice {
     int C, G, cg;
     int gs;          // groups of a slice
     int cols;        // vectors of a slice's row
-    int k;           // rows in flight; k * cols <= threads
+    int k;           // rows in flight
+    int p;           // samples of a block (the backward's); p * k * cols <= threads
 };
 
 template <typename T, int V, int ACT>
@@ -683,145 +684,159 @@ __global__ __launch_bounds__(V == 8 ? GN_T : GN_TS) void gn_small_kernel(const T
     }
 }
 
-// The backward of a slice: the samples one after another in one block, so
-// that dgamma and dbeta need no second launch.
+// The backward of a slice.  Where a block holds all samples beside each other
+// it writes dgamma and dbeta; else it takes one sample and writes its channel
+// sums, which gn_bwd_small_join_kernel adds.  (2 x 8^3 x 256 fp32: one launch
+// 9.0 us, two 9.9; the samples one after another in one block 12.9, and 3 to 8
+// us for each further one.  8 x 8^3 x 256 bf16: two launches 15.4, streaming
+// 23.3.)
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(GN_T) void gn_bwd_small_kernel(const T* __restrict__ X, const T* __restrict__ dY,
-                                                             GnSlice q, int N, const float* __restrict__ gamma,
+                                                             GnSlice q, const float* __restrict__ gamma,
                                                              const float* __restrict__ beta,
                                                              const float* __restrict__ mean,
                                                              const float* __restrict__ rstd, float slope,
                                                              T* __restrict__ dX, float* __restrict__ dgamma,
-                                                             float* __restrict__ dbeta)
+                                                             float* __restrict__ dbeta, double2* __restrict__ part)
 {
     extern __shared__ double sh[];
-    const int t = (int)threadIdx.x, T_ = (int)blockDim.x, r = t / q.cols, col = t % q.cols;
+    const int t = (int)threadIdx.x, T_ = (int)blockDim.x, per = q.k * q.cols, p = t / per, tp = t - p * per;
+    const int r = tp / q.cols, col = tp % q.cols, n0 = (int)blockIdx.y * q.p, n = n0 + p;
     const int W = q.gs * q.cg, c0 = (int)blockIdx.x * W, g0 = (int)blockIdx.x * q.gs;
-    double* cha = sh + q.k * W;              // [W] channel sums of dz, then of dz xhat
-    double* chb = cha + W;
-    double* tota = chb + W;                  // [W] the same over the samples
-    double* totb = tota + W;
-    float2* s12 = reinterpret_cast<float2*>(totb + W);
+    double* cha = sh + q.p * q.k * W;        // [p][W] channel sums of dz, then of dz xhat
+    double* chb = cha + q.p * W;
+    float2* s12 = reinterpret_cast<float2*>(chb + q.p * W);
+    float2* stat = s12 + q.p * q.gs;         // [p][gs] mean, rstd
     const double M = (double)q.nrows * q.cg;
-    const bool on = r < q.k;
-    for (int c = t; c < W; c += T_) tota[c] = totb[c] = 0.0;
+    const bool on = p < q.p;
+    const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
+    Vec<T, V> u[GN_ROWS_B], d[GN_ROWS_B];
     float ga[V] = {}, be[V] = {};
-    if (on)
+    if (on) {
+#pragma unroll
+        for (int l = 0; l < GN_ROWS_B; ++l) {
+            const int i = min(r + l * q.k, q.nrows - 1);
+            u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
+            d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             ga[j] = gamma[c0 + col * V + j];
             be[j] = beta[c0 + col * V + j];
         }
-    float2* stat = s12 + q.gs;               // [N][gs] mean, rstd
-    struct Held {
-        Vec<T, V> u[GN_ROWS_B], d[GN_ROWS_B];
-    };
+    }
+    for (int e = t; e < q.p * q.gs; e += T_) {
+        const int64_t i = (int64_t)(n0 + e / q.gs) * q.G + g0 + e % q.gs;
+        stat[e] = make_float2(mean[i], rstd[i]);
+    }
+    __syncthreads();
     const Channel first(col * V, W, q.cg);
-    auto load = [&](Held& x, int n) {
-        if (!on) return;
-        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
-#pragma unroll
-        for (int l = 0; l < GN_ROWS_B; ++l) {
-            const int i = min(r + l * q.k, q.nrows - 1);
-            x.u[l] = vload<T, V>(X + at + (int64_t)i * q.C);
-            x.d[l] = vload<T, V>(dY + at + (int64_t)i * q.C);
-        }
-    };
-    RowSums rows{sh, 31 - __builtin_clz(V), q.k * q.cols, q.cols, 0};
-    auto sample = [&](const Held& x, int n) {
-        float mu[V] = {}, rs[V] = {};
-        if (on) {
-            Channel ch = first;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                mu[j] = stat[n * q.gs + ch.g].x;
-                rs[j] = stat[n * q.gs + ch.g].y;
-                ch.next(W, q.cg);
-            }
-        }
-        double a[V] = {}, b[V] = {};
-#pragma unroll
-        for (int l = 0; l < GN_ROWS_B; ++l)
-            if (on && r + l * q.k < q.nrows)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xv = wide(x.u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
-                    const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
-                    a[j] += (double)dz;
-                    b[j] += (double)(dz * xhat);
-                }
-        put_rows<V>(a, sh, q.k * q.cols, 0);
-        rows.parts = fold_rows(sh, V, q.k, q.cols);
-        for (int c = t; c < W; c += T_) {
-            const double v = rows.total(c);
-            cha[c] = v;
-            tota[c] += v;
-        }
-        __syncthreads();
-        put_rows<V>(b, sh, q.k * q.cols, 0);
-        rows.parts = fold_rows(sh, V, q.k, q.cols);
-        for (int c = t; c < W; c += T_) {
-            const double v = rows.total(c);
-            chb[c] = v;
-            totb[c] += v;
-        }
-        __syncthreads();
-        for (int g = t >> 6; g < q.gs; g += T_ >> 6) {
-            double s1 = 0.0, s2 = 0.0;
-            for (int i = t & 63; i < q.cg; i += 64) {
-                const double gm = (double)gamma[c0 + g * q.cg + i];
-                s1 += gm * cha[g * q.cg + i];
-                s2 += gm * chb[g * q.cg + i];
-            }
-            s1 = wave_sum(s1);
-            s2 = wave_sum(s2);
-            if ((t & 63) == 0) s12[g] = make_float2((float)(s1 / M), (float)(s2 / M));
-        }
-        __syncthreads();
-        if (!on) return;
-        const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
-        float s1[V], s2[V];
+    float mu[V] = {}, rs[V] = {};
+    if (on) {
         Channel ch = first;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float2 v = s12[ch.g];
-            s1[j] = v.x;
-            s2[j] = v.y;
+            mu[j] = stat[p * q.gs + ch.g].x;
+            rs[j] = stat[p * q.gs + ch.g].y;
             ch.next(W, q.cg);
         }
+    }
+    double a[V] = {}, b[V] = {};
 #pragma unroll
-        for (int l = 0; l < GN_ROWS_B; ++l) {
-            const int i = r + l * q.k;
-            if (i >= q.nrows) continue;
-            Vec<T, V> o;
+    for (int l = 0; l < GN_ROWS_B; ++l)
+        if (on && r + l * q.k < q.nrows)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xv = wide(x.u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
-                const float dz = act_bwd<ACT>(wide(x.d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
-                narrow(o.v[j], rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
+                const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+                const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+                a[j] += (double)dz;
+                b[j] += (double)(dz * xhat);
             }
-            vstore<T, V>(dX + at + (int64_t)i * q.C, o);
+    // channel sums of each sample
+    auto sums = [&](const double (&v)[V], double* to) {
+        put_rows<V>(v, sh + p * V * per, per, 0, on ? tp : per);
+        const int parts = fold_rows(sh, q.p * V, q.k, q.cols);
+        for (int e = t; e < q.p * W; e += T_) {
+            const int i = e / W;
+            to[e] = RowSums{sh + i * V * per, 31 - __builtin_clz(V), per, q.cols, parts}.total(e - i * W);
         }
+        __syncthreads();
     };
-    // the next sample's loads are in flight while this one is summed
-    Held x, y;
-    load(x, 0);
-    for (int e = t; e < N * q.gs; e += T_) {
-        const int64_t g = (int64_t)(e / q.gs) * q.G + g0 + e % q.gs;
-        stat[e] = make_float2(mean[g], rstd[g]);
+    sums(a, cha);
+    sums(b, chb);
+    for (int g = t >> 6; g < q.p * q.gs; g += T_ >> 6) {
+        double s1 = 0.0, s2 = 0.0;
+        const int c = g % q.gs * q.cg;
+        for (int i = t & 63; i < q.cg; i += 64) {
+            const double gm = (double)gamma[c0 + c + i];
+            s1 += gm * cha[g * q.cg + i];
+            s2 += gm * chb[g * q.cg + i];
+        }
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if ((t & 63) == 0) s12[g] = make_float2((float)(s1 / M), (float)(s2 / M));
     }
     __syncthreads();
-    for (int n = 0; n < N; n += 2) {
-        if (n + 1 < N) load(y, n + 1);
-        sample(x, n);
-        if (n + 1 == N) break;
-        if (n + 2 < N) load(x, n + 2);
-        sample(y, n + 1);
-    }
     for (int c = t; c < W; c += T_) {
-        dbeta[c0 + c] = (float)tota[c];
-        dgamma[c0 + c] = (float)totb[c];
+        double ta = 0.0, tb = 0.0;
+        for (int i = 0; i < q.p; ++i) {
+            ta += cha[i * W + c];
+            tb += chb[i * W + c];
+        }
+        if (part) {
+            part[(int64_t)n0 * q.C + c0 + c] = make_double2(ta, tb);
+        } else {
+            dbeta[c0 + c] = (float)ta;
+            dgamma[c0 + c] = (float)tb;
+        }
     }
+    if (!on) return;
+    float s1[V], s2[V];
+    Channel ch = first;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float2 v = s12[p * q.gs + ch.g];
+        s1[j] = v.x;
+        s2[j] = v.y;
+        ch.next(W, q.cg);
+    }
+#pragma unroll
+    for (int l = 0; l < GN_ROWS_B; ++l) {
+        const int i = r + l * q.k;
+        if (i >= q.nrows) continue;
+        Vec<T, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xv = wide(u[l].v[j]), xhat = (xv - mu[j]) * rs[j];
+            const float dz = act_bwd<ACT>(wide(d[l].v[j]), xv, mu[j], rs[j], xhat, ga[j], be[j], slope);
+            narrow(o.v[j], rs[j] * (fmaf(ga[j], dz, -s1[j]) - xhat * s2[j]));
+        }
+        vstore<T, V>(dX + at + (int64_t)i * q.C, o);
+    }
+}
+
+// dgamma and dbeta: 32 channels a block, eight threads to a channel's samples.
+__global__ __launch_bounds__(256) void gn_bwd_small_join_kernel(int C, int N, const double2* __restrict__ part,
+                                                                float* __restrict__ dgamma, float* __restrict__ dbeta)
+{
+    __shared__ double2 sh[8][32];
+    const int i = (int)threadIdx.x % 32, way = (int)threadIdx.x / 32, c = (int)blockIdx.x * 32 + i;
+    double2 a = make_double2(0.0, 0.0);
+    if (c < C)
+        for (int n = way; n < N; n += 8) {
+            const double2 v = part[(int64_t)n * C + c];
+            a.x += v.x;
+            a.y += v.y;
+        }
+    sh[way][i] = a;
+    __syncthreads();
+    if (way || c >= C) return;
+    for (int w = 1; w < 8; ++w) {
+        a.x += sh[w][i].x;
+        a.y += sh[w][i].y;
+    }
+    dbeta[c] = (float)a.x;
+    dgamma[c] = (float)a.y;
 }
 
 // -------------------------------------------------------------------- plans
@@ -855,9 +870,10 @@ template <typename T> GnGeom gn_geom(const cf_dims& x, int G)
 
 // The slice plan of a shape, or cols = 0 where a group does not fit one block.
 // `held` vectors per thread, `arrays` doubles per channel beside the sums in
-// LDS (4 in the backward).
-template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int threads, int held, int arrays)
+// LDS (2 in the backward), `p` samples of a block.
+template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int threads, int held, int arrays, int p)
 {
+    threads /= p;
     GnSlice q{};
     const int64_t vox = x.d * x.h * x.w;
     q.C = (int)x.c;
@@ -866,8 +882,10 @@ template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int thread
     q.S = vox * x.c;
     if (vox > (int64_t)threads * held || q.C % V) return q;
     q.nrows = (int)vox;
+    q.p = p;
     // whole vectors, and 64 bytes of a voxel where the registers allow it and many blocks are left: what a block
-    // computes takes longer than what it reads
+    // computes takes longer than what it reads while every CU has one block at most (backward of 12 x 8^3 x 256 bf16:
+    // 384 blocks of 16 bytes 26.4 us, 192 of 32 bytes 13.7)
     for (int gs = 1; gs <= G; ++gs) {
         const int W = gs * q.cg;
         if (G % gs || W % V) continue;
@@ -875,12 +893,14 @@ template <int V> GnSlice gn_slice(const cf_dims& x, int G, int esize, int thread
         if (cols > threads) break;
         const int k = (int)std::min<int64_t>(vox, threads / cols);
         if ((vox + k - 1) / k > held) break;
-        if (((size_t)(k + arrays) * W + (1 + GN_SMALL_N) * gs) * sizeof(double) > GN_LDS) break;
+        if (p * ((size_t)(k + arrays) * W + 2 * gs) * sizeof(double) > GN_LDS) break;
         q.gs = gs;
         q.cols = cols;
         q.k = k;
-        if (W * esize >= 64 || G / gs <= GN_SLICES) break;
+        if (W * esize >= 64 || G / gs * (x.n / p) <= GN_SLICES) break;
     }
+    // more blocks of narrow slices take longer than streaming (24 x 12^3 x 128 bf16: 46.9 us, 41.0)
+    if (q.cols && q.gs < G && q.gs * q.cg * esize < 64 && G / q.gs * (x.n / p) > GN_SLICES) q.cols = 0;
     return q;
 }
 
@@ -888,20 +908,25 @@ template <typename T> GnSlice fwd_slice(const cf_dims& x, int G, int* V)
 {
     constexpr int v = vec_of<T>();
     *V = v;
-    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), v == 8 ? GN_T : GN_TS, GN_ROWS_F, 0);
+    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), v == 8 ? GN_T : GN_TS, GN_ROWS_F, 0, 1);
     if (q.cols) return q;
     *V = 1;
-    return gn_slice<1>(x, G, (int)sizeof(T), GN_TS, GN_ROWS_F, 0);
+    return gn_slice<1>(x, G, (int)sizeof(T), GN_TS, GN_ROWS_F, 0, 1);
 }
 template <typename T> GnSlice bwd_slice(const cf_dims& x, int G, int* V)
 {
     constexpr int v = vec_of<T>();
-    *V = v;
-    if (x.n > GN_SMALL_N) return GnSlice{};
-    GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 4);
-    if (q.cols) return q;
-    *V = 1;
-    return gn_slice<1>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 4);
+    // all samples in a block, if they fit, then one
+    for (int p : {(int)x.n, 1}) {
+        if (p > GN_T) continue;
+        *V = v;
+        GnSlice q = gn_slice<v>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 2, p);
+        if (q.cols) return q;
+        *V = 1;
+        q = gn_slice<1>(x, G, (int)sizeof(T), GN_T, GN_ROWS_B, 2, p);
+        if (q.cols) return q;
+    }
+    return GnSlice{};
 }
 
 template <typename T, int V, int ACT>
@@ -917,12 +942,17 @@ hipError_t run_small_fwd(const GnSlice& q, int64_t N, const T* X, const float* g
 template <typename T, int V, int ACT>
 hipError_t run_small_bwd(const GnSlice& q, int64_t N, const T* X, const T* dY, const float* gamma, const float* beta,
                          const float* mean, const float* rstd, float slope, T* dX, float* dgamma, float* dbeta,
-                         hipStream_t s)
+                         double2* part, hipStream_t s)
 {
-    const size_t lds = ((size_t)(q.k + 4) * q.gs * q.cg + (1 + N) * q.gs) * sizeof(double);
-    hipLaunchKernelGGL((gn_bwd_small_kernel<T, V, ACT>), dim3((unsigned)(q.G / q.gs)),
-                       dim3((unsigned)up64(q.k * q.cols)), lds, s, X, dY, q, (int)N, gamma, beta, mean, rstd, slope,
-                       dX, dgamma, dbeta);
+    const size_t lds = q.p * ((size_t)(q.k + 2) * q.gs * q.cg + 2 * q.gs) * sizeof(double);
+    const bool join = N > q.p;
+    hipLaunchKernelGGL((gn_bwd_small_kernel<T, V, ACT>), dim3((unsigned)(q.G / q.gs), (unsigned)(N / q.p)),
+                       dim3((unsigned)up64(q.p * q.k * q.cols)), lds, s, X, dY, q, gamma, beta, mean, rstd, slope, dX,
+                       dgamma, dbeta, join ? part : nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !join) return e;
+    hipLaunchKernelGGL(gn_bwd_small_join_kernel, dim3((unsigned)((q.C + 31) / 32)), dim3(256), 0, s, q.C, (int)N,
+                       (const double2*)part, dgamma, dbeta);
     return hipGetLastError();
 }
 
@@ -957,8 +987,10 @@ hipError_t run_bwd(const T* X, const T* dY, const float* gamma, const float* bet
     int v;
     const GnSlice sl = bwd_slice<T>(x, G, &v);
     if (sl.cols)
-        return v == 1 ? run_small_bwd<T, 1, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, s)
-                      : run_small_bwd<T, V, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta, s);
+        return v == 1 ? run_small_bwd<T, 1, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta,
+                                                 (double2*)ws, s)
+                      : run_small_bwd<T, V, ACT>(sl, x.n, X, dY, gamma, beta, mean, rstd, slope, dX, dgamma, dbeta,
+                                                 (double2*)ws, s);
     const GnGeom q = gn_geom<T>(x, G);
     const int npart = q.nb * q.chunks;
     char* p = (char*)ws;
@@ -983,7 +1015,8 @@ hipError_t run_bwd(const T* X, const T* dY, const float* gamma, const float* bet
 template <typename T> size_t ws_bytes(const cf_dims& x, int G, bool bwd)
 {
     int v;
-    if ((bwd ? bwd_slice<T>(x, G, &v) : fwd_slice<T>(x, G, &v)).cols) return 0;
+    const GnSlice sl = bwd ? bwd_slice<T>(x, G, &v) : fwd_slice<T>(x, G, &v);
+    if (sl.cols) return bwd && x.n > sl.p ? up256b((size_t)x.n * x.c * sizeof(double2)) : 0;
     const GnGeom q = gn_geom<T>(x, G);
     const size_t npart = (size_t)x.n * q.nb * q.chunks;
     if (!bwd) return up256b(npart * G * sizeof(double2));

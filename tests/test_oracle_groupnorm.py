@@ -105,3 +105,11 @@ def test_binding_refuses_other_layouts():
         cf.cf_groupnorm_bwd(x, x.bfloat16(), 2, v, v, m, m)
     with pytest.raises(ValueError):
         cf.cf_groupnorm_bwd(x, x[:, :1].contiguous(), 2, v, v, m, m)
+
+
+@pytest.mark.parametrize("dt,shape,groups", [(cf.CF_BF16, (8, 8, 8, 8, 64), 8), (cf.CF_F32, (16, 8, 8, 8, 256), 32)])
+def test_sums_of_samples_need_their_workspace(dt, shape, groups):
+    n = cf.cf_groupnorm_workspace_size(dt, shape, groups, True)
+    assert n >= 16 * shape[0] * shape[4]
+    assert _bwd(dt=dt, shape=shape, groups=groups, wsb=n - 1) == cf.CF_ERR_WORKSPACE
+    assert _bwd(dt=dt, shape=shape, groups=groups, ws=None) == cf.CF_ERR_INVALID
