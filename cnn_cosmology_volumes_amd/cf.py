@@ -577,7 +577,7 @@ def _packed(name, t, dtype=None, shape=None):
         raise ValueError("%s must be contiguous" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -599,13 +599,13 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
                      stream=None):
     """Group norm of NDHWC X, then the activation -> (Y, mean [N, groups],
     rstd [N, groups])."""
-    dt, d, groups = dtype_code(X.dtype), dims(X.shape), int(groups)
+    dt, d, groups = dtype_code(X.dtype), cf_dims(*X.shape), int(groups)
     _packed("X", X)
     _packed("gamma", gamma, torch.float32, (d.c,))
     _packed("beta", beta, torch.float32, (d.c,))
     Y = torch.empty_like(X) if Y is None else Y
     mean = gamma.new_empty((d.n, groups)) if mean is None else mean
-    rstd = gamma.new_empty((d.n, groups)) if rstd is None else rstd
+    rstd = torch.empty_like(mean) if rstd is None else rstd
     ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
     check(lib().cf_groupnorm_fwd(dt, d, _ptr(X), groups, _ptr(gamma), _ptr(beta), float(eps), int(act), float(slope),
                                  _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), _stream(stream)))
@@ -616,7 +616,7 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
 def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, slope=1.0, dX=None, ws=None,
                      stream=None):
     """-> (dX, dgamma, dbeta) from the forward's mean and rstd."""
-    dt, d, groups = dtype_code(X.dtype), dims(X.shape), int(groups)
+    dt, d, groups = dtype_code(X.dtype), cf_dims(*X.shape), int(groups)
     _packed("X", X)
     _packed("dY", dY, X.dtype, X.shape)
     _packed("gamma", gamma, torch.float32, (d.c,))
