@@ -25,7 +25,7 @@
 // written.
 //
 // Work split: tiles of 64 x 64, a block each, where they are few (the block's
-// waves share the reduction), else of 128 or 256 (sp_tile gives the rule).
+// waves share the reduction), else of 128 or 256 (sp_plan gives the rule).
 // There a launch has one block per CU, and the (tile, piece of the reduction)
 // units in tile order are cut into equal ranges, one for each block, since the
 // number of tiles seldom fills the chip evenly (136 tiles of a symmetric
@@ -241,17 +241,23 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
 }
 
 // ------------------------------------------------------------------ product
-// Two shapes of a block:
-//   256: 8 waves of 128 x 64, two stages of a piece in LDS (128 KB);
-//   128: 4 waves of 64 x 64, four stages (128 KB): a piece takes a quarter of
-//        the time there, less than a load's latency.
+// Two shapes of a block of 8 waves, with two stages in LDS (128 KB):
+//   256: waves of 128 x 64, a stage holds a piece;
+//   128: two groups of waves of 64 x 64, each with every other piece of the
+//        tile: a stage holds a piece for each, and the two sums are added in
+//        the end.  (One group with four stages takes the same time at 2048 x
+//        2048, 763 us: what bounds these products is power, in which a byte
+//        from L2 to LDS costs as much as the products made of it.  512 x 4096
+//        takes 250 us that way, 255 this way, 2500 x 2500 1223 and 1200.)
 template <int TILE> struct SpShape {
-    static constexpr int WAVES = TILE == 256 ? 8 : 4;
-    static constexpr int WC = WAVES / 2;            // waves side by side
+    static constexpr int WAVES = 8;
+    static constexpr int GW = TILE / 32;            // waves of a group
+    static constexpr int GROUPS = WAVES / GW;
+    static constexpr int WC = GW / 2;               // waves side by side
     static constexpr int MI = TILE / 64;            // a wave's 32 x 32 blocks: rows,
-    static constexpr int NJ = TILE / WC / 32;       // columns
-    static constexpr int STAGES = TILE == 256 ? 2 : 4;
-    static constexpr int CHUNKS = 2 * TILE * 8;     // 16-byte chunks of a stage
+    static constexpr int NJ = 2;                    // columns
+    static constexpr int LINES = 2 * TILE * 8;      // 16-byte chunks of a piece
+    static constexpr int CHUNKS = GROUPS * LINES;   // and of a stage
 };
 
 // Raw 32-bit words from p on.
@@ -260,24 +266,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t sp_rsrc(const void* p)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)0xffffffffu, 0x00020000);
 }
 
-// A stage: TILE lines of p, then TILE of r.  The 16-byte chunk c of row r's
+// A piece in a stage: TILE lines of p, then TILE of r.  The 16-byte chunk c of row r's
 // line lies at slot c ^ (r / 2 & 7): sixteen rows read at one chunk fall on all
 // banks.
 //
-// Starts the loads of a piece; a wave's instruction takes eight rows' lines.
+// Starts the loads of a stage; a wave's instruction takes eight rows' lines of
+// its group's piece.
 // src: this wave's first row of p and of r at that piece, off: the lane's
 // offset in bytes from there, for an even and an odd group of eight rows.
 template <int TILE>
 __device__ __forceinline__ void sp_load(uint4* stage, const char* const (&src)[2], const uint32_t (&off)[2], int64_t ld)
 {
+    using S = SpShape<TILE>;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    uint4* to = stage + wave / S::GW * S::LINES + wave % S::GW * 4 * 64;
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                sp_rsrc(src[o]), (__attribute__((address_space(3))) void*)(stage + o * (TILE * 8) + (wave * 4 + i) * 64),
-                16, off[i & 1], i * 8 * (uint32_t)ld, 0, 0);
+                sp_rsrc(src[o]), (__attribute__((address_space(3))) void*)(to + o * (TILE * 8) + i * 64), 16, off[i & 1],
+                i * 8 * (uint32_t)ld, 0, 0);
 }
 constexpr int SP_LOADS = 8;      // instructions of sp_load
 
@@ -288,8 +297,9 @@ template <int TILE> struct SpFrag {
 template <int TILE> __device__ __forceinline__ void sp_read(SpFrag<TILE>& f, const uint4* stage, int half)
 {
     using S = SpShape<TILE>;
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int wi = wave / S::WC * S::MI * 32, wj = wave % S::WC * S::NJ * 32;
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, w = wave % S::GW;
+    const int wi = w / S::WC * S::MI * 32, wj = w % S::WC * S::NJ * 32;
+    stage += wave / S::GW * S::LINES;
     const int swz = (lane >> 1) & 7;
     const int ch = (half * 2 + lane / 32) ^ swz, cl = (4 + half * 2 + lane / 32) ^ swz;
     const f16x8* A = reinterpret_cast<const f16x8*>(stage) + (wi + lane % 32) * 8;
@@ -351,9 +361,8 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
     // (arrays of their own: loads into one do not hold up reads of another)
     __shared__ uint4 s0[S::CHUNKS];
     __shared__ uint4 s1[S::CHUNKS];
-    __shared__ uint4 s2[S::STAGES > 2 ? S::CHUNKS : 1];
-    __shared__ uint4 s3[S::STAGES > 2 ? S::CHUNKS : 1];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int group = wave / S::GW, w = wave % S::GW;
     const int b = (int)xcd_remap(blockIdx.x, (uint32_t)q.grid);
     const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)row_lines(q.kb) * 128;      // bytes from row to row
     uint32_t off[2];
@@ -366,17 +375,17 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
         const int len = (int)min((int64_t)(q.kb - k0), u1 - u);
         int ti, tj;
         sp_tile_at(q, t, ti, tj);
-        int piece = (k0 + (q.last ? (ti + 1) * (TILE / SP_K) : 0)) % q.kb;
-        const char* src[2] = {(const char*)q.p + ((int64_t)ti * TILE + wave * 32) * ld + (int64_t)piece * 128,
-                              (const char*)q.r + ((int64_t)tj * TILE + wave * 32) * ld + (int64_t)piece * 128};
+        int piece = (k0 + group + (q.last ? (ti + 1) * (TILE / SP_K) : 0)) % q.kb;
+        const char* src[2] = {(const char*)q.p + ((int64_t)ti * TILE + w * 32) * ld + (int64_t)piece * 128,
+                              (const char*)q.r + ((int64_t)tj * TILE + w * 32) * ld + (int64_t)piece * 128};
         f32x16 acc[S::MI][S::NJ] = {};
-        int left = len;      // pieces whose loads have not begun
+        int left = (len - group + S::GROUPS - 1) / S::GROUPS;      // the group's pieces whose loads have not begun
         // (past the last piece it is loaded again and not used: the waits count on a load every time)
         auto load = [&](uint4* stage) {
             sp_load<TILE>(stage, src, off, ld);
-            const bool wrap = piece + 1 == q.kb, more = --left > 0;
-            const int64_t step = more ? 128 - (wrap ? (int64_t)q.kb * 128 : 0) : 0;
-            piece = wrap ? 0 : piece + 1;
+            const bool wrap = piece + S::GROUPS >= q.kb, more = --left > 0;
+            const int64_t step = more ? S::GROUPS * 128 - (wrap ? (int64_t)q.kb * 128 : 0) : 0;
+            piece += S::GROUPS - (wrap ? q.kb : 0);
             src[0] += step;
             src[1] += step;
         };
@@ -384,61 +393,94 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
         SpFrag<TILE> f0, f1;
         load(s0);
         load(s1);
-        if (S::STAGES > 2) {
-            load(s2);
-            load(s3);
-        }
-        sp_landed<S::STAGES - 1>();
+        sp_landed<1>();
         sp_read<TILE>(f0, s0, 0);
-        auto piece_of = [&](uint4* cur, uint4* nxt) {
+        auto pieces_of = [&](uint4* cur, uint4* nxt) {
             sp_read<TILE>(f1, cur, 1);
             sp_multiply<TILE>(f0, acc);
             sp_interleave<TILE, false>();
-            sp_landed<S::STAGES - 2>();
+            sp_landed<0>();
             load(cur);
             sp_read<TILE>(f0, nxt, 0);      // (past the last piece: read and not used)
             sp_multiply<TILE>(f1, acc);
             sp_interleave<TILE, true>();
         };
-        for (int i = 0; i < len / S::STAGES; ++i) {
-            piece_of(s0, s1);
-            if constexpr (S::STAGES == 2) {
-                piece_of(s1, s0);
-            } else {
-                piece_of(s1, s2);
-                piece_of(s2, s3);
-                piece_of(s3, s0);
-            }
+        // the last one of an odd number is the first group's
+        auto odd_piece = [&](uint4* cur) {
+            if (S::GROUPS == 1 || group || !(len & 1)) return;
+            sp_read<TILE>(f1, cur, 1);
+            sp_multiply<TILE>(f0, acc);
+            sp_multiply<TILE>(f1, acc);
+        };
+        const int stages = len / S::GROUPS;
+        for (int i = 0; i < stages / 2; ++i) {
+            pieces_of(s0, s1);
+            pieces_of(s1, s0);
         }
-        if (const int rest = len % S::STAGES) {
-            piece_of(s0, s1);
-            if (rest > 1) piece_of(s1, s2);
-            if (rest > 2) piece_of(s2, s3);
+        if (stages & 1) {
+            pieces_of(s0, s1);
+            odd_piece(s1);
+        } else {
+            odd_piece(s0);
         }
         constexpr int E = TILE / 32;
-        const int wi = wave / S::WC * S::MI, wj = wave % S::WC * S::NJ;
+        const int wi = w / S::WC * S::MI, wj = w % S::WC * S::NJ;
         sp_landed<0>();
-        if (len == q.kb) {
-            float* sh = reinterpret_cast<float*>(s0) + wave * (32 * SP_SB);
+        // A wave ends with DONE rows of blocks, from row i0 of its own: with two groups, each hands the other the sums
+        // of one of its two rows.
+        constexpr int DONE = S::MI / S::GROUPS;
+        const int i0 = S::GROUPS == 1 ? 0 : group;
+        f32x16 total[DONE][S::NJ];
+        if constexpr (S::GROUPS == 1) {
 #pragma unroll
-            for (int i = 0; i < S::MI; ++i)
+            for (int i = 0; i < DONE; ++i)
+#pragma unroll
+                for (int j = 0; j < S::NJ; ++j) total[i][j] = acc[i][j];
+        } else {
+            float4* swap = reinterpret_cast<float4*>(s0) + lane;
+            auto slot = [&](int i, int j, int v) { return (((w * 2 + i) * S::NJ + j) * 4 + v) * 64; };
+#pragma unroll
+            for (int j = 0; j < S::NJ; ++j) {
+                const f32x16 give = group ? acc[0][j] : acc[1][j];
+                total[0][j] = group ? acc[1][j] : acc[0][j];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    swap[slot(1 - group, j, v)] = make_float4(give[4 * v], give[4 * v + 1], give[4 * v + 2],
+                                                              give[4 * v + 3]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < S::NJ; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float4 x = swap[slot(group, j, v)];
+                    total[0][j][4 * v] += x.x;
+                    total[0][j][4 * v + 1] += x.y;
+                    total[0][j][4 * v + 2] += x.z;
+                    total[0][j][4 * v + 3] += x.w;
+                }
+        }
+        if (len == q.kb) {
+            float* sh = reinterpret_cast<float*>(s1) + wave * (32 * SP_SB);
+#pragma unroll
+            for (int i = 0; i < DONE; ++i)
 #pragma unroll
                 for (int j = 0; j < S::NJ; ++j)
-                    sp_block<MODE>(acc[i][j], sh, q, fin, ti * E + wi + i, tj * E + wj + j);
-            __syncthreads();
+                    sp_block<MODE>(total[i][j], sh, q, fin, ti * E + wi + i0 + i, tj * E + wj + j);
         } else {
             // [block of 32 x 32][quarter of a lane's registers][lane]
             float4* out = reinterpret_cast<float4*>(q.part + ((int64_t)b * 2 + seg) * (TILE * TILE));
 #pragma unroll
-            for (int i = 0; i < S::MI; ++i)
+            for (int i = 0; i < DONE; ++i)
 #pragma unroll
                 for (int j = 0; j < S::NJ; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        out[(((wi + i) * E + wj + j) * 4 + v) * 64 + lane] =
-                            make_float4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
-                                        acc[i][j][4 * v + 3]);
+                        out[(((wi + i0 + i) * E + wj + j) * 4 + v) * 64 + lane] =
+                            make_float4(total[i][j][4 * v], total[i][j][4 * v + 1], total[i][j][4 * v + 2],
+                                        total[i][j][4 * v + 3]);
         }
+        __syncthreads();      // before the next tile's loads into LDS
         u += len;
     }
 }
@@ -702,7 +744,7 @@ hipError_t sp_run(SpProduct q, const SpFinal<T, F>& fin, hipStream_t s)
     if (q.tile == 256)
         hipLaunchKernelGGL((sp_product_kernel<256, MODE, T, F>), dim3((unsigned)q.grid), dim3(512), 0, s, q, fin);
     else
-        hipLaunchKernelGGL((sp_product_kernel<128, MODE, T, F>), dim3((unsigned)q.grid), dim3(256), 0, s, q, fin);
+        hipLaunchKernelGGL((sp_product_kernel<128, MODE, T, F>), dim3((unsigned)q.grid), dim3(512), 0, s, q, fin);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (units % q.grid == 0 && units / q.grid % q.kb == 0)) return e;      // whole tiles everywhere
     const int edge = q.tile / 32;
