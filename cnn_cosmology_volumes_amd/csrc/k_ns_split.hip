@@ -34,7 +34,7 @@
 // adds in the order of the blocks.  No atomics and no waiting between blocks:
 // results are reproducible bit for bit.
 //
-// What bounds it: 4096 x 4096 takes 3850 us, of it 330 for each P X (1.25
+// What bounds it: 4096 x 4096 takes 3870 us, of it 330 for each P X (1.25
 // PFLOP/s of fp16 products; a library fp16 product of that size reaches 1.26)
 // with the matrix cores busy 77% of the cycles at 1.5 GHz: the chip's power.
 // 2048 x 2048 takes 733 us, 56 for each P X (55% at 1.6 GHz) and 46 for each
