@@ -20,6 +20,17 @@
 // the exact one than fp32 products of X.  Only the last product, s Q U, is
 // fp32, as products of three bf16 parts.
 //
+// An eigenvalue of A_0 that should be 0 comes out as about +-2^-53 and grows by
+// a^2 a step.  While it stays below 2^-24 (8 steps of a = 3.4445) it is no more
+// than fp32's rounding.  With more steps it would come to matter, and a
+// negative one would run away, since a + b t + c t^2 draws only positive ones
+// back.  Such calls (ns_many) take A_0 + 2^-48 trace(A_0) I in place of A_0,
+// which is what singular values of 2^-24 |X0|, fp32's rounding of X0, would
+// add: no eigenvalue is negative then, and each ends where the polynomial's
+// range ends.  Q holds factors of up to 2^24 beside those of 1 then, so s Q U
+// is an fp64 product there too.  (128 x 4096 of rank 8, 20 steps: singular
+// values up to 1.134, where X's own steps give them; without this, NaN.)
+//
 // Launches take a list of matrices; partial sums are added in a fixed order
 // and there are no atomics: results are reproducible bit for bit.
 //
@@ -34,6 +45,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 namespace cf {
 namespace {
@@ -236,8 +248,9 @@ __host__ __device__ inline int64_t ns_plane(int m) { return (int64_t)ns_ld(m) * 
 
 // Block = one row of a tile pair: four groups of threads each sum every fourth
 // split, then the groups are added in order; scales by s^2 and writes the
-// element and its mirror.  Block 0 of a matrix also stores s.
-__global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, double* ws, double* scale)
+// element and its mirror.  Block 0 of a matrix also stores s.  The diagonal is
+// raised by `lift` times the trace.
+__global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, double lift, double* ws, double* scale)
 {
     __shared__ double red[4], group[4][NS_TILE];
     const int q = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[q];
@@ -259,7 +272,8 @@ __global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, 
     group[w][j] = v;
     double tr = 0.0;
     for (int e = (int)threadIdx.x; e < splits * nt; e += NS_T) tr += part[(int64_t)splits * pairs * (NS_TILE * NS_TILE) + e];
-    const double s = 1.0 / (sqrt(block_sum(tr, red)) + (double)eps);      // (its barriers cover `group` too)
+    tr = block_sum(tr, red);      // (its barriers cover `group` too)
+    const double s = 1.0 / (sqrt(tr) + (double)eps);
     if (b == 0 && threadIdx.x == 0) scale[q] = s;
     int ti, tj;
     tile_pair(p, nt, ti, tj);
@@ -267,6 +281,7 @@ __global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, 
     v = (((group[0][j] + group[1][j]) + group[2][j]) + group[3][j]) * (s * s);
     double* A = ws + g.sq[q];
     const int64_t I = ti * NS_TILE + i, J = tj * NS_TILE + j;
+    if (I == J && I < m) v += lift * tr * (s * s);
     A[I * ld + J] = v;
     A[J * ld + I] = v;
 }
@@ -544,13 +559,89 @@ __global__ __launch_bounds__(NS_T) void ns_final_kernel(FinalArgs g, F f, const 
     else final_tile<false>(U, Q, scale[i], g.m[i], g.n[i], b, f, i, sh);
 }
 
+// Block = the same tile in fp64, with Q as the rounds leave it; each wave a
+// 32 x 32 quadrant.  U's panel is staged in LDS, Q's rows come from memory, 32
+// bytes a lane: k = 4 (lane / 16) + 0..3 of a piece of 16, for both operands.
+// 449 x 4300 takes 65 us here and 41 with three bf16 parts.
+template <bool TALL, typename T, typename F>
+__device__ void final64_tile(const T* U, const double* Q, double s, int m, int n, int b, const F& f, int q, float* su)
+{
+    const int ld = ns_ld(m), across = (m + NS_TILE - 1) / NS_TILE;
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, h = lane / 16, c = lane % 16;
+    const int i0 = b % across * NS_TILE, j0 = b / across * NS_TILE;      // short, long
+    const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
+    const double* qr = Q + (int64_t)(i0 + wi + c) * ld + 4 * h;
+    f64x4 acc[2][2] = {};      // [short][long]
+    float v[NS_PV];
+    panel_load<!TALL>(v, U, n, m, j0, 0, m);      // rows of the long side, the short side to be summed over
+    for (int k0 = 0; k0 < m; k0 += NS_K) {
+        __syncthreads();
+        panel_store<!TALL>(v, su);
+        __syncthreads();
+        if (k0 + NS_K < m) panel_load<!TALL>(v, U, n, m, j0, k0 + NS_K, m);
+#pragma unroll
+        for (int p = 0; p < NS_K; p += 16) {
+            if (k0 + p >= m) break;      // (Q's columns are zeros up to a multiple of 16 above m, and hold anything after it)
+            f64x4 x[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) x[r] = *reinterpret_cast<const f64x4*>(qr + (int64_t)r * 16 * ld + k0 + p);
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                const int k = p + 4 * h + l;
+                double y[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int j = wj + r * 16 + c;
+                    y[r] = (double)su[TALL ? j * NS_SK + k : k * NS_SP + j];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[i][j] = TALL ? __builtin_amdgcn_mfma_f64_16x16x4f64(y[j], x[i][l], acc[i][j], 0, 0, 0)
+                                         : __builtin_amdgcn_mfma_f64_16x16x4f64(x[i][l], y[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+    // element e of a lane's four: row 4 e + lane / 16, column lane % 16
+    auto place = [&](int i, int j, int e) {
+        const int I = i0 + wi + i * 16 + (TALL ? c : 4 * e + h), J = j0 + wj + j * 16 + (TALL ? 4 * e + h : c);
+        return I < m && J < n ? TALL ? (int64_t)J * m + I : (int64_t)I * n + J : (int64_t)-1;
+    };
+    float w[2][2][4];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        w[e / 8][e / 4 % 2][e % 4] = before(f, q, max(place(e / 8, e / 4 % 2, e % 4), (int64_t)0));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float& o = w[e / 8][e / 4 % 2][e % 4];
+        o = result(f, q, (float)(acc[e / 8][e / 4 % 2][e % 4] * s), o);
+        settle(o);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int64_t at = place(e / 8, e / 4 % 2, e % 4);
+        if (at >= 0) finish<T>(f, q, at, w[e / 8][e / 4 % 2][e % 4]);
+    }
+}
+
+template <typename T, typename F>
+__global__ __launch_bounds__(NS_T) void ns_final64_kernel(FinalArgs g, F f, const double* ws, const double* scale)
+{
+    __shared__ float sh[NS_PANEL];
+    const int i = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[i];
+    const T* U = (const T*)g.u[i];
+    if (g.tall >> i & 1) final64_tile<true>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
+    else final64_tile<false>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
+}
+
 // ----------------------------------------------- one block for a small matrix
 // The iteration of a matrix with m <= 64 in one block's LDS: three fp64 m x m
 // buffers, results held in registers until every wave has read.  64 x 512 takes
 // 42 us for 14 rounds' 65; the matrix cores are busy half of the time, the rest
 // is barriers and the uneven share of 10 tiles among 4 SIMDs.  WHOLE: also
 // U U^T and s Q U, from U in LDS; else A_0 comes from the joining launch and Q
-// goes to its planes.
+// goes to its planes, or as it is where s Q U is an fp64 product.
 constexpr int NB_T = 1024;
 constexpr int NB_W = NB_T / 64;                  // waves
 constexpr int NB_M = 64;
@@ -565,8 +656,9 @@ struct BlockArgs {
     int m[CF_MAX_OPT_TENSORS], n[CF_MAX_OPT_TENSORS];
     uint32_t tall;
     int64_t a[CF_MAX_OPT_TENSORS], q[CF_MAX_OPT_TENSORS];      // A_0 and Q's planes, doubles from the workspace's start
-    int steps;
+    int steps, many;
     float ca, cb, cc, eps;
+    double lift;
 };
 
 template <bool WHOLE, typename T, typename F>
@@ -654,7 +746,11 @@ __global__ __launch_bounds__(NB_T) void ns_block_kernel(BlockArgs g, F f, double
         }
         __syncthreads();
         s = 1.0 / (sqrt(trace[0]) + (double)g.eps);
-        for (int e = t; e < mp * mp; e += NB_T) A[e / mp * LD + e % mp] *= s * s;
+        const double up = g.lift * trace[0];
+        for (int e = t; e < mp * mp; e += NB_T) {
+            double& v = A[e / mp * LD + e % mp];
+            v = (e / mp == e % mp && e % mp < m ? v + up : v) * (s * s);
+        }
     } else {
         const double* in = ws + g.a[q];
         const int ld = ns_ld(m);
@@ -724,6 +820,10 @@ __global__ __launch_bounds__(NB_T) void ns_block_kernel(BlockArgs g, F f, double
             for (int v = 0; v < 4; ++v)
                 if (at[v] >= 0) finish<T>(f, q, at[v], x[v]);
         }
+    } else if (g.many) {
+        const int ld = ns_ld(m);
+        double* out = ws + g.q[q];
+        for (int e = t; e < mp * mp; e += NB_T) out[(int64_t)(e / mp) * ld + e % mp] = Q[e / mp * LD + e % mp];
     } else {
         const int ld = ns_plane_ld(m);
         uint16_t* out = (uint16_t*)(ws + g.q[q]);
@@ -809,11 +909,18 @@ NsPlan ns_plan(const NsShapes& l)
     return p;
 }
 
+// Whether eigenvalues of A_0's rounding, 2^-53, could grow past 2^-24, a^2 a
+// step; what the diagonal is raised by then.
+bool ns_many(const NsCoef& c) { return std::fabs(c.a) > 1.f && 2.0 * c.steps * std::log2(std::fabs((double)c.a)) > 29.0; }
+constexpr double NS_LIFT = 0x1p-48;
+
 // Everything of a list from U on.
 template <typename T, typename F>
 hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, const F& f, double* ws, hipStream_t s)
 {
     const NsPlan p = ns_plan(l);
+    const bool many = ns_many(c);
+    const double lift = many ? NS_LIFT : 0.0;
     bool whole = true;
     int maxm = 0;
     BlockArgs k{};
@@ -823,6 +930,8 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
     k.cb = c.b;
     k.cc = c.c;
     k.eps = c.eps;
+    k.many = many;
+    k.lift = lift;
     for (int i = 0; i < l.count; ++i) {
         whole = whole && ns_whole(l.m[i], l.n[i]);
         maxm = std::max(maxm, l.m[i]);
@@ -864,7 +973,7 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
     hipLaunchKernelGGL(ns_gram_kernel<T>, dim3((unsigned)grams), dim3(NS_T), 0, s, g, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ns_join_kernel, dim3((unsigned)joins), dim3(NS_T), 0, s, sq, c.eps, ws, ws);
+    hipLaunchKernelGGL(ns_join_kernel, dim3((unsigned)joins), dim3(NS_T), 0, s, sq, c.eps, lift, ws, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
     int A = 0, T_ = 1, P = 2, Q = 3, R = 4;      // buffers: A_k, P A, P_k, Q and a free one
@@ -894,14 +1003,15 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
         };
         for (int i = 0; i < c.steps; ++i) {
             const bool last = i + 1 == c.steps;
+            const int planes = last && !many;
             if (i == 0) {
-                if ((e = round({{A, A, Q, 1, last}})) != hipSuccess) return e;      // Q = P_0
+                if ((e = round({{A, A, Q, 1, planes}})) != hipSuccess) return e;      // Q = P_0
                 if (!last && (e = round({{Q, A, T_, 0, 0}})) != hipSuccess) return e;
                 if (!last && (e = round({{T_, Q, A, 0, 0}})) != hipSuccess) return e;
                 continue;
             }
             if ((e = round({{A, A, P, 1, 0}})) != hipSuccess) return e;
-            if (last) e = round({{P, Q, R, 0, 1}});
+            if (last) e = round({{P, Q, R, 0, planes}});
             else e = round({{P, A, T_, 0, 0}, {P, Q, R, 0, 0}});
             if (e != hipSuccess) return e;
             std::swap(Q, R);
@@ -909,7 +1019,8 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
         }
     }
     for (int i = 0; i < l.count; ++i) a.q[i] = p.sq[i] + Q * ns_size(l.m[i]);
-    hipLaunchKernelGGL((ns_final_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
+    if (many) hipLaunchKernelGGL((ns_final64_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
+    else hipLaunchKernelGGL((ns_final_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
     return hipGetLastError();
 }
 

@@ -333,8 +333,10 @@ size_t cf_newton_schulz_workspace_size(cf_dtype dtype, int32_t nmat, const int64
  * arrays; x and out entries are DEVICE pointers and must not overlap.  The
  * shorter side must be at most 16384 and a matrix at most 2^36 elements (else
  * CF_ERR_UNSUPPORTED).  Products of fp32 accuracy or better throughout, also
- * for CF_BF16, whose results are rounded once.  Sums are added in a fixed
- * order: results are reproducible bit for bit. */
+ * for CF_BF16, whose results are rounded once; singular values of x below
+ * 2^-24 |x|_F are fp32's rounding, and many steps can raise them to anything
+ * up to the largest value of the polynomial.  Sums are added in a fixed order:
+ * results are reproducible bit for bit. */
 cf_status cf_newton_schulz(const cf_newton_schulz_params* ns, cf_dtype dtype, int32_t nmat, const int64_t* rows,
                            const int64_t* cols, const void* const* x, void* const* out, void* ws, size_t ws_bytes,
                            hipStream_t stream);
