@@ -520,7 +520,7 @@ def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
         _packed("matrix %d" % i, t, mats[0].dtype)
         _packed("output %d" % i, o, t.dtype, t.shape)
     rows, cols = _mat_sizes(mats)
-    ws = _ws(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
+    ws = _scratch(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
     check(lib().cf_newton_schulz(ctypes.byref(ns), dt, len(mats), rows, cols, _pointers(mats), _pointers(out),
                                  _ptr(ws), _wsbytes(ws), _stream(stream)))
     _record(stream, ws, *out)
@@ -538,7 +538,7 @@ def cf_muon(hp, params, grads, m, ws=None, stream=None):
         _packed("gradient %d" % i, grads[i], torch.float32, params[i].shape)
         _packed("momentum %d" % i, m[i], torch.float32, params[i].shape)
     rows, cols = _mat_sizes(params)
-    ws = _ws(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
+    ws = _scratch(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
     check(lib().cf_muon(ctypes.byref(hp), k, rows, cols, _pointers(params), _pointers(grads), _pointers(m), _ptr(ws),
                         _wsbytes(ws), _stream(stream)))
     _record(stream, ws)
@@ -581,6 +581,13 @@ def _packed(name, t, dtype=None, shape=None):
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+def _scratch(nbytes, device, ws):
+    """_ws for a caller's tensor that may be of any type but has no gaps."""
+    if ws is not None:
+        _packed("ws", ws)
+    return _ws(nbytes, device, ws)
+
+
 def _record(stream, *tensors):
     """Tensors made here on the current stream and used on `stream`: their
     memory is not reused before that stream is done with it."""
@@ -603,10 +610,16 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
     _packed("X", X)
     _packed("gamma", gamma, torch.float32, (d.c,))
     _packed("beta", beta, torch.float32, (d.c,))
-    Y = torch.empty_like(X) if Y is None else Y
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _packed(name, t, torch.float32, (d.n, groups))
+    if Y is None:
+        Y = torch.empty_like(X)
+    else:
+        _packed("Y", Y, X.dtype, X.shape)
     mean = gamma.new_empty((d.n, groups)) if mean is None else mean
     rstd = torch.empty_like(mean) if rstd is None else rstd
-    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
+    ws = _scratch(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
     check(lib().cf_groupnorm_fwd(dt, d, _ptr(X), groups, _ptr(gamma), _ptr(beta), float(eps), int(act), float(slope),
                                  _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), _stream(stream)))
     _record(stream, Y, mean, rstd, ws)
@@ -623,9 +636,12 @@ def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, s
     _packed("beta", beta, torch.float32, (d.c,))
     _packed("mean", mean, torch.float32, (d.n, groups))
     _packed("rstd", rstd, torch.float32, (d.n, groups))
-    dX = torch.empty_like(X) if dX is None else dX
+    if dX is None:
+        dX = torch.empty_like(X)
+    else:
+        _packed("dX", dX, X.dtype, X.shape)
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
-    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
+    ws = _scratch(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
     check(lib().cf_groupnorm_bwd(dt, d, _ptr(X), _ptr(dY), groups, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
                                  int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws),
                                  _stream(stream)))
