@@ -520,7 +520,8 @@ def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
         _packed("matrix %d" % i, t, mats[0].dtype)
         _packed("output %d" % i, o, t.dtype, t.shape)
     rows, cols = _mat_sizes(mats)
-    ws = _scratch(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
+    _on_gpu(ws, *mats, *out)
+    ws = _ws(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
     check(lib().cf_newton_schulz(ctypes.byref(ns), dt, len(mats), rows, cols, _pointers(mats), _pointers(out),
                                  _ptr(ws), _wsbytes(ws), _stream(stream)))
     _record(stream, ws, *out)
@@ -538,7 +539,8 @@ def cf_muon(hp, params, grads, m, ws=None, stream=None):
         _packed("gradient %d" % i, grads[i], torch.float32, params[i].shape)
         _packed("momentum %d" % i, m[i], torch.float32, params[i].shape)
     rows, cols = _mat_sizes(params)
-    ws = _scratch(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
+    _on_gpu(ws, *params, *grads, *m)
+    ws = _ws(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
     check(lib().cf_muon(ctypes.byref(hp), k, rows, cols, _pointers(params), _pointers(grads), _pointers(m), _ptr(ws),
                         _wsbytes(ws), _stream(stream)))
     _record(stream, ws)
@@ -581,11 +583,19 @@ def _packed(name, t, dtype=None, shape=None):
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _scratch(nbytes, device, ws):
-    """_ws for a caller's tensor that may be of any type but has no gaps."""
+def _on_gpu(ws, *tensors):
+    """Raises unless the workspace has no gaps and all tensors (or None) are on
+    one GPU, the current one: the kernels run there and take bare addresses."""
     if ws is not None:
         _packed("ws", ws)
-    return _ws(nbytes, device, ws)
+    at = tensors[0].get_device()
+    if at < 0:
+        raise ValueError("tensors must be on a GPU")
+    for t in (ws,) + tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError("tensors must be on one GPU: %s and %s" % (tensors[0].device, t.device))
+    if torch.cuda.is_initialized() and torch.cuda.current_device() != at:
+        raise ValueError("tensors are on GPU %d, the current one is %d" % (at, torch.cuda.current_device()))
 
 
 def _record(stream, *tensors):
@@ -617,9 +627,10 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
         Y = torch.empty_like(X)
     else:
         _packed("Y", Y, X.dtype, X.shape)
+    _on_gpu(ws, X, gamma, beta, Y, mean, rstd)
     mean = gamma.new_empty((d.n, groups)) if mean is None else mean
     rstd = torch.empty_like(mean) if rstd is None else rstd
-    ws = _scratch(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
+    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
     check(lib().cf_groupnorm_fwd(dt, d, _ptr(X), groups, _ptr(gamma), _ptr(beta), float(eps), int(act), float(slope),
                                  _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), _stream(stream)))
     _record(stream, Y, mean, rstd, ws)
@@ -640,8 +651,9 @@ def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, s
         dX = torch.empty_like(X)
     else:
         _packed("dX", dX, X.dtype, X.shape)
+    _on_gpu(ws, X, dY, gamma, beta, mean, rstd, dX)
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
-    ws = _scratch(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
+    ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
     check(lib().cf_groupnorm_bwd(dt, d, _ptr(X), _ptr(dY), groups, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
                                  int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws),
                                  _stream(stream)))
