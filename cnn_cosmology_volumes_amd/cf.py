@@ -509,7 +509,7 @@ def _pointers(ts):
 def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
     """The nearly orthogonal factor of each matrix (all fp32 or all bf16, two
     dimensions or more, the last one the columns) -> list of tensors like
-    them."""
+    them.  `out` may not overlap `mats`."""
     if not mats:
         raise ValueError("no matrices")
     dt = dtype_code(mats[0].dtype)

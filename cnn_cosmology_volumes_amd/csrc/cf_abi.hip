@@ -871,6 +871,24 @@ cf_status cf_adam_larc(const cf_adam_larc_params* hp, int64_t t, int32_t ntensor
     return CF_OK;
 }
 
+// An argument's bytes.
+struct Span {
+    const void* at;
+    size_t bytes;
+    bool written;
+};
+
+// Whether something that is written shares bytes with another argument.
+static bool overlapping(const Span* s, int count)
+{
+    for (int i = 0; i < count; ++i)
+        for (int j = 0; j < i; ++j)
+            if ((s[i].written || s[j].written) && (uintptr_t)s[i].at < (uintptr_t)s[j].at + s[j].bytes &&
+                (uintptr_t)s[j].at < (uintptr_t)s[i].at + s[i].bytes)
+                return true;
+    return false;
+}
+
 // ------------------------------------------ Newton-Schulz products and Muon
 static cf_status check_ns(const cf_newton_schulz_params* ns, const char* fn)
 {
@@ -934,6 +952,15 @@ cf_status cf_newton_schulz(const cf_newton_schulz_params* ns, cf_dtype dtype, in
     const size_t need = ns_ws_bytes(l);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    Span span[2 * CF_MAX_OPT_TENSORS + 1];
+    int spans = 0;
+    for (int i = 0; i < nmat; ++i) {
+        const size_t bytes = (size_t)(rows[i] * cols[i]) * (dtype == CF_F32 ? 4 : 2);
+        span[spans++] = {x[i], bytes, false};
+        span[spans++] = {out[i], bytes, true};
+    }
+    span[spans++] = {ws, need, true};
+    if (overlapping(span, spans)) return fail(CF_ERR_INVALID, "%s: outputs or workspace overlap other arguments", fn);
     CF_TRY_HIP(dtype == CF_F32 ? launch_newton_schulz<float>(l, ns_coef(*ns), x, out, ws, stream)
                                : launch_newton_schulz<uint16_t>(l, ns_coef(*ns), x, out, ws, stream),
                "newton-schulz");
@@ -975,6 +1002,17 @@ cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, c
     const size_t need = muon_ws_bytes(l, hp->nesterov != 0);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    Span span[3 * CF_MAX_OPT_TENSORS + 1];
+    int spans = 0;
+    for (int i = 0; i < nmat; ++i) {
+        const size_t bytes = (size_t)(rows[i] * cols[i]) * sizeof(float);
+        span[spans++] = {w[i], bytes, true};
+        span[spans++] = {g[i], bytes, false};
+        span[spans++] = {m[i], bytes, true};
+    }
+    span[spans++] = {ws, need, true};
+    if (overlapping(span, spans))
+        return fail(CF_ERR_INVALID, "%s: weights, momenta or workspace overlap other arguments", fn);
     MuonArgs a{};
     a.momentum = hp->momentum;
     a.nesterov = hp->nesterov != 0;
@@ -1067,6 +1105,11 @@ static cf_status check_act(cf_act act, float slope, const char* fn)
     return CF_OK;
 }
 
+static size_t gn_bytes(cf_dtype dtype, const cf_dims& x)
+{
+    return (size_t)(x.n * x.d * x.h * x.w * x.c) * (dtype == CF_F32 ? 4 : 2);
+}
+
 size_t cf_groupnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t groups, int32_t backward)
 {
     if (check_gn(dtype, x, groups, "cf_groupnorm_workspace_size") != CF_OK) return 0;
@@ -1087,6 +1130,12 @@ cf_status cf_groupnorm_fwd(cf_dtype dtype, cf_dims x, const void* X, int32_t gro
     const size_t need = gn_ws_bytes(dtype, x, groups, false);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "cf_groupnorm_fwd: workspace %zu < %zu bytes", ws_bytes, need);
     if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: workspace null or misaligned");
+    const size_t bytes = gn_bytes(dtype, x), channels = (size_t)x.c * sizeof(float);
+    const size_t stats = (size_t)x.n * groups * sizeof(float);
+    const Span span[] = {{X, bytes, false}, {gamma, channels, false}, {beta, channels, false}, {Y, bytes, true},
+                         {mean, stats, true}, {rstd, stats, true}, {ws, need, true}};
+    if (overlapping(span, 7))
+        return fail(CF_ERR_INVALID, "cf_groupnorm_fwd: outputs or workspace overlap other arguments");
     hipError_t e = dtype == CF_F32
                        ? launch_gn_fwd<float>((const float*)X, gamma, beta, eps, act, slope, (float*)Y, mean, rstd, x,
                                               groups, ws, stream)
@@ -1112,6 +1161,13 @@ cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
     const size_t need = gn_ws_bytes(dtype, x, groups, true);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "cf_groupnorm_bwd: workspace %zu < %zu bytes", ws_bytes, need);
     if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "cf_groupnorm_bwd: workspace null or misaligned");
+    const size_t bytes = gn_bytes(dtype, x), channels = (size_t)x.c * sizeof(float);
+    const size_t stats = (size_t)x.n * groups * sizeof(float);
+    const Span span[] = {{X, bytes, false}, {dY, bytes, false}, {gamma, channels, false}, {beta, channels, false},
+                         {mean, stats, false}, {rstd, stats, false}, {dX, bytes, true}, {dgamma, channels, true},
+                         {dbeta, channels, true}, {ws, need, true}};
+    if (overlapping(span, 10))
+        return fail(CF_ERR_INVALID, "cf_groupnorm_bwd: outputs or workspace overlap other arguments");
     hipError_t e = dtype == CF_F32
                        ? launch_gn_bwd<float>((const float*)X, (const float*)dY, gamma, beta, mean, rstd, act, slope,
                                               (float*)dX, dgamma, dbeta, x, groups, ws, stream)

@@ -330,8 +330,9 @@ size_t cf_newton_schulz_workspace_size(cf_dtype dtype, int32_t nmat, const int64
  *   steps times, with A = X X^T:  X <- a X + (b A + c A A) X
  *   out[i] = X (dtype)
  * (rows > cols: the same on the transpose).  rows, cols, x and out are HOST
- * arrays; x and out entries are DEVICE pointers and must not overlap.  The
- * shorter side must be at most 16384 and a matrix at most 2^36 elements (else
+ * arrays; x and out entries are DEVICE pointers, and no out entry may overlap
+ * another one, an x entry or the workspace (CF_ERR_INVALID).  The shorter side
+ * must be at most 16384 and a matrix at most 2^36 elements (else
  * CF_ERR_UNSUPPORTED).  Products of fp32 accuracy or better throughout, also
  * for CF_BF16, whose results are rounded once; singular values of x below
  * 2^-24 |x|_F are fp32's rounding, and many steps can raise them to anything
@@ -364,7 +365,8 @@ size_t cf_muon_workspace_size(const cf_muon_params* hp, int32_t nmat, const int6
  *   m <- mu m + g;  u = g + mu m (nesterov) or m
  *   w <- w (1 - lr weight_decay) - lr scale(rows, cols) NewtonSchulz(u)
  * rows, cols, w, g, m are HOST arrays; w, g, m entries are DEVICE pointers
- * (m starts at zero).  Sizes as for cf_newton_schulz. */
+ * (m starts at zero), and no w or m entry may overlap any other argument
+ * (CF_ERR_INVALID).  Sizes as for cf_newton_schulz. */
 cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols, float* const* w,
                   const float* const* g, float* const* m, void* ws, size_t ws_bytes, hipStream_t stream);
 
@@ -417,7 +419,8 @@ size_t cf_groupnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t groups, in
  *   X, Y [x.n, x.d, x.h, x.w, x.c] (dtype); gamma, beta [x.c] fp32;
  *   mean, rstd [x.n, groups] fp32, outputs for the backward.
  * x.c must be a multiple of groups (else CF_ERR_INVALID) and at most 4096,
- * x.n at most 65535 (else CF_ERR_UNSUPPORTED); eps positive and finite.
+ * x.n at most 65535 (else CF_ERR_UNSUPPORTED); eps positive and finite.  Y,
+ * mean and rstd may not overlap any other argument (CF_ERR_INVALID).
  * Statistics are summed in fp64 in a fixed order: results are reproducible
  * bit for bit. */
 cf_status cf_groupnorm_fwd(cf_dtype dtype, cf_dims x, const void* X, int32_t groups, const float* gamma,
@@ -429,7 +432,8 @@ cf_status cf_groupnorm_fwd(cf_dtype dtype, cf_dims x, const void* X, int32_t gro
  * ReLU's derivative is slope at z <= 0):
  *   dbeta_c = sum dz;  dgamma_c = sum dz xhat     (over n, d, h, w; fp32)
  *   dX = rstd (gamma dz - s1 - xhat s2), s1 and s2 the group's sums of
- *   gamma dz and gamma dz xhat divided by M       (dtype) */
+ *   gamma dz and gamma dz xhat divided by M       (dtype)
+ * dX, dgamma and dbeta may not overlap any other argument (CF_ERR_INVALID). */
 cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void* dY, int32_t groups,
                            const float* gamma, const float* beta, const float* mean, const float* rstd, cf_act act,
                            float slope, void* dX, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
