@@ -4,6 +4,11 @@ torch tensors, outputs and workspaces are allocated with torch on the
 tensors' device, the call goes to the library on torch's current stream, and
 a non-zero status raises CfError.  Every step of the computation runs in the
 library's HIP kernels; there is no other code path.
+
+cf_groupnorm_fwd / _bwd, cf_newton_schulz and cf_muon check that tensors are on
+the current GPU.  With stream=s they make their outputs in s's memory; order s
+after what wrote the inputs, and the current stream after s before it reads the
+outputs (wait_stream).
 """
 import ctypes
 import os
@@ -512,6 +517,8 @@ def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
     them.  `out` may not overlap `mats`."""
     if not mats:
         raise ValueError("no matrices")
+    if stream is not None:
+        return _on_stream(stream, cf_newton_schulz, (*mats, *(out or ()), ws), ns, mats, out, ws)
     dt = dtype_code(mats[0].dtype)
     out = [torch.empty_like(t) for t in mats] if out is None else out
     if len(out) != len(mats):
@@ -520,11 +527,10 @@ def cf_newton_schulz(ns, mats, out=None, ws=None, stream=None):
         _packed("matrix %d" % i, t, mats[0].dtype)
         _packed("output %d" % i, o, t.dtype, t.shape)
     rows, cols = _mat_sizes(mats)
-    _on_gpu(ws, *mats, *out)
+    s = _on_gpu(ws, *mats, *out)
     ws = _ws(int(lib().cf_newton_schulz_workspace_size(dt, len(mats), rows, cols)), mats[0].device, ws)
     check(lib().cf_newton_schulz(ctypes.byref(ns), dt, len(mats), rows, cols, _pointers(mats), _pointers(out),
-                                 _ptr(ws), _wsbytes(ws), _stream(stream)))
-    _record(stream, ws, *out)
+                                 _ptr(ws), _wsbytes(ws), s))
     return out
 
 
@@ -534,16 +540,17 @@ def cf_muon(hp, params, grads, m, ws=None, stream=None):
     k = len(params)
     if not k or len(grads) != k or len(m) != k:
         raise ValueError("params, grads and m must be lists of one length, not empty")
+    if stream is not None:
+        return _on_stream(stream, cf_muon, (*params, *grads, *m, ws), hp, params, grads, m, ws)
     for i in range(k):
         _packed("param %d" % i, params[i], torch.float32)
         _packed("gradient %d" % i, grads[i], torch.float32, params[i].shape)
         _packed("momentum %d" % i, m[i], torch.float32, params[i].shape)
     rows, cols = _mat_sizes(params)
-    _on_gpu(ws, *params, *grads, *m)
+    s = _on_gpu(ws, *params, *grads, *m)
     ws = _ws(int(lib().cf_muon_workspace_size(ctypes.byref(hp), k, rows, cols)), params[0].device, ws)
     check(lib().cf_muon(ctypes.byref(hp), k, rows, cols, _pointers(params), _pointers(grads), _pointers(m), _ptr(ws),
-                        _wsbytes(ws), _stream(stream)))
-    _record(stream, ws)
+                        _wsbytes(ws), s))
 
 
 # --------------------------------------------------------------- batch norm
@@ -583,28 +590,39 @@ def _packed(name, t, dtype=None, shape=None):
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _on_gpu(ws, *tensors):
-    """Raises unless the workspace has no gaps and all tensors (or None) are on
-    one GPU, the current one: the kernels run there and take bare addresses."""
+def _on_gpu(ws, first, *others):
+    """The current stream, where all tensors (or None) are on its GPU, on which
+    the kernels take bare addresses, and the workspace has no gaps; else raises."""
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("tensors must be on one GPU: %s and %s" % (first.device, t.device))
     if ws is not None:
         _packed("ws", ws)
-    at = tensors[0].get_device()
+        if ws.get_device() != at:
+            raise ValueError("ws must be on the tensors' GPU: %s and %s" % (ws.device, first.device))
     if at < 0:
         raise ValueError("tensors must be on a GPU")
-    for t in (ws,) + tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError("tensors must be on one GPU: %s and %s" % (tensors[0].device, t.device))
-    if torch.cuda.is_initialized() and torch.cuda.current_device() != at:
-        raise ValueError("tensors are on GPU %d, the current one is %d" % (at, torch.cuda.current_device()))
+    if torch.cuda.current_device() != at:
+        raise ValueError("tensors and stream must be on the current GPU: %d and %d" % (at, torch.cuda.current_device()))
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(at)
 
 
-def _record(stream, *tensors):
-    """Tensors made here on the current stream and used on `stream`: their
-    memory is not reused before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on_stream(stream, call, given, *args):
+    """call(*args) on another stream than the current one.  What the call makes
+    is made in that stream's memory: the current stream's may still be in use
+    there.  Nothing has its memory reused before both streams are done with it;
+    for the values of the `given` tensors and of the outputs the caller orders
+    the streams (wait_stream)."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in given:
+        if t is not None:
+            t.record_stream(stream)
+    for t in out or ():
+        t.record_stream(here)
+    return out
 
 
 # --------------------------------------------------------------- group norm
@@ -616,6 +634,9 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
                      stream=None):
     """Group norm of NDHWC X, then the activation -> (Y, mean [N, groups],
     rstd [N, groups])."""
+    if stream is not None:
+        return _on_stream(stream, cf_groupnorm_fwd, (X, gamma, beta, Y, mean, rstd, ws), X, groups, gamma, beta, eps, act,
+                          slope, Y, mean, rstd, ws)
     dt, d, groups = dtype_code(X.dtype), cf_dims(*X.shape), int(groups)
     _packed("X", X)
     _packed("gamma", gamma, torch.float32, (d.c,))
@@ -623,23 +644,24 @@ def cf_groupnorm_fwd(X, groups, gamma, beta, eps, act=CF_ACT_LRELU, slope=1.0, Y
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t is not None:
             _packed(name, t, torch.float32, (d.n, groups))
-    if Y is None:
-        Y = torch.empty_like(X)
-    else:
+    if Y is not None:
         _packed("Y", Y, X.dtype, X.shape)
-    _on_gpu(ws, X, gamma, beta, Y, mean, rstd)
+    s = _on_gpu(ws, X, gamma, beta, Y, mean, rstd)
+    Y = torch.empty_like(X) if Y is None else Y
     mean = gamma.new_empty((d.n, groups)) if mean is None else mean
     rstd = torch.empty_like(mean) if rstd is None else rstd
     ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 0)), X.device, ws)
     check(lib().cf_groupnorm_fwd(dt, d, _ptr(X), groups, _ptr(gamma), _ptr(beta), float(eps), int(act), float(slope),
-                                 _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), _stream(stream)))
-    _record(stream, Y, mean, rstd, ws)
+                                 _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(ws), _wsbytes(ws), s))
     return Y, mean, rstd
 
 
 def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, slope=1.0, dX=None, ws=None,
                      stream=None):
     """-> (dX, dgamma, dbeta) from the forward's mean and rstd."""
+    if stream is not None:
+        return _on_stream(stream, cf_groupnorm_bwd, (X, dY, gamma, beta, mean, rstd, dX, ws), X, dY, groups, gamma, beta,
+                          mean, rstd, act, slope, dX, ws)
     dt, d, groups = dtype_code(X.dtype), cf_dims(*X.shape), int(groups)
     _packed("X", X)
     _packed("dY", dY, X.dtype, X.shape)
@@ -647,17 +669,14 @@ def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, s
     _packed("beta", beta, torch.float32, (d.c,))
     _packed("mean", mean, torch.float32, (d.n, groups))
     _packed("rstd", rstd, torch.float32, (d.n, groups))
-    if dX is None:
-        dX = torch.empty_like(X)
-    else:
+    if dX is not None:
         _packed("dX", dX, X.dtype, X.shape)
-    _on_gpu(ws, X, dY, gamma, beta, mean, rstd, dX)
+    s = _on_gpu(ws, X, dY, gamma, beta, mean, rstd, dX)
+    dX = torch.empty_like(X) if dX is None else dX
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
     ws = _ws(int(lib().cf_groupnorm_workspace_size(dt, d, groups, 1)), X.device, ws)
     check(lib().cf_groupnorm_bwd(dt, d, _ptr(X), _ptr(dY), groups, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
-                                 int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws),
-                                 _stream(stream)))
-    _record(stream, dX, dgamma, dbeta, ws)
+                                 int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws), s))
     return dX, dgamma, dbeta
 
 
