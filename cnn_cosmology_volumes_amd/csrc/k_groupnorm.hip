@@ -21,8 +21,10 @@
 // sample go element by element.
 //
 // Sums: the forward adds x and x^2 in fp64 (products of fp32 values are exact
-// there up to one rounding), so a mean far above the spread costs no digits;
-// the backward adds fp32 products in fp64.  Blocks write partial sums that
+// there up to one rounding): the variance keeps about 52 - 2 log2(mean /
+// spread) bits, and x - mean is taken with the fp64 mean, whose part below
+// fp32 is folded into the offset.  The backward starts from the fp32 mean and
+// adds fp32 products in fp64.  Blocks write partial sums that
 // are added in a fixed order: no atomics, results are reproducible bit for
 // bit.
 //
@@ -175,12 +177,14 @@ __host__ __device__ __forceinline__ int same_group(int cg, int V)
     return l;
 }
 
-// Mean and 1 / sqrt(var + eps) from fp64 sums of x and x^2 over M values.
-__device__ __forceinline__ float2 moments(double s, double ss, double M, float eps)
+// Mean and 1 / sqrt(var + eps) from fp64 sums of x and x^2 over M values; low:
+// what the fp32 mean lacks.
+__device__ __forceinline__ float2 moments(double s, double ss, double M, float eps, float& low)
 {
     const double mu = s / M;
     double var = ss / M - mu * mu;
     if (var < 0.0) var = 0.0;
+    low = (float)(mu - (double)(float)mu);
     return make_float2((float)mu, (float)(1.0 / sqrt(var + (double)eps)));
 }
 
@@ -280,8 +284,9 @@ __global__ __launch_bounds__(GN_T) void gn_stats_kernel(const T* __restrict__ X,
     }
 }
 
-// y = act((x - mean) (rstd gamma) + beta).  Every block first adds its
-// sample's partial sums (npart of them per group, in the same order).
+// y = act((x - mean) (rstd gamma) + beta), with the mean's low part in beta.
+// Every block first adds its sample's partial sums (npart of them per group, in
+// the same order).
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X, GnGeom q, int npart,
                                                         const double2* __restrict__ part,
@@ -290,7 +295,8 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
                                                         T* __restrict__ Y, float* __restrict__ mean,
                                                         float* __restrict__ rstd)
 {
-    extern __shared__ float2 stat[];     // [G] mean, rstd
+    extern __shared__ float2 stat[];     // [G] mean, rstd; then [G] the mean's low parts
+    float* lows = reinterpret_cast<float*>(stat + q.G);
     const int t = (int)threadIdx.x, n = (int)blockIdx.z;
     const int r = t / q.cc, col = (int)blockIdx.y * q.cc + t % q.cc;
     const bool on = r < q.k && col < q.cols;
@@ -328,8 +334,10 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
         s = wave_sum(s);
         ss = wave_sum(ss);
         if ((t & 63) == 0) {
-            const float2 m = moments(s, ss, (double)(q.S / q.C) * q.cg, eps);
+            float low;
+            const float2 m = moments(s, ss, (double)(q.S / q.C) * q.cg, eps, low);
             stat[g] = m;
+            lows[g] = low;
             if (blockIdx.x == 0 && blockIdx.y == 0) {
                 mean[(int64_t)n * q.G + g] = m.x;
                 rstd[(int64_t)n * q.G + g] = m.y;
@@ -345,7 +353,7 @@ __global__ __launch_bounds__(GN_T) void gn_apply_kernel(const T* __restrict__ X,
         const float2 m = stat[ch.g];
         mu[j] = m.x;
         sc[j] = m.y * gamma[ch.c];
-        be[j] = beta[ch.c];
+        be[j] = fmaf(-lows[ch.g], sc[j], beta[ch.c]);
         ch.next(q.C, q.cg);
     }
     auto out1 = [&](int j, T w) { return act_fwd<ACT>(fmaf(wide(w) - mu[j], sc[j], be[j]), slope); };
@@ -613,7 +621,8 @@ __global__ __launch_bounds__(V == 8 ? GN_T : GN_TS) void gn_small_kernel(const T
     extern __shared__ double sh[];
     const int t = (int)threadIdx.x, r = t / q.cols, col = t % q.cols, n = (int)blockIdx.y;
     const int W = q.gs * q.cg, c0 = (int)blockIdx.x * W, g0 = (int)blockIdx.x * q.gs;
-    float2* stat = reinterpret_cast<float2*>(sh + q.k * W);      // [gs] mean, rstd; then [gs] sums of x
+    float2* stat = reinterpret_cast<float2*>(sh + q.k * W);      // [gs] mean, rstd; then [gs] sums of x, in whose
+                                                                 // place the mean's low parts come
     const int64_t at = (int64_t)n * q.S + c0 + (int64_t)col * V;
     const double M = (double)q.nrows * q.cg;
     Vec<T, V> u[GN_ROWS_F];
@@ -655,8 +664,10 @@ __global__ __launch_bounds__(V == 8 ? GN_T : GN_TS) void gn_small_kernel(const T
         b.parts = fold_rows(sh, nv, q.k, q.cols);
     }
     groups(b, [&](int g, double v) {
-        const float2 m = moments(sh[q.k * W + q.gs + g], v, M, eps);
+        float low;
+        const float2 m = moments(sh[q.k * W + q.gs + g], v, M, eps, low);
         stat[g] = m;
+        sh[q.k * W + q.gs + g] = (double)low;
         mean[(int64_t)n * q.G + g0 + g] = m.x;
         rstd[(int64_t)n * q.G + g0 + g] = m.y;
     });
@@ -669,7 +680,7 @@ __global__ __launch_bounds__(V == 8 ? GN_T : GN_TS) void gn_small_kernel(const T
         const float2 m = stat[ch.g];
         mu[j] = m.x;
         sc[j] = m.y * gamma[c0 + col * V + j];
-        be[j] = beta[c0 + col * V + j];
+        be[j] = fmaf(-(float)sh[q.k * W + q.gs + ch.g], sc[j], beta[c0 + col * V + j]);
         ch.next(W, q.cg);
     }
 #pragma unroll
@@ -973,7 +984,7 @@ hipError_t run_fwd(const T* X, const float* gamma, const float* beta, float eps,
                        (size_t)q.k * q.cc * (2 * V >> same_group(q.cg, V)) * sizeof(double), s, X, q, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gn_apply_kernel<T, V, ACT>), grid, block, (size_t)G * sizeof(float2), s, X, q,
+    hipLaunchKernelGGL((gn_apply_kernel<T, V, ACT>), grid, block, (size_t)G * (sizeof(float2) + sizeof(float)), s, X, q,
                        q.nb * q.chunks, (const double2*)part, gamma, beta, eps, slope, Y, mean, rstd);
     return hipGetLastError();
 }
