@@ -250,10 +250,11 @@ __host__ __device__ inline int64_t ns_plane(int m) { return (int64_t)ns_ld(m) * 
 // split, then the groups are added in order; scales by s^2 and writes the
 // element and its mirror.  Block 0 of a matrix also stores s.  The diagonal is
 // raised by `lift` times the trace.
-__global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, float eps, double lift, double* ws, double* scale)
+__global__ __launch_bounds__(NS_T) void ns_join_kernel(SquareArgs g, int first, float eps, double lift, double* ws,
+                                                       double* scale)
 {
     __shared__ double red[4], group[4][NS_TILE];
-    const int q = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[q];
+    const int block = first + (int)blockIdx.x, q = find(g.start, block), b = block - g.start.at[q];
     const int m = g.m[q], splits = g.splits[q], ld = ns_ld(m), nt = ld / NS_TILE, pairs = nt * (nt + 1) / 2;
     const double* part = ws + g.part[q];
     const int p = b / NS_TILE, i = b % NS_TILE, j = (int)threadIdx.x % NS_TILE, w = (int)threadIdx.x / NS_TILE;
@@ -549,10 +550,10 @@ __device__ void final_tile(const T* U, const uint16_t* Q, double s, int m, int n
 }
 
 template <typename T, typename F>
-__global__ __launch_bounds__(NS_T) void ns_final_kernel(FinalArgs g, F f, const double* ws, const double* scale)
+__global__ __launch_bounds__(NS_T) void ns_final_kernel(FinalArgs g, int first, F f, const double* ws, const double* scale)
 {
     __shared__ __attribute__((aligned(16))) uint16_t sh[6 * NF_PLANE];
-    const int i = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[i];
+    const int block = first + (int)blockIdx.x, i = find(g.start, block), b = block - g.start.at[i];
     const T* U = (const T*)g.u[i];
     const uint16_t* Q = (const uint16_t*)(ws + g.q[i]);
     if (g.tall >> i & 1) final_tile<true>(U, Q, scale[i], g.m[i], g.n[i], b, f, i, sh);
@@ -626,10 +627,11 @@ __device__ void final64_tile(const T* U, const double* Q, double s, int m, int n
 }
 
 template <typename T, typename F>
-__global__ __launch_bounds__(NS_T) void ns_final64_kernel(FinalArgs g, F f, const double* ws, const double* scale)
+__global__ __launch_bounds__(NS_T) void ns_final64_kernel(FinalArgs g, int first, F f, const double* ws,
+                                                          const double* scale)
 {
     __shared__ float sh[NS_PANEL];
-    const int i = find(g.start, (int)blockIdx.x), b = (int)blockIdx.x - g.start.at[i];
+    const int block = first + (int)blockIdx.x, i = find(g.start, block), b = block - g.start.at[i];
     const T* U = (const T*)g.u[i];
     if (g.tall >> i & 1) final64_tile<true>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
     else final64_tile<false>(U, ws + g.q[i], scale[i], g.m[i], g.n[i], b, f, i, sh);
@@ -914,6 +916,21 @@ NsPlan ns_plan(const NsShapes& l)
 bool ns_many(const NsCoef& c) { return std::fabs(c.a) > 1.f && 2.0 * c.steps * std::log2(std::fabs((double)c.a)) > 29.0; }
 constexpr double NS_LIFT = 0x1p-48;
 
+// Calls launch(first block, blocks) over a launch's blocks: more than once
+// where they have 2^32 threads or more, which one launch may not (a matrix of
+// 1 x 2^30 has 2^24 tiles).
+template <typename L> hipError_t in_launches(int blocks, const L& launch)
+{
+    constexpr int most = (1 << 24) - 1;
+    static_assert((int64_t)most * NS_T < (int64_t)1 << 32, "threads of a launch");
+    for (int at = 0; at < blocks; at += most) {
+        launch(at, dim3((unsigned)std::min(most, blocks - at)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Everything of a list from U on.
 template <typename T, typename F>
 hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, const F& f, double* ws, hipStream_t s)
@@ -973,8 +990,10 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
     hipLaunchKernelGGL(ns_gram_kernel<T>, dim3((unsigned)grams), dim3(NS_T), 0, s, g, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ns_join_kernel, dim3((unsigned)joins), dim3(NS_T), 0, s, sq, c.eps, lift, ws, ws);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = in_launches(joins, [&](int first, dim3 grid) {
+        hipLaunchKernelGGL(ns_join_kernel, grid, dim3(NS_T), 0, s, sq, first, c.eps, lift, ws, ws);
+    });
+    if (e != hipSuccess) return e;
 
     int A = 0, T_ = 1, P = 2, Q = 3, R = 4;      // buffers: A_k, P A, P_k, Q and a free one
     if (maxm <= NB_M) {
@@ -1019,9 +1038,10 @@ hipError_t ns_f64(const NsShapes& l, const void* const* u, const NsCoef& c, cons
         }
     }
     for (int i = 0; i < l.count; ++i) a.q[i] = p.sq[i] + Q * ns_size(l.m[i]);
-    if (many) hipLaunchKernelGGL((ns_final64_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
-    else hipLaunchKernelGGL((ns_final_kernel<T, F>), dim3((unsigned)finals), dim3(NS_T), 0, s, a, f, ws, ws);
-    return hipGetLastError();
+    return in_launches(finals, [&](int first, dim3 grid) {
+        if (many) hipLaunchKernelGGL((ns_final64_kernel<T, F>), grid, dim3(NS_T), 0, s, a, first, f, ws, ws);
+        else hipLaunchKernelGGL((ns_final_kernel<T, F>), grid, dim3(NS_T), 0, s, a, first, f, ws, ws);
+    });
 }
 
 // The matrices of a list that take the fp64 launches together, and those that
