@@ -985,7 +985,7 @@ static cf_status check_muon(const cf_muon_params* hp, int32_t nmat, const int64_
 size_t cf_muon_workspace_size(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols)
 {
     if (check_muon(hp, nmat, rows, cols, "cf_muon_workspace_size") != CF_OK) return 0;
-    return muon_ws_bytes(ns_shapes(nmat, rows, cols), hp->nesterov != 0);
+    return muon_ws_bytes(ns_shapes(nmat, rows, cols), ns_coef(hp->ns), hp->nesterov != 0);
 }
 
 cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols, float* const* w,
@@ -999,7 +999,7 @@ cf_status cf_muon(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, c
         if (!w[i] || !g[i] || !m[i] || !al16(w[i]) || !al16(g[i]) || !al16(m[i]))
             return fail(CF_ERR_INVALID, "%s: matrix %d has a null or misaligned pointer", fn, i);
     const NsShapes l = ns_shapes(nmat, rows, cols);
-    const size_t need = muon_ws_bytes(l, hp->nesterov != 0);
+    const size_t need = muon_ws_bytes(l, ns_coef(hp->ns), hp->nesterov != 0);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
     Span span[3 * CF_MAX_OPT_TENSORS + 1];

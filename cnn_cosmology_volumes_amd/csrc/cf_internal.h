@@ -347,7 +347,8 @@ struct MuonArgs {
     float rate[CF_MAX_OPT_TENSORS];     // lr times the matrix's scale
 };
 size_t ns_ws_bytes(const NsShapes& l);
-size_t muon_ws_bytes(const NsShapes& l, bool nesterov);
+size_t ns_ws_bytes(const NsShapes& l, const NsCoef& c);
+size_t muon_ws_bytes(const NsShapes& l, const NsCoef& c, bool nesterov);
 template <typename T>
 hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* const* x, void* const* out, void* ws,
                                 hipStream_t s);

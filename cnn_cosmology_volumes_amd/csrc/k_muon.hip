@@ -1077,15 +1077,21 @@ size_t ns_f64_ws_bytes(const NsShapes& l) { return l.count ? up256b((size_t)ns_p
 
 }  // namespace
 
-// The sizes alone fix the workspace: the larger of what any coefficients need.
-size_t ns_ws_bytes(const NsShapes& l)
+namespace {
+size_t ns_parts_ws_bytes(const NsShapes& l, const NsParts& p)
 {
-    size_t b = ns_f64_ws_bytes(l);
-    const NsParts p = ns_parts(l, true);
-    b = std::max(b, ns_f64_ws_bytes(p.f64));
+    size_t b = ns_f64_ws_bytes(p.f64);
     for (int i = 0; i < p.splits; ++i) b = std::max(b, ns_split_ws_bytes(l.m[p.split[i]], l.n[p.split[i]]));
     return b;
 }
+}  // namespace
+
+// What any coefficients need at most, and what these need.
+size_t ns_ws_bytes(const NsShapes& l)
+{
+    return std::max(ns_parts_ws_bytes(l, ns_parts(l, false)), ns_parts_ws_bytes(l, ns_parts(l, true)));
+}
+size_t ns_ws_bytes(const NsShapes& l, const NsCoef& c) { return ns_parts_ws_bytes(l, ns_parts(l, ns_split_coef(c))); }
 
 template <typename T>
 hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* const* x, void* const* out, void* ws,
@@ -1109,9 +1115,9 @@ hipError_t launch_newton_schulz(const NsShapes& l, const NsCoef& c, const void* 
     return ns_f64<T>(p.f64, u, c, f, (double*)ws, s);
 }
 
-size_t muon_ws_bytes(const NsShapes& l, bool nesterov)
+size_t muon_ws_bytes(const NsShapes& l, const NsCoef& c, bool nesterov)
 {
-    size_t b = ns_ws_bytes(l);
+    size_t b = ns_ws_bytes(l, c);
     if (nesterov)
         for (int i = 0; i < l.count; ++i) b += up256b((size_t)l.m[i] * l.n[i] * sizeof(float));
     return b;
@@ -1122,7 +1128,7 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
 {
     MomentumArgs a{};
     const float* u[CF_MAX_OPT_TENSORS];
-    char* at = (char*)ws + ns_ws_bytes(l);
+    char* at = (char*)ws + ns_ws_bytes(l, c);
     a.start.clear();
     int blocks = 0;
     for (int i = 0; i < l.count; ++i) {

@@ -321,7 +321,8 @@ typedef struct {
 } cf_newton_schulz_params;
 
 /* Workspace bytes for cf_newton_schulz over matrices of these sizes (HOST
- * arrays; dtype as there).  Returns 0 for invalid arguments. */
+ * arrays; dtype as there), enough for any parameters.  Returns 0 for invalid
+ * arguments. */
 size_t cf_newton_schulz_workspace_size(cf_dtype dtype, int32_t nmat, const int64_t* rows, const int64_t* cols);
 
 /* The nearly orthogonal factor of each of nmat (1..CF_MAX_OPT_TENSORS)
@@ -357,7 +358,8 @@ typedef struct {
     cf_newton_schulz_params ns;
 } cf_muon_params;
 
-/* Workspace bytes for cf_muon. */
+/* Workspace bytes for cf_muon with these parameters.  Returns 0 for invalid
+ * arguments. */
 size_t cf_muon_workspace_size(const cf_muon_params* hp, int32_t nmat, const int64_t* rows, const int64_t* cols);
 
 /* One Muon update of nmat fp32 weight matrices in place.  Conv weights
