@@ -15,7 +15,10 @@
 // fp16 products run at a third of 2.5 PFLOP/s, five times the fp32 matrix
 // rate.  The scales come from the host: the iteration's polynomial bounds every
 // singular value, and so every element, of every step's X, A and P
-// (ns_bounds); coefficients without a small bound take the fp64 path.
+// (ns_bounds); coefficients without a small bound take the fp64 path.  Where
+// |U| is below eps, X_0 is small and so are the next steps' X, by more than
+// the host can know: a power of two on top of each step's scale, found on the
+// device (sp_lift), keeps their digits.
 //
 // Layout: a row is cut into pieces of 32 values, each one 128-byte line, the
 // 32 hi and then the 32 lo.  Both operands of a product are read along their
@@ -81,6 +84,7 @@ struct SpProduct {
                             // the small terms is rounded at its own size
     int m, n;
     float f, g, diag;
+    const float* lift;      // what f and g are multiplied by (but for SP_GRAM)
     const uint16_t* s;
     uint16_t* d;
     uint16_t* dt;
@@ -126,8 +130,8 @@ __device__ __forceinline__ void sp_wave_sync()
 // SP_POLY adds S, and leaves the sums in LDS for the mirror; else the block is
 // multiplied by f.
 template <int MODE>
-__device__ __forceinline__ void sp_put(float* sh, bool flip, float f, const SpProduct& q, uint16_t* d, int kd, int r0,
-                                       int c0, int rows, int cols)
+__device__ __forceinline__ void sp_put(float* sh, bool flip, float f, float g, const SpProduct& q, uint16_t* d, int kd,
+                                       int r0, int c0, int rows, int cols)
 {
     const int lane = (int)threadIdx.x & 63, chunk = lane & 7, k8 = (chunk & 3) * 8;
     if (c0 >= kd * SP_K) return;
@@ -149,7 +153,7 @@ __device__ __forceinline__ void sp_put(float* sh, bool flip, float f, const SpPr
         for (int j = 0; j < 8; ++j) {
             float v = f * (flip ? sh[(k8 + j) * SP_SB + r] : sh[r * SP_SB + k8 + j]);
             if (MODE == SP_POLY) {
-                v = fmaf(q.g, (float)hi[it][j] + (float)lo[it][j], v);
+                v = fmaf(g, (float)hi[it][j] + (float)lo[it][j], v);
                 if (r0 + r == c0 + k8 + j) v += q.diag;
                 sums[it][j] = v;
             }
@@ -194,11 +198,18 @@ template <typename T, typename F> struct SpFinal {
     int tall;
 };
 
+// f and g of a product, with the lifts of its operands and its result.
+template <int MODE> __device__ __forceinline__ float2 sp_factors(const SpProduct& q)
+{
+    if (MODE == SP_GRAM) return make_float2(q.f, 0.f);
+    return make_float2(q.f * q.lift[0], MODE == SP_POLY ? q.g * q.lift[1] : 0.f);
+}
+
 // One 32 x 32 block of the product in a wave's registers, at row block bi and
-// column block bj of C; sh: this wave's 32 x SP_SB floats.
+// column block bj of C; sh: this wave's 32 x SP_SB floats; fg: sp_factors.
 template <int MODE, typename T, typename F>
 __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpProduct& q, const SpFinal<T, F>& fin,
-                                         int bi, int bj)
+                                         float2 fg, int bi, int bj)
 {
     const int i0 = bi * 32, j0 = bj * 32, lane = (int)threadIdx.x & 63;
     if (i0 >= q.m || j0 >= q.n || (q.sym && bi > bj)) return;
@@ -207,15 +218,15 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
     for (int r = 0; r < 16; ++r) sh[(8 * (r / 4) + 4 * (lane / 32) + r % 4) * SP_SB + lane % 32] = acc[r];
     sp_wave_sync();
     if constexpr (MODE == SP_GRAM || MODE == SP_POLY) {
-        sp_put<MODE>(sh, false, q.f, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
+        sp_put<MODE>(sh, false, fg.x, fg.y, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
         if (bi < bj) {
             // (S is symmetric: the mirror's sums are the same)
             if (MODE == SP_POLY) sp_wave_sync();
-            sp_put<SP_GRAM>(sh, true, MODE == SP_POLY ? 1.f : q.f, q, q.d, pieces(q.n), j0, i0, q.m, q.n);
+            sp_put<SP_GRAM>(sh, true, MODE == SP_POLY ? 1.f : fg.x, 0.f, q, q.d, pieces(q.n), j0, i0, q.m, q.n);
         }
     } else if constexpr (MODE == SP_BOTH) {
-        sp_put<MODE>(sh, false, q.f, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
-        sp_put<MODE>(sh, true, q.f, q, q.dt, pieces(q.m), j0, i0, q.n, q.m);
+        sp_put<MODE>(sh, false, fg.x, 0.f, q, q.d, pieces(q.n), i0, j0, q.m, q.n);
+        sp_put<MODE>(sh, true, fg.x, 0.f, q, q.dt, pieces(q.m), j0, i0, q.n, q.m);
     } else {
         const int c = lane % 32, x0 = fin.tall ? j0 : i0, y0 = fin.tall ? i0 : j0;
         const int rows = fin.tall ? q.n : q.m, cols = fin.tall ? q.m : q.n;
@@ -228,7 +239,7 @@ __device__ __forceinline__ void sp_block(const f32x16& acc, float* sh, const SpP
 #pragma unroll
         for (int it = 0; it < 16; ++it) {
             const int r = it * 2 + lane / 32;
-            w[it] = sp_result(fin.f, q.f * (fin.tall ? sh[c * SP_SB + r] : sh[r * SP_SB + c]), w[it]);
+            w[it] = sp_result(fin.f, fg.x * (fin.tall ? sh[c * SP_SB + r] : sh[r * SP_SB + c]), w[it]);
             asm volatile("" : "+v"(w[it]));      // computed before the stores
         }
 #pragma unroll
@@ -364,6 +375,7 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int group = wave / S::GW, w = wave % S::GW;
     const int b = (int)xcd_remap(blockIdx.x, (uint32_t)q.grid);
+    const float2 fg = sp_factors<MODE>(q);
     const int64_t u1 = sp_first(q, b + 1), ld = (int64_t)row_lines(q.kb) * 128;      // bytes from row to row
     uint32_t off[2];
 #pragma unroll
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(64 * SpShape<TILE>::WAVES) void sp_product_kernel(S
             for (int i = 0; i < DONE; ++i)
 #pragma unroll
                 for (int j = 0; j < S::NJ; ++j)
-                    sp_block<MODE>(total[i][j], sh, q, fin, ti * E + wi + i0 + i, tj * E + wj + j);
+                    sp_block<MODE>(total[i][j], sh, q, fin, fg, ti * E + wi + i0 + i, tj * E + wj + j);
         } else {
             // [block of 32 x 32][quarter of a lane's registers][lane]
             float4* out = reinterpret_cast<float4*>(q.part + ((int64_t)b * 2 + seg) * (TILE * TILE));
@@ -556,6 +568,7 @@ __global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int ti, tj;
     sp_tile_at(q, (int)xcd_remap(blockIdx.x, gridDim.x), ti, tj);
+    const float2 fg = sp_factors<MODE>(q);
     const int64_t ld = (int64_t)row_lines(q.kb) * 128;
     uint32_t off[2];
 #pragma unroll
@@ -633,7 +646,7 @@ __global__ __launch_bounds__(256) void sp_small_kernel(SpProduct q, SpFinal<T, F
             total[4 * v + 2] += x.z;
             total[4 * v + 3] += x.w;
         }
-    sp_block<MODE>(total, reinterpret_cast<float*>(sb) + wave * (32 * SP_SB), q, fin, ti * 2 + wave / 2, tj * 2 + wave % 2);
+    sp_block<MODE>(total, reinterpret_cast<float*>(sb) + wave * (32 * SP_SB), q, fin, fg, ti * 2 + wave / 2, tj * 2 + wave % 2);
 }
 
 // Adds the partial sums of the tiles that several blocks share.  A wave takes
@@ -688,7 +701,7 @@ __global__ __launch_bounds__(256) void sp_join_kernel(SpProduct q, SpFinal<T, F>
     }
     int ti, tj;
     sp_tile_at(q, t, ti, tj);
-    sp_block<MODE>(acc, shared[wave], q, fin, ti * edge + blk / edge, tj * edge + blk % edge);
+    sp_block<MODE>(acc, shared[wave], q, fin, sp_factors<MODE>(q), ti * edge + blk / edge, tj * edge + blk % edge);
 }
 
 // Tiles and blocks of a product: those of least estimated time, in
@@ -799,17 +812,42 @@ template <typename T> __global__ __launch_bounds__(256) void sp_norm_kernel(cons
     if (threadIdx.x == 0) part[blockIdx.x] = a;
 }
 
-// X0 = U / (|U|_F + eps) in both layouts; a wave takes 32 x 32 elements.
+// The lift of X_k, log2: |X_k| is at most r = |U| / (|U| + eps) times the
+// product of the bounds of P_0 .. P_{k-1}, and room[k] is X_k's bound over that
+// product.  A is lifted twice as much, P not.  (Factors of f and g that
+// underflow belong to terms that far below a I; up to 2^90, so that the last
+// product's f, 2^-30, stays a normal number.)
+constexpr int SP_STEPS = 32;
+struct SpRoom {
+    int steps;
+    float room[SP_STEPS];
+};
+__device__ __forceinline__ int sp_lift(float room, double r)
+{
+    const double l = (double)room / r;
+    return l >= 2.0 ? min(ilogb(l), 90) : 0;      // (0 also where r is no number)
+}
+
+// X0 = U / (|U|_F + eps) in both layouts; a wave takes 32 x 32 elements.  Block
+// 0 also writes the lifts: of each step's f and g of P, and of f of P X.
 template <typename T>
 __global__ __launch_bounds__(256) void sp_split_kernel(const T* u, int rows, int cols, const double* part, float eps,
-                                                       float scale, SpProduct q, int tall)
+                                                       float scale, SpProduct q, int tall, SpRoom room, float* lift)
 {
     __shared__ double red[4];
     __shared__ float shared[4][32 * SP_SB];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     double a = 0.0;
     for (int i = (int)threadIdx.x; i < SP_NORM; i += 256) a += part[i];
-    const double s = (double)scale / (sqrt(sp_block_sum(a, red)) + (double)eps);
+    const double norm = sqrt(sp_block_sum(a, red)), r = norm / (norm + (double)eps);
+    const double s = ldexp((double)scale, sp_lift(room.room[0], r)) / (norm + (double)eps);
+    if (blockIdx.x == 0 && (int)threadIdx.x < room.steps) {
+        const int k = (int)threadIdx.x, now = sp_lift(room.room[k], r);
+        const int next = k + 1 < room.steps ? sp_lift(room.room[k + 1], r) : 0;
+        lift[3 * k] = (float)ldexp(1.0, -4 * now);
+        lift[3 * k + 1] = (float)ldexp(1.0, -2 * now);
+        lift[3 * k + 2] = (float)ldexp(1.0, next - now);
+    }
     const int bc = pieces(cols);
     const int64_t blk = (int64_t)blockIdx.x * 4 + wave;
     const int64_t br = blk / bc;
@@ -824,15 +862,15 @@ __global__ __launch_bounds__(256) void sp_split_kernel(const T* u, int rows, int
         sh[r * SP_SB + c] = v;
     }
     sp_wave_sync();
-    sp_put<SP_BOTH>(sh, false, 1.f, q, tall ? q.dt : q.d, bc, r0, c0, rows, cols);
-    sp_put<SP_BOTH>(sh, true, 1.f, q, tall ? q.d : q.dt, pieces(rows), c0, r0, cols, rows);
+    sp_put<SP_BOTH>(sh, false, 1.f, 0.f, q, tall ? q.dt : q.d, bc, r0, c0, rows, cols);
+    sp_put<SP_BOTH>(sh, true, 1.f, 0.f, q, tall ? q.d : q.dt, pieces(rows), c0, r0, cols, rows);
 }
 
 // -------------------------------------------------------------------- plan
 // Bounds of the singular values of X_k and of the eigenvalues of P_k.
 struct SpBounds {
     bool fits;
-    double x[33], p[32];
+    double x[SP_STEPS + 1], p[SP_STEPS];
 };
 
 SpBounds ns_bounds(const NsCoef& c)
@@ -871,7 +909,7 @@ SpBounds ns_bounds(const NsCoef& c)
 double sp_scale(double bound) { return std::ldexp(1.0, (int)std::floor(std::log2(32768.0 / std::max(bound, 1e-3)))); }
 
 struct SpLayout {
-    size_t norm, x, xt[2], a, p, part, bytes;
+    size_t norm, lift, x, xt[2], a, p, part, bytes;
 };
 SpLayout sp_layout(int m, int n)
 {
@@ -884,6 +922,7 @@ SpLayout sp_layout(int m, int n)
         return r;
     };
     l.norm = take(SP_NORM * sizeof(double));
+    l.lift = take(3 * SP_STEPS * sizeof(float));
     l.x = take(rows(m) * row_lines(pieces(n)) * 128);
     l.xt[0] = take(rows(n) * row_lines(pieces(m)) * 128);
     l.xt[1] = take(rows(n) * row_lines(pieces(m)) * 128);
@@ -900,6 +939,7 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
     const SpLayout l = sp_layout(m, n);
     const SpBounds bd = ns_bounds(c);
     double* norm = (double*)(ws + l.norm);
+    float* lift = (float*)(ws + l.lift);
     uint16_t* X = (uint16_t*)(ws + l.x);
     uint16_t* XT[2] = {(uint16_t*)(ws + l.xt[0]), (uint16_t*)(ws + l.xt[1])};
     uint16_t* A = (uint16_t*)(ws + l.a);
@@ -914,9 +954,16 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
     if (e != hipSuccess) return e;
     q.d = X;
     q.dt = XT[0];
+    SpRoom room{};
+    room.steps = c.steps;
+    double grown = 1.0;      // the bounds of the P before
+    for (int k = 0; k < c.steps; ++k) {
+        room.room[k] = (float)(bd.x[k] / grown);
+        grown *= bd.p[k];
+    }
     const int64_t blocks = ((int64_t)pieces(rows) * pieces(cols) + 3) / 4;
     hipLaunchKernelGGL(sp_split_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, s, u, rows, cols, norm, c.eps,
-                       (float)sx, q, (int)tall);
+                       (float)sx, q, (int)tall, room, lift);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
     const SpFinal<float, SpNone> none{};
@@ -935,10 +982,12 @@ hipError_t sp_newton_schulz(int m, int n, bool tall, const NsCoef& c, const T* u
         q.f = (float)(sp * c.c / (sa * sa));
         q.g = (float)(sp * c.b / sa);
         q.diag = (float)(sp * c.a);
+        q.lift = lift + 3 * k;
         q.d = P;
         if ((e = sp_run<SP_POLY>(q, none, s)) != hipSuccess) return e;
         q.p = P;
         q.r = XT[k & 1];
+        q.lift = lift + 3 * k + 2;
         q.sym = 0;
         q.last = 1;
         q.n = n;
