@@ -36,8 +36,10 @@
 //
 // What bounds it: large samples, memory: 8 x 128^3 x 32 bf16 forward takes 603
 // us for 3.2 GB (x is read twice; 5.3 TB/s, a copy reaches 5.1), 8 x 64^3 x 64
-// backward 286 us for 1.34 GB.  A few MB, the latencies of two or three
-// dependent launches: 3 x 37 x 29 x 31 x 60 fp32 forward 20.6 us.
+// backward 287 us for 1.34 GB.  A few MB, the latencies of two or three
+// dependent launches: 3 x 37 x 29 x 31 x 60 fp32 forward 20.4 us; 2 x 45 x 33 x
+// 27 x 96 bf16 backward 32 us, whose two passes keep the VALU busy 43 to 47% of
+// the cycles while waves wait for 57% of theirs (two waves a SIMD).
 #include "cf_internal.h"
 
 #include <algorithm>

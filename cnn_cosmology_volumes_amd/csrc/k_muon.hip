@@ -34,10 +34,10 @@
 // Launches take a list of matrices; partial sums are added in a fixed order
 // and there are no atomics: results are reproducible bit for bit.
 //
-// What bounds it: the chain of launches.  256 x 256 takes 112 us in 17 of them
+// What bounds it: the chain of launches.  256 x 256 takes 111 us in 17 of them
 // (a launch of this kind takes about 5 us with almost no work), the eight
-// matrices of the 128^3 benchmark network 196 us: momentum 14, U U^T 32 (fp64
-// matrix cores), its join 10, 14 rounds of 7.5, s Q U 32.  Shorter sides up to
+// matrices of the 128^3 benchmark network 196 to 205 us: momentum 15, U U^T 32
+// (fp64 matrix cores), its join 10, 14 rounds of 8, s Q U 32.  Shorter sides up to
 // 64 iterate in one block instead (108 x 32: 21 us, 70 by rounds), and large
 // matrices whose long side is not much longer take split products of X
 // (k_ns_split.hip).

@@ -37,11 +37,12 @@
 // adds in the order of the blocks.  No atomics and no waiting between blocks:
 // results are reproducible bit for bit.
 //
-// What bounds it: 4096 x 4096 takes 3870 us, of it 330 for each P X (1.25
-// PFLOP/s of fp16 products; a library fp16 product of that size reaches 1.26)
-// with the matrix cores busy 77% of the cycles at 1.5 GHz: the chip's power.
-// 2048 x 2048 takes 733 us, 56 for each P X (55% at 1.6 GHz) and 46 for each
-// symmetric product, 13 of them the joining launch.
+// What bounds it: 4096 x 4096 takes 3820 to 3890 us by card.  In a kernel trace,
+// which adds up to 8% more, each P X takes 350 (1.18 PFLOP/s of fp16 products; a
+// library fp16 product of that size reaches 1.26) with the matrix cores busy 77%
+// of the cycles at 1.5 GHz: the chip's power.  2048 x 2048 takes 757 to 805 us;
+// in a trace of 5 to 10% more, 56 to 59 for each P X (55% at 1.6 GHz) and 49 to
+// 53 for each symmetric product, 13 to 15 of them the joining launch.
 #include "cf_internal.h"
 
 #include <algorithm>
