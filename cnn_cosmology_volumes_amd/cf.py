@@ -5,8 +5,9 @@ tensors' device, the call goes to the library on torch's current stream, and
 a non-zero status raises CfError.  Every step of the computation runs in the
 library's HIP kernels; there is no other code path.
 
-cf_groupnorm_fwd / _bwd, cf_newton_schulz and cf_muon check that tensors are on
-the current GPU.  With stream=s they make their outputs in s's memory; order s
+cf_groupnorm_fwd / _bwd, cf_linear_fwd / _bwd, cf_resnorm_fwd / _bwd,
+cf_grad_clip, cf_newton_schulz and cf_muon check that tensors are on the current
+GPU.  With stream=s they make their outputs in s's memory; order s
 after what wrote the inputs, and the current stream after s before it reads the
 outputs (wait_stream).
 """
@@ -62,6 +63,8 @@ CF_POOL_MAX, CF_POOL_AVG, CF_POOL_NONE = 0, 1, 2
 CF_OPT_SGD, CF_OPT_ADAM_LARC = 0, 1
 CF_ACT_LRELU, CF_ACT_SILU = 0, 1
 CF_MUON_SCALE_ASPECT, CF_MUON_SCALE_RMS = 0, 1
+CF_NORM_RMS, CF_NORM_LAYER = 0, 1
+CF_MAX_CLIP_TENSORS = 1024
 
 
 class cf_net_desc(ctypes.Structure):
@@ -85,6 +88,12 @@ class cf_newton_schulz_params(ctypes.Structure):
 class cf_muon_params(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("nesterov", ctypes.c_int32),
                 ("weight_decay", ctypes.c_float), ("scale", ctypes.c_int32), ("ns", cf_newton_schulz_params)]
+
+
+class cf_resnorm_params(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("gpre", ctypes.c_void_p), ("bpre", ctypes.c_void_p), ("gpost", ctypes.c_void_p),
+                ("bpost", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_n", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -132,6 +141,18 @@ _SIG = {
     "cf_muon_workspace_size": ([ctypes.POINTER(cf_muon_params), ctypes.c_int32, _PI64, _PI64], ctypes.c_size_t),
     "cf_muon": ([ctypes.POINTER(cf_muon_params), ctypes.c_int32, _PI64, _PI64, ctypes.POINTER(_P),
                  ctypes.POINTER(_P), ctypes.POINTER(_P), _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_linear_workspace_size": ([ctypes.c_int, ctypes.c_int64] + [ctypes.c_int32] * 3, ctypes.c_size_t),
+    "cf_linear_fwd": ([ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, ctypes.c_int,
+                       ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_linear_bwd": ([ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_int,
+                       ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_resnorm_workspace_size": ([ctypes.c_int, cf_dims, ctypes.c_int32], ctypes.c_size_t),
+    "cf_resnorm_fwd": ([ctypes.c_int, cf_dims, ctypes.POINTER(cf_resnorm_params), _P, _P, _P, _P, _P], ctypes.c_int),
+    "cf_resnorm_bwd": ([ctypes.c_int, cf_dims, ctypes.POINTER(cf_resnorm_params)] + [_P] * 12 + [ctypes.c_size_t, _P],
+                       ctypes.c_int),
+    "cf_grad_clip_workspace_size": ([ctypes.c_int, ctypes.c_int32, _PI64], ctypes.c_size_t),
+    "cf_grad_clip": ([ctypes.c_int, ctypes.c_int32, _PI64, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.c_float, _P, _P,
+                      ctypes.c_size_t, _P], ctypes.c_int),
     "cf_net_param_count": ([ctypes.POINTER(cf_net_desc), ctypes.POINTER(ctypes.c_int64)], ctypes.c_int32),
     "cf_net_train_step_workspace_size": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32], ctypes.c_size_t),
     "cf_net_train_step": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.POINTER(_P),
@@ -484,6 +505,33 @@ def cf_adam_larc(hp, t, params, grads, m, v, lr_out=None, ws=None, stream=None):
                              _ptr(ws), _wsbytes(ws), _stream(stream)))
 
 
+def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
+    """Scales gradients (all fp32 or all bf16, at most CF_MAX_CLIP_TENSORS), in
+    place or into the tensors of `out`, to a global norm of at most max_norm
+    (math.inf: measures only) -> [norm, factor], two floats on the GPU."""
+    k = len(grads)
+    if not k or (out is not None and len(out) != k):
+        raise ValueError("grads must not be empty, and out be as long")
+    if stream is not None:
+        return _on_stream(stream, cf_grad_clip, (*grads, *(out or ()), stats, ws), grads, max_norm, out, stats, ws)
+    first = grads[0]
+    dt, kind = dtype_code(first.dtype), first.dtype
+    for i, t in enumerate(grads):
+        _packed("gradient %d" % i, t, kind)
+        if out is not None:
+            _packed("output %d" % i, out[i], kind, t.shape)
+    if stats is not None:
+        _packed("stats", stats, torch.float32, (2,))
+    s = _on_gpu(ws, *grads, *(out or ()), stats)
+    n = (ctypes.c_int64 * k)(*[t.numel() for t in grads])
+    stats = first.new_empty(2, dtype=torch.float32) if stats is None else stats
+    L = lib()
+    ws = _ws(L.cf_grad_clip_workspace_size(dt, k, n), first.device, ws)
+    check(L.cf_grad_clip(dt, k, n, _pointers(grads), None if out is None else _pointers(out), float(max_norm),
+                         _ptr(stats), _ptr(ws), _wsbytes(ws), s))
+    return stats
+
+
 # ------------------------------------------------- Newton-Schulz and Muon
 def newton_schulz_params(steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7):
     return cf_newton_schulz_params(int(steps), float(a), float(b), float(c), float(eps))
@@ -620,8 +668,9 @@ def _on_stream(stream, call, given, *args):
     for t in given:
         if t is not None:
             t.record_stream(stream)
-    for t in out or ():
-        t.record_stream(here)
+    for t in (out,) if isinstance(out, torch.Tensor) else out or ():
+        if t is not None:
+            t.record_stream(here)
     return out
 
 
@@ -678,6 +727,145 @@ def cf_groupnorm_bwd(X, dY, groups, gamma, beta, mean, rstd, act=CF_ACT_LRELU, s
     check(lib().cf_groupnorm_bwd(dt, d, _ptr(X), _ptr(dY), groups, _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
                                  int(act), float(slope), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws), _wsbytes(ws), s))
     return dX, dgamma, dbeta
+
+
+# ------------------------------------------------------------- linear layers
+def cf_linear_workspace_size(dtype, rows, fin, fout, backward):
+    return int(lib().cf_linear_workspace_size(dtype, int(rows), int(fin), int(fout), int(bool(backward))))
+
+
+def _linear_sizes(X, W):
+    """(rows, in, out) of X [..., in] and W [in, out]."""
+    _packed("X", X)
+    if W.dim() != 2 or X.dim() < 1 or X.shape[-1] != W.shape[0]:
+        raise ValueError("X must be [..., in] and W [in, out], not %s and %s" % (tuple(X.shape), tuple(W.shape)))
+    _packed("W", W, X.dtype)
+    fin, fout = W.shape
+    return X.numel() // max(1, fin), fin, fout
+
+
+def cf_linear_fwd(X, W, bias=None, act=CF_ACT_LRELU, slope=1.0, R=None, need_pre=True, pre=None, Y=None, ws=None,
+                  stream=None):
+    """act(X W + bias) + R -> (pre, Y).  X [..., in] (an NDHWC tensor: a 1^3
+    convolution), W [in, out] of X's type, bias [out] fp32 or None, R [..., out]
+    or None.  need_pre=False (serving): pre is neither made nor written, and
+    None is returned for it unless it is given."""
+    if stream is not None:
+        return _on_stream(stream, cf_linear_fwd, (X, W, bias, R, pre, Y, ws), X, W, bias, act, slope, R, need_pre, pre,
+                          Y, ws)
+    dt = dtype_code(X.dtype)
+    rows, fin, fout = _linear_sizes(X, W)
+    shape = X.shape[:-1] + (fout,)
+    if bias is not None:
+        _packed("bias", bias, torch.float32, (fout,))
+    for name, t in (("R", R), ("pre", pre), ("Y", Y)):
+        if t is not None:
+            _packed(name, t, X.dtype, shape)
+    s = _on_gpu(ws, X, W, bias, R, pre, Y)
+    Y = X.new_empty(shape) if Y is None else Y
+    pre = X.new_empty(shape) if pre is None and need_pre else pre
+    L = lib()
+    ws = _ws(L.cf_linear_workspace_size(dt, rows, fin, fout, 0), X.device, ws)
+    check(L.cf_linear_fwd(dt, rows, fin, fout, _ptr(X), _ptr(W), _ptr(bias), int(act), float(slope), _ptr(R), _ptr(pre),
+                          _ptr(Y), _ptr(ws), _wsbytes(ws), s))
+    return pre, Y
+
+
+def cf_linear_bwd(X, W, pre, dY, act=CF_ACT_LRELU, slope=1.0, need_dx=True, dX=None, dW=None, db=None, ws=None,
+                  stream=None):
+    """-> (dX, dW, db), dW and db fp32, dX None unless need_dx or given; pre may
+    be None without an activation (CF_ACT_LRELU with slope 1).  The gradient of
+    the forward's R is dY."""
+    if stream is not None:
+        return _on_stream(stream, cf_linear_bwd, (X, W, pre, dY, dX, dW, db, ws), X, W, pre, dY, act, slope, need_dx, dX,
+                          dW, db, ws)
+    dt = dtype_code(X.dtype)
+    rows, fin, fout = _linear_sizes(X, W)
+    shape = X.shape[:-1] + (fout,)
+    _packed("dY", dY, X.dtype, shape)
+    if pre is not None:
+        _packed("pre", pre, X.dtype, shape)
+    if dX is not None:
+        _packed("dX", dX, X.dtype, X.shape)
+    if dW is not None:
+        _packed("dW", dW, torch.float32, W.shape)
+    if db is not None:
+        _packed("db", db, torch.float32, (fout,))
+    s = _on_gpu(ws, X, W, pre, dY, dX, dW, db)
+    dX = torch.empty_like(X) if dX is None and need_dx else dX
+    dW = X.new_empty((fin, fout), dtype=torch.float32) if dW is None else dW
+    db = X.new_empty((fout,), dtype=torch.float32) if db is None else db
+    L = lib()
+    ws = _ws(L.cf_linear_workspace_size(dt, rows, fin, fout, 1), X.device, ws)
+    check(L.cf_linear_bwd(dt, rows, fin, fout, _ptr(X), _ptr(W), _ptr(pre), _ptr(dY), int(act), float(slope), _ptr(dX),
+                          _ptr(dW), _ptr(db), _ptr(ws), _wsbytes(ws), s))
+    return dX, dW, db
+
+
+# ------------------------------------------------ norms around a residual join
+def cf_resnorm_workspace_size(dtype, xshape, gate_n):
+    return int(lib().cf_resnorm_workspace_size(dtype, dims(xshape), int(gate_n)))
+
+
+def _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha):
+    for name, t in (("gpre", gpre), ("bpre", bpre), ("gpost", gpost), ("bpost", bpost)):
+        if t is not None:
+            _packed(name, t, torch.float32, (d.c,))
+    gate_n = 0
+    if gate is not None:
+        gate_n = gate.shape[0] if gate.dim() == 2 else 1
+        _packed("gate", gate, torch.float32, (gate_n, d.c) if gate.dim() == 2 else (d.c,))
+    return cf_resnorm_params(int(kind), float(eps), float(alpha), _ptr(gpre), _ptr(bpre), _ptr(gpost), _ptr(bpost),
+                             _ptr(gate), gate_n)
+
+
+def cf_resnorm_fwd(X, F, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None, gate=None, alpha=1.0, need_y=True,
+                   R=None, Y=None, stream=None):
+    """The join of a residual block, over the channels of NDHWC tensors:
+    R = alpha X + gate post(F), Y = pre(R) -> (R, Y).  kind: CF_NORM_RMS or
+    CF_NORM_LAYER; gpost None: no norm of F; gate [C], [1, C] or, one for each
+    sample, [N, C].  need_y=False: no further norm, None for Y unless it is given."""
+    if stream is not None:
+        return _on_stream(stream, cf_resnorm_fwd, (X, F, gpre, bpre, gpost, bpost, gate, R, Y), X, F, kind, eps, gpre,
+                          bpre, gpost, bpost, gate, alpha, need_y, R, Y)
+    dt, d = dtype_code(X.dtype), cf_dims(*X.shape)
+    _packed("X", X)
+    _packed("F", F, X.dtype, X.shape)
+    for name, t in (("R", R), ("Y", Y)):
+        if t is not None:
+            _packed(name, t, X.dtype, X.shape)
+    p = _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha)
+    s = _on_gpu(None, X, F, gpre, bpre, gpost, bpost, gate, R, Y)
+    R = torch.empty_like(X) if R is None else R
+    Y = torch.empty_like(X) if Y is None and need_y else Y
+    check(lib().cf_resnorm_fwd(dt, d, ctypes.byref(p), _ptr(X), _ptr(F), _ptr(R), _ptr(Y), s))
+    return R, Y
+
+
+def cf_resnorm_bwd(F, R, dR, dY, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None, gate=None, alpha=1.0, dX=None,
+                   dF=None, ws=None, stream=None):
+    """-> (dX, dF, dgpre, dbpre, dgpost, dbpost, dgate) from the forward's F and
+    R; dR or dY may be None (not both).  None is returned for the gradients of
+    vectors that are None, and for dgpre and dbpre without dY."""
+    if stream is not None:
+        return _on_stream(stream, cf_resnorm_bwd, (F, R, dR, dY, gpre, bpre, gpost, bpost, gate, dX, dF, ws), F, R, dR,
+                          dY, kind, eps, gpre, bpre, gpost, bpost, gate, alpha, dX, dF, ws)
+    dt, d = dtype_code(F.dtype), cf_dims(*F.shape)
+    _packed("F", F)
+    for name, t in (("R", R), ("dR", dR), ("dY", dY), ("dX", dX), ("dF", dF)):
+        if t is not None:
+            _packed(name, t, F.dtype, F.shape)
+    p = _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha)
+    s = _on_gpu(ws, F, R, dR, dY, gpre, bpre, gpost, bpost, gate, dX, dF)
+    dX = torch.empty_like(F) if dX is None else dX
+    dF = torch.empty_like(F) if dF is None else dF
+    like = lambda t, wanted=True: torch.empty_like(t) if t is not None and wanted else None
+    g = [like(gpre, dY is not None), like(bpre, dY is not None), like(gpost), like(bpost), like(gate)]
+    L = lib()
+    ws = _ws(L.cf_resnorm_workspace_size(dt, d, p.gate_n), F.device, ws)
+    check(L.cf_resnorm_bwd(dt, d, ctypes.byref(p), _ptr(F), _ptr(R), _ptr(dR), _ptr(dY), _ptr(dX), _ptr(dF),
+                           *[_ptr(t) for t in g], _ptr(ws), _wsbytes(ws), s))
+    return (dX, dF, *g)
 
 
 # ------------------------------------------------------ general network step

@@ -6,6 +6,7 @@
 // are the caller's (cf_step_aux).
 #include "cf_internal.h"
 
+#include <algorithm>
 #include <atomic>
 #include <math.h>
 #include <stdarg.h>
@@ -1174,6 +1175,239 @@ cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
                        : launch_gn_bwd<uint16_t>((const uint16_t*)X, (const uint16_t*)dY, gamma, beta, mean, rstd, act,
                                                  slope, (uint16_t*)dX, dgamma, dbeta, x, groups, ws, stream);
     CF_TRY_HIP(e, "group norm backward");
+    return CF_OK;
+}
+
+// ------------------------------------------------------------ linear layers
+static cf_status check_linear(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const char* fn)
+{
+    cf_status st = check_dtype(dtype);
+    if (st != CF_OK) return st;
+    if (rows < 1 || in < 1 || out < 1) return fail(CF_ERR_INVALID, "%s: sizes must be positive", fn);
+    if (rows > kMaxDim || in > 65536 || out > 65536) return fail(CF_ERR_INVALID, "%s: dimension too large", fn);
+    if (rows * in > kMaxElems || rows * out > kMaxElems) return fail(CF_ERR_INVALID, "%s: tensor too large", fn);
+    return CF_OK;
+}
+
+size_t cf_linear_workspace_size(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, int32_t backward)
+{
+    if (check_linear(dtype, rows, in, out, "cf_linear_workspace_size") != CF_OK) return 0;
+    return linear_ws_bytes(dtype, rows, in, out, backward != 0);
+}
+
+cf_status cf_linear_fwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
+                        const float* bias, cf_act act, float slope, const void* R, void* pre, void* Y, void* ws,
+                        size_t ws_bytes, hipStream_t stream)
+{
+    const char* fn = "cf_linear_fwd";
+    cf_status st = check_linear(dtype, rows, in, out, fn);
+    if (st != CF_OK) return st;
+    if ((st = check_act(act, slope, fn)) != CF_OK) return st;
+    if (!X || !W || !Y) return fail(CF_ERR_INVALID, "%s: null pointer", fn);
+    if (!al16(X) || !al16(W) || !al16(bias) || !al16(R) || !al16(pre) || !al16(Y))
+        return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+    const size_t need = linear_ws_bytes(dtype, rows, in, out, false);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    const size_t size = dtype == CF_F32 ? 4 : 2, xb = (size_t)rows * in * size, yb = (size_t)rows * out * size;
+    const Span span[] = {{X, xb, false}, {W, (size_t)in * out * size, false}, {bias, bias ? (size_t)out * 4 : 0, false},
+                         {R, R ? yb : 0, false}, {pre, pre ? yb : 0, true}, {Y, yb, true}, {ws, need, true}};
+    if (overlapping(span, 7)) return fail(CF_ERR_INVALID, "%s: outputs or workspace overlap other arguments", fn);
+    CF_TRY_HIP(dtype == CF_F32
+                   ? launch_linear_fwd<float>(rows, in, out, (const float*)X, (const float*)W, bias, act, slope,
+                                              (const float*)R, (float*)pre, (float*)Y, ws, stream)
+                   : launch_linear_fwd<uint16_t>(rows, in, out, (const uint16_t*)X, (const uint16_t*)W, bias, act, slope,
+                                                 (const uint16_t*)R, (uint16_t*)pre, (uint16_t*)Y, ws, stream),
+               "linear forward");
+    return CF_OK;
+}
+
+cf_status cf_linear_bwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
+                        const void* pre, const void* dY, cf_act act, float slope, void* dX, float* dW, float* db,
+                        void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const char* fn = "cf_linear_bwd";
+    cf_status st = check_linear(dtype, rows, in, out, fn);
+    if (st != CF_OK) return st;
+    if ((st = check_act(act, slope, fn)) != CF_OK) return st;
+    const bool gated = act == CF_ACT_SILU || slope != 1.f;
+    if (!X || !W || !dY || !dW || (gated && !pre)) return fail(CF_ERR_INVALID, "%s: null pointer", fn);
+    if (!al16(X) || !al16(W) || !al16(pre) || !al16(dY) || !al16(dX) || !al16(dW) || !al16(db))
+        return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+    const size_t need = linear_ws_bytes(dtype, rows, in, out, true);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (need && (!ws || !al16(ws))) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    const size_t size = dtype == CF_F32 ? 4 : 2, xb = (size_t)rows * in * size, yb = (size_t)rows * out * size;
+    const Span span[] = {{X, xb, false}, {W, (size_t)in * out * size, false}, {pre, pre ? yb : 0, false},
+                         {dY, yb, false}, {dX, dX ? xb : 0, true}, {dW, (size_t)in * out * 4, true},
+                         {db, db ? (size_t)out * 4 : 0, true}, {ws, need, true}};
+    if (overlapping(span, 8)) return fail(CF_ERR_INVALID, "%s: outputs or workspace overlap other arguments", fn);
+    CF_TRY_HIP(dtype == CF_F32
+                   ? launch_linear_bwd<float>(rows, in, out, (const float*)X, (const float*)W, (const float*)pre,
+                                              (const float*)dY, act, slope, (float*)dX, dW, db, ws, stream)
+                   : launch_linear_bwd<uint16_t>(rows, in, out, (const uint16_t*)X, (const uint16_t*)W,
+                                                 (const uint16_t*)pre, (const uint16_t*)dY, act, slope, (uint16_t*)dX,
+                                                 dW, db, ws, stream),
+               "linear backward");
+    return CF_OK;
+}
+
+// ------------------------------------------ norms around a residual join
+static cf_status check_resnorm(cf_dtype dtype, const cf_dims& x, int32_t gate_n, const char* fn)
+{
+    cf_status st = check_dtype(dtype);
+    if (st != CF_OK) return st;
+    if ((st = check_dims(x, "x")) != CF_OK) return st;
+    if (gate_n != 0 && gate_n != 1 && gate_n != x.n) return fail(CF_ERR_INVALID, "%s: gate_n must be 0, 1 or x.n", fn);
+    if (x.c > 4096) return fail(CF_ERR_UNSUPPORTED, "%s: at most 4096 channels", fn);
+    return CF_OK;
+}
+
+static cf_status check_resnorm_params(const cf_resnorm_params* p, const char* fn)
+{
+    if (!p) return fail(CF_ERR_INVALID, "%s: null parameters", fn);
+    if (p->kind != CF_NORM_RMS && p->kind != CF_NORM_LAYER) return fail(CF_ERR_INVALID, "%s: unknown norm %d", fn, p->kind);
+    if (!(p->eps > 0.f) || !(p->eps < INFINITY)) return fail(CF_ERR_INVALID, "%s: eps must be positive and finite", fn);
+    if (!isfinite(p->alpha)) return fail(CF_ERR_INVALID, "%s: alpha must be finite", fn);
+    if ((p->gate == nullptr) != (p->gate_n == 0)) return fail(CF_ERR_INVALID, "%s: gate and gate_n do not go together", fn);
+    if (!p->gpost && p->bpost) return fail(CF_ERR_INVALID, "%s: bpost without gpost", fn);
+    if (!al16(p->gpre) || !al16(p->bpre) || !al16(p->gpost) || !al16(p->bpost) || !al16(p->gate))
+        return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+    return CF_OK;
+}
+
+// The vectors' bytes.
+static int resnorm_spans(const cf_resnorm_params& p, const cf_dims& x, Span* span)
+{
+    const size_t c = (size_t)x.c * sizeof(float);
+    const Span s[] = {{p.gpre, p.gpre ? c : 0, false}, {p.bpre, p.bpre ? c : 0, false}, {p.gpost, p.gpost ? c : 0, false},
+                      {p.bpost, p.bpost ? c : 0, false}, {p.gate, p.gate ? c * p.gate_n : 0, false}};
+    for (int i = 0; i < 5; ++i) span[i] = s[i];
+    return 5;
+}
+
+static ResnormArgs resnorm_args(const cf_resnorm_params& p)
+{
+    return ResnormArgs{p.kind == CF_NORM_LAYER, p.eps, p.alpha, p.gpre, p.bpre, p.gpost, p.bpost, p.gate, p.gate_n};
+}
+
+size_t cf_resnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t gate_n)
+{
+    if (check_resnorm(dtype, x, gate_n, "cf_resnorm_workspace_size") != CF_OK) return 0;
+    return resnorm_ws_bytes(x, gate_n);
+}
+
+cf_status cf_resnorm_fwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* X, const void* F, void* R,
+                         void* Y, hipStream_t stream)
+{
+    const char* fn = "cf_resnorm_fwd";
+    cf_status st = check_resnorm_params(p, fn);
+    if (st != CF_OK || (st = check_resnorm(dtype, x, p->gate_n, fn)) != CF_OK) return st;
+    if (!X || !F || !R) return fail(CF_ERR_INVALID, "%s: null pointer", fn);
+    if (!al16(X) || !al16(F) || !al16(R) || !al16(Y)) return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+    const size_t bytes = gn_bytes(dtype, x);
+    Span span[9] = {{X, bytes, false}, {F, bytes, false}, {R, bytes, true}, {Y, Y ? bytes : 0, true}};
+    const int spans = 4 + resnorm_spans(*p, x, span + 4);
+    if (overlapping(span, spans)) return fail(CF_ERR_INVALID, "%s: outputs overlap other arguments", fn);
+    CF_TRY_HIP(dtype == CF_F32 ? launch_resnorm_fwd<float>(x, resnorm_args(*p), X, F, R, Y, stream)
+                               : launch_resnorm_fwd<uint16_t>(x, resnorm_args(*p), X, F, R, Y, stream),
+               "residual norm forward");
+    return CF_OK;
+}
+
+cf_status cf_resnorm_bwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* F, const void* R,
+                         const void* dR, const void* dY, void* dX, void* dF, float* dgpre, float* dbpre, float* dgpost,
+                         float* dbpost, float* dgate, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const char* fn = "cf_resnorm_bwd";
+    cf_status st = check_resnorm_params(p, fn);
+    if (st != CF_OK || (st = check_resnorm(dtype, x, p->gate_n, fn)) != CF_OK) return st;
+    if (!F || !dX || !dF || (!dR && !dY) || (dY && !R) || (p->gate && !dgate))
+        return fail(CF_ERR_INVALID, "%s: null pointer", fn);
+    if (!al16(F) || !al16(R) || !al16(dR) || !al16(dY) || !al16(dX) || !al16(dF) || !al16(dgpre) || !al16(dbpre) ||
+        !al16(dgpost) || !al16(dbpost) || !al16(dgate))
+        return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+    const size_t need = resnorm_ws_bytes(x, p->gate_n);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    const size_t bytes = gn_bytes(dtype, x), c = (size_t)x.c * sizeof(float);
+    Span span[17] = {{F, bytes, false}, {R, R ? bytes : 0, false}, {dR, dR ? bytes : 0, false},
+                     {dY, dY ? bytes : 0, false}, {dX, bytes, true}, {dF, bytes, true}, {dgpre, dgpre ? c : 0, true},
+                     {dbpre, dbpre ? c : 0, true}, {dgpost, dgpost ? c : 0, true}, {dbpost, dbpost ? c : 0, true},
+                     {dgate, p->gate ? c * p->gate_n : 0, true}, {ws, need, true}};
+    const int spans = 12 + resnorm_spans(*p, x, span + 12);
+    if (overlapping(span, spans)) return fail(CF_ERR_INVALID, "%s: outputs or workspace overlap other arguments", fn);
+    const ResnormGrads g = {dgpre, dbpre, p->gpost ? dgpost : nullptr, p->gpost ? dbpost : nullptr,
+                            p->gate ? dgate : nullptr};
+    CF_TRY_HIP(dtype == CF_F32 ? launch_resnorm_bwd<float>(x, resnorm_args(*p), F, R, dR, dY, dX, dF, g, ws, stream)
+                               : launch_resnorm_bwd<uint16_t>(x, resnorm_args(*p), F, R, dR, dY, dX, dF, g, ws, stream),
+               "residual norm backward");
+    return CF_OK;
+}
+
+// --------------------------------------- global gradient norm and clipping
+static cf_status check_clip(cf_dtype dtype, int32_t nt, const int64_t* n, const char* fn)
+{
+    cf_status st = check_dtype(dtype);
+    if (st != CF_OK) return st;
+    if (!n) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
+    if (nt < 1 || nt > CF_MAX_CLIP_TENSORS)
+        return fail(CF_ERR_INVALID, "%s: ntensors must be 1..%d (got %d)", fn, CF_MAX_CLIP_TENSORS, nt);
+    for (int i = 0; i < nt; ++i)
+        if (n[i] <= 0 || n[i] > ((int64_t)1 << 36)) return fail(CF_ERR_INVALID, "%s: n[%d] out of range", fn, i);
+    return CF_OK;
+}
+
+// Whether what is written shares bytes with anything but its own input: by
+// sorted addresses, since pairs of a thousand tensors are too many.
+static bool clip_overlapping(Span* s, int count)
+{
+    std::sort(s, s + count, [](const Span& a, const Span& b) { return (uintptr_t)a.at < (uintptr_t)b.at; });
+    uintptr_t end = 0, written_end = 0;      // of everything before, and of what is written before
+    for (int i = 0; i < count; ++i) {
+        if ((uintptr_t)s[i].at < (s[i].written ? end : written_end)) return true;
+        const uintptr_t e = (uintptr_t)s[i].at + s[i].bytes;
+        end = std::max(end, e);
+        if (s[i].written) written_end = std::max(written_end, e);
+    }
+    return false;
+}
+
+size_t cf_grad_clip_workspace_size(cf_dtype dtype, int32_t ntensors, const int64_t* n)
+{
+    if (check_clip(dtype, ntensors, n, "cf_grad_clip_workspace_size") != CF_OK) return 0;
+    return clip_ws_bytes(dtype, ntensors, n);
+}
+
+cf_status cf_grad_clip(cf_dtype dtype, int32_t ntensors, const int64_t* n, const void* const* g, void* const* out,
+                       float max_norm, float* stats, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const char* fn = "cf_grad_clip";
+    cf_status st = check_clip(dtype, ntensors, n, fn);
+    if (st != CF_OK) return st;
+    if (!g) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
+    if (!(max_norm >= 0.f)) return fail(CF_ERR_INVALID, "%s: max_norm must be >= 0", fn);
+    if (!al16(stats)) return fail(CF_ERR_INVALID, "%s: stats must be 16-byte aligned", fn);
+    const size_t need = clip_ws_bytes(dtype, ntensors, n);
+    if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+    if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
+    Span span[2 * CF_MAX_CLIP_TENSORS + 2];
+    void* to[CF_MAX_CLIP_TENSORS];
+    int spans = 0;
+    for (int i = 0; i < ntensors; ++i) {
+        to[i] = out ? out[i] : const_cast<void*>(g[i]);
+        if (!g[i] || !to[i] || !al16(g[i]) || !al16(to[i]))
+            return fail(CF_ERR_INVALID, "%s: tensor %d has a null or misaligned pointer", fn, i);
+        const size_t bytes = (size_t)n[i] * (dtype == CF_F32 ? 4 : 2);
+        if (to[i] != g[i]) span[spans++] = {g[i], bytes, false};
+        span[spans++] = {to[i], bytes, true};
+    }
+    if (stats) span[spans++] = {stats, 8, true};
+    span[spans++] = {ws, need, true};
+    if (clip_overlapping(span, spans)) return fail(CF_ERR_INVALID, "%s: outputs or workspace overlap other arguments", fn);
+    CF_TRY_HIP(dtype == CF_F32 ? launch_grad_clip<float>(ntensors, n, g, to, max_norm, stats, ws, stream)
+                               : launch_grad_clip<uint16_t>(ntensors, n, g, to, max_norm, stats, ws, stream),
+               "gradient clipping");
     return CF_OK;
 }
 

@@ -364,4 +364,37 @@ hipError_t launch_ns_split_apply(int m, int n, bool tall, const NsCoef& c, const
 hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, float* const* w, const float* const* g,
                        float* const* m, void* ws, hipStream_t s);
 
+// Linear layers over rows (k_linear.hip).  T = float or uint16_t (bf16).
+size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd);
+template <typename T>
+hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T* W, const float* bias, cf_act act,
+                             float slope, const T* R, T* pre, T* Y, void* ws, hipStream_t s);
+template <typename T>
+hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T* W, const T* pre, const T* dY,
+                             cf_act act, float slope, T* dX, float* dW, float* db, void* ws, hipStream_t s);
+
+// The join of a residual block (k_resnorm.hip).  gate_n: 0 (no gate), 1, or x.n.
+struct ResnormArgs {
+    bool layer;
+    float eps, alpha;
+    const float *gpre, *bpre, *gpost, *bpost, *gate;
+    int gate_n;
+};
+struct ResnormGrads {
+    float *gpre, *bpre, *gpost, *bpost, *gate;      // null where there is none
+};
+size_t resnorm_ws_bytes(const cf_dims& x, int gate_n);
+template <typename T>
+hipError_t launch_resnorm_fwd(const cf_dims& x, const ResnormArgs& p, const void* X, const void* F, void* R, void* Y,
+                              hipStream_t s);
+template <typename T>
+hipError_t launch_resnorm_bwd(const cf_dims& x, const ResnormArgs& p, const void* F, const void* R, const void* dR,
+                              const void* dY, void* dX, void* dF, const ResnormGrads& g, void* ws, hipStream_t s);
+
+// Global gradient norm and clipping (k_clip.hip); stats: norm and factor.
+size_t clip_ws_bytes(cf_dtype dt, int count, const int64_t* n);
+template <typename T>
+hipError_t launch_grad_clip(int count, const int64_t* n, const void* const* g, void* const* out, float max_norm,
+                            float* stats, void* ws, hipStream_t s);
+
 }  // namespace cf

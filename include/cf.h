@@ -68,6 +68,12 @@ typedef enum { CF_F32 = 0, CF_BF16 = 1 } cf_dtype;
 /* Packed NDHWC tensor shape. */
 typedef struct { int64_t n, d, h, w, c; } cf_dims;
 
+/* Activation applied to normalised values or to a linear layer's. */
+typedef enum {
+    CF_ACT_LRELU = 0,  /* z > 0 ? z : slope * z, slope >= 0 (1 = none) */
+    CF_ACT_SILU = 1    /* z / (1 + exp(-z)); slope is ignored */
+} cf_act;
+
 /* Convolution geometry; `pad` is the zero padding below each dimension.
  * This build supports k = 3 with
  *  - stride 1, pad 1: the "same" stride-1 convolution of [OY] Sec. IV;
@@ -274,6 +280,66 @@ cf_status cf_mse(int32_t B, int32_t K, const float* yhat, const float* t, float*
 /* SGD update W <- W - lr * dW on n fp32 values ([OY] Sec. II-A). */
 cf_status cf_sgd(int64_t n, float lr, float* W, const float* dW, hipStream_t stream);
 
+/* ----------------------------------------------------- linear layers */
+
+/* Workspace bytes for cf_linear_fwd (backward = 0) or cf_linear_bwd
+ * (backward != 0) with any activation; 0 is possible.  Returns 0 also for
+ * invalid arguments. */
+size_t cf_linear_workspace_size(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, int32_t backward);
+
+/* Linear layer over rows, with bias, activation and residual: a dense layer
+ * ([OY] Table I fc layers) in either data type, or a 1^3 convolution, which
+ * cf_conv3d_fwd does not take, over the rows = n d h w voxels of an NDHWC tensor:
+ *   pre[r,o] = sum_i X[r,i] * W[i,o] + bias[o];  Y = act(pre) + R
+ *   X [rows,in], W [in,out] (dtype); bias [out] fp32 or NULL (zero)
+ *   R [rows,out] (dtype) or NULL (zero)
+ *   pre [rows,out] (dtype), kept for the backward, or NULL (not written)
+ *   Y [rows,out] (dtype)
+ * act and slope as for cf_groupnorm_fwd (CF_ACT_LRELU with slope 1: none).  Y is
+ * made from the unrounded pre.  rows at most 2^30, in and out at most 65536, no
+ * tensor above 2^40 elements.  Sums are added in a fixed order: results are
+ * reproducible bit for bit.  pre and Y may not overlap any other argument
+ * (CF_ERR_INVALID). */
+cf_status cf_linear_fwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
+                        const float* bias, cf_act act, float slope, const void* R, void* pre, void* Y, void* ws,
+                        size_t ws_bytes, hipStream_t stream);
+
+/* Backward of cf_linear_fwd from its pre.  With D = dY act'(pre) (the leaky
+ * ReLU's derivative is slope at pre <= 0):
+ *   dX[r,i] = sum_o D[r,o] W[i,o]   (dtype; skipped when dX is NULL)
+ *   dW[i,o] = sum_r X[r,i] D[r,o];  db[o] = sum_r D[r,o]   (fp32)
+ * db may be NULL; pre may be NULL for CF_ACT_LRELU with slope 1.  R's gradient
+ * is dY itself.  For CF_BF16 dX takes D rounded to bf16, dW and db take it with
+ * 16 bits or more.  dX, dW and db may not overlap any other argument
+ * (CF_ERR_INVALID). */
+cf_status cf_linear_bwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
+                        const void* pre, const void* dY, cf_act act, float slope, void* dX, float* dW, float* db,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------- global gradient norm and clipping */
+
+#define CF_MAX_CLIP_TENSORS 1024
+
+/* Workspace bytes for cf_grad_clip over tensors of these sizes (HOST array).
+ * Returns 0 for invalid arguments. */
+size_t cf_grad_clip_workspace_size(cf_dtype dtype, int32_t ntensors, const int64_t* n);
+
+/* Scales ntensors (1..CF_MAX_CLIP_TENSORS) gradients, together one vector, to a
+ * norm of at most max_norm:
+ *   norm = sqrt(sum of g^2 over every tensor)
+ *   factor = max_norm / norm where norm > max_norm, else 1
+ *   out[i] = factor g[i]
+ * n, g and out are HOST arrays; g[i] and out[i] are DEVICE pointers to n[i]
+ * values (dtype).  out may be NULL, or out[i] = g[i]: in place; no other overlap
+ * of out[i] with any argument (CF_ERR_INVALID).  max_norm >= 0; INFINITY
+ * measures the norm alone (the factor is 1).  A norm that is infinite gives the
+ * factor 0 (infinite gradients become NaN), one that is NaN the factor NaN.
+ * stats: two device floats, the norm and the factor, or NULL.  Squares are added
+ * in fp64 and in a fixed order: they neither overflow nor vanish, and results are
+ * reproducible bit for bit. */
+cf_status cf_grad_clip(cf_dtype dtype, int32_t ntensors, const int64_t* n, const void* const* g, void* const* out,
+                       float max_norm, float* stats, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------ Adam + LARC + polynomial decay */
 
 /* Optimizer of [CF] Sec. III-B (Adam with LARC and polynomial decay of
@@ -402,12 +468,6 @@ cf_status cf_batchnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
 
 /* ------------------------------------------- group norm with activation */
 
-/* Activation applied to the normalised values. */
-typedef enum {
-    CF_ACT_LRELU = 0,  /* z > 0 ? z : slope * z, slope >= 0 (1 = none) */
-    CF_ACT_SILU = 1    /* z / (1 + exp(-z)); slope is ignored */
-} cf_act;
-
 /* Workspace bytes for cf_groupnorm_fwd (backward = 0) or cf_groupnorm_bwd
  * (backward != 0); 0 is possible.  Returns 0 also for invalid arguments. */
 size_t cf_groupnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t groups, int32_t backward);
@@ -440,6 +500,54 @@ cf_status cf_groupnorm_bwd(cf_dtype dtype, cf_dims x, const void* X, const void*
                            const float* gamma, const float* beta, const float* mean, const float* rstd, cf_act act,
                            float slope, void* dX, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
                            hipStream_t stream);
+
+/* ------------------------------------------ norms around a residual join */
+
+typedef enum {
+    CF_NORM_RMS = 0,   /* v rstd gamma + beta, rstd = 1 / sqrt(mean(v^2) + eps) */
+    CF_NORM_LAYER = 1  /* (v - mean) rstd gamma + beta, rstd from the (biased) variance */
+} cf_norm;
+
+/* The parameters of cf_resnorm_fwd and cf_resnorm_bwd.  Vectors are fp32, [c]
+ * each; a NULL offset is zero. */
+typedef struct {
+    int32_t kind;                     /* cf_norm, of both norms */
+    float eps;                        /* positive, finite */
+    float alpha;                      /* residual scale, finite */
+    const float *gpre, *bpre;         /* the norm before the next branch; gpre NULL: without its factors */
+    const float *gpost, *bpost;       /* the norm after this branch; gpost NULL: no norm (bpost must be NULL) */
+    const float* gate;                /* [gate_n, c] or NULL (one) */
+    int32_t gate_n;                   /* 0 (gate NULL), 1, or x.n: a gate for each sample */
+} cf_resnorm_params;
+
+/* Workspace bytes for cf_resnorm_bwd (the forward needs none).  Returns 0 for
+ * invalid arguments. */
+size_t cf_resnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t gate_n);
+
+/* The join of a residual block with the norms after its branch and before the
+ * next, each over the c channels of a voxel:
+ *   H = post(F) (F itself where gpost is NULL)
+ *   R = alpha X + gate H;  Y = pre(R)
+ *   X, F, R, Y [x.n, x.d, x.h, x.w, x.c] (dtype); Y may be NULL (the last block:
+ *   no further norm).
+ * Y is made from the unrounded R.  x.c at most 4096 (else CF_ERR_UNSUPPORTED).  R
+ * and Y may not overlap any other argument (CF_ERR_INVALID). */
+cf_status cf_resnorm_fwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* X, const void* F, void* R,
+                         void* Y, hipStream_t stream);
+
+/* Backward of cf_resnorm_fwd from F and its R, with dR the gradient that reaches
+ * R by other ways than Y (NULL: none) and dY that of Y (NULL: none; at least one
+ * is given):
+ *   d = dR + (dY through the norm);  dX = alpha d;  dF = (gate d through the norm)
+ *   dgpre, dbpre, dgpost, dbpost [c], dgate [gate_n, c]: fp32 sums over what each
+ *   is shared by.  A pointer may be NULL where the gradient is not wanted, but
+ *   for dgate where there is a gate; dgpre and dbpre are not written without dY,
+ *   dgpost and dbpost not without gpost.
+ * Sums are added in a fixed order: results are reproducible bit for bit.  Outputs
+ * may not overlap any other argument (CF_ERR_INVALID). */
+cf_status cf_resnorm_bwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* F, const void* R,
+                         const void* dR, const void* dY, void* dX, void* dF, float* dgpre, float* dbpre, float* dgpost,
+                         float* dbpost, float* dgate, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* --------------------------------------------------------- training step */
 

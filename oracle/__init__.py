@@ -567,6 +567,94 @@ def groupnorm_bwd(x, dy, groups, gamma, beta, mean, rstd, act, slope):
     return dx.reshape(x.shape), dgamma, dbeta
 
 
+# ------------------------------------- linear layers, residual joins, clipping
+def linear_fwd(x, w, bias, act, slope, r=None):
+    """pre = x w + bias, y = act(pre) + r over the last dimension of x.
+    Returns (pre, y)."""
+    pre = _f64(x) @ _f64(w)
+    if bias is not None:
+        pre = pre + _f64(bias)
+    y = _act(pre, act, slope)[0]
+    return pre, y if r is None else y + _f64(r)
+
+
+def linear_bwd(x, w, pre, dy, act, slope):
+    """With d = dy act'(pre): (d w^T, x^T d, column sums of d)."""
+    w = _f64(w)
+    d = (_f64(dy) * _act(_f64(pre), act, slope)[1]).reshape(-1, w.shape[1])
+    t = _f64(x).reshape(-1, w.shape[0])
+    return (d @ w.T).reshape(np.shape(x)), t.T @ d, d.sum(axis=0)
+
+
+def row_norm(v, kind, eps):
+    """Rows (last dimension) normalised by their root mean square (kind "rms")
+    or centred and by their standard deviation ("layer").  Returns (rows, rstd)."""
+    v = _f64(v)
+    if kind == "layer":
+        v = v - v.mean(axis=-1, keepdims=True)
+    rstd = 1.0 / np.sqrt((v * v).mean(axis=-1, keepdims=True) + eps)
+    return v * rstd, rstd
+
+
+def row_norm_bwd(d, hat, rstd, kind):
+    """The rows' gradient from that of their normalised values."""
+    t = d - hat * (d * hat).mean(axis=-1, keepdims=True)
+    return rstd * (t - d.mean(axis=-1, keepdims=True) if kind == "layer" else t)
+
+
+def _per_sample(gate, shape):
+    """gate None, [c] or [1 or n, c] -> broadcastable over [n, d, h, w, c]."""
+    if gate is None:
+        return np.ones((1, 1, 1, 1, shape[-1]))
+    return _f64(gate).reshape(-1, 1, 1, 1, shape[-1])
+
+
+def _vec(v, c, other):
+    return np.full(c, other) if v is None else _f64(v)
+
+
+def resnorm_fwd(x, f, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None, gate=None, alpha=1.0):
+    """r = alpha x + gate post(f), y = pre(r), norms over the channels.
+    Returns (r, y)."""
+    c = x.shape[-1]
+    h = _f64(f)
+    if gpost is not None:
+        h = row_norm(f, kind, eps)[0] * _f64(gpost) + _vec(bpost, c, 0.0)
+    r = alpha * _f64(x) + _per_sample(gate, x.shape) * h
+    return r, row_norm(r, kind, eps)[0] * _vec(gpre, c, 1.0) + _vec(bpre, c, 0.0)
+
+
+def resnorm_bwd(f, r, dr, dy, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None, gate=None, alpha=1.0):
+    """Backward of resnorm_fwd from f and r; dr or dy may be None.  Returns a
+    dict of dx, df, dgpre, dbpre, dgpost, dbpost, dgate."""
+    c, lead = f.shape[-1], (0, 1, 2, 3)
+    g = {}
+    d = np.zeros(f.shape) if dr is None else _f64(dr)
+    if dy is not None:
+        hat, rstd = row_norm(r, kind, eps)
+        g["dgpre"], g["dbpre"] = (_f64(dy) * hat).sum(axis=lead), _f64(dy).sum(axis=lead)
+        d = d + row_norm_bwd(_f64(dy) * _vec(gpre, c, 1.0), hat, rstd, kind)
+    gate5 = _per_sample(gate, f.shape)
+    h, dh = _f64(f), gate5 * d
+    g["dx"], g["df"] = alpha * d, dh
+    if gpost is not None:
+        hat, rstd = row_norm(f, kind, eps)
+        h = hat * _f64(gpost) + _vec(bpost, c, 0.0)
+        g["dgpost"], g["dbpost"] = (dh * hat).sum(axis=lead), dh.sum(axis=lead)
+        g["df"] = row_norm_bwd(dh * _f64(gpost), hat, rstd, kind)
+    if gate is not None:
+        t = (d * h).sum(axis=(1, 2, 3))
+        g["dgate"] = (t.sum(axis=0) if gate5.shape[0] == 1 else t).reshape(np.shape(gate))
+    return g
+
+
+def grad_clip(grads, max_norm):
+    """Returns (scaled gradients, norm, factor)."""
+    norm = float(np.sqrt(sum(float((_f64(g) ** 2).sum()) for g in grads)))
+    factor = max_norm / norm if norm > max_norm else 1.0
+    return [_f64(g) * factor for g in grads], norm, factor
+
+
 # ------------------------------------------------- general network step
 def net_param_shapes(cin, layers, dense, batch_norm, dense_bias, in_size):
     """Parameter shapes in the order the step takes them: per conv layer W
