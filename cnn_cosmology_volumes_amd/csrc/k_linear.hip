@@ -6,74 +6,12 @@
 // One product kernel serves all three, C [M][N] = sum_k A(m, k) B(k, n), for
 // operands whose values lie along k (X and D in the first two, W in W^T) or
 // across it (W forward, both operands of dW).
-#include "cf_internal.h"
-
-#include <math.h>
+#include "linear_common.h"
 
 namespace cf {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
 constexpr int LIN_T = 256;
-
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
-
-struct LinAct {
-    int act;
-    float slope;
-};
-__device__ __forceinline__ float lin_act(const LinAct& a, float z)
-{
-    if (a.act == CF_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
-    return z > 0.f ? z : a.slope * z;
-}
-__device__ __forceinline__ float lin_dact(const LinAct& a, float z)
-{
-    if (a.act == CF_ACT_SILU) {
-        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
-        return s * fmaf(z, 1.f - s, 1.f);
-    }
-    return z > 0.f ? 1.f : a.slope;
-}
-
-// What becomes of the product.
-enum LinMode {
-    LIN_FWD,        // bias, pre, activation, residual
-    LIN_PLAIN,      // rounded to TO
-};
-
-template <typename T> struct LinProduct {
-    const T* A;
-    const T* B;
-    const T* B2;            // k >= K: B2(k - K, n) with A(m, k - K), or null
-    int64_t M, K;
-    int N;
-    int64_t lda, ldb;
-    int64_t tiles_m;
-    int tiles_n;
-    int splits;             // of the reduction
-    int kb, kb_split;       // pieces of the reduction, and of a split
-    float* part;            // [splits][M][N], where splits > 1
-    float* db_part;         // [db_parts][N], column sums of B
-    int db_parts;
-    void* C;
-    const float* bias;
-    const T* R;
-    T* pre;
-    LinAct act;
-    float* db;
-};
-
-template <typename T> struct LinTile;
-template <> struct LinTile<uint16_t> {
-    static constexpr int V = 8, BK = 64;
-};
-template <> struct LinTile<float> {
-    static constexpr int V = 4, BK = 32;
-};
 
 // Values from p on, of which n are inside; zeros for the others.
 template <typename T> __device__ __forceinline__ uint4 lin_chunk(const T* p, int64_t n)
@@ -156,38 +94,6 @@ template <typename T, bool ALONG, int ROWS> struct LinOperand {
     }
 };
 
-__device__ __forceinline__ void lin_mma(const bf16x8& a, const bf16x8& b, f32x16& c)
-{
-    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ void lin_mma(const f32x4& a, const f32x4& b, f32x16& c)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
-}
-__device__ __forceinline__ bf16x8 ones(const bf16x8&)
-{
-    bf16x8 v;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (__bf16)1.f;
-    return v;
-}
-__device__ __forceinline__ f32x4 ones(const f32x4&) { return f32x4{1.f, 1.f, 1.f, 1.f}; }
-
-// One value of the result.
-template <typename T, typename TO, int MODE>
-__device__ __forceinline__ void lin_result(const LinProduct<T>& q, int64_t m, int n, float v)
-{
-    const int64_t at = m * q.N + n;
-    if (MODE == LIN_FWD) {
-        if (q.bias) v += q.bias[n];
-        if (q.pre) Elem<T>::store(q.pre, at, v);
-        v = lin_act(q.act, v);
-        if (q.R) v += widen(q.R[at]);
-    }
-    Elem<TO>::store((TO*)q.C, at, v);
-}
-
 // TILE x TILE of the result a block, four waves of TILE/2 x TILE/2.
 template <typename T, typename TO, bool AA, bool BA, int TILE, int MODE, bool DB>
 __global__ __launch_bounds__(LIN_T) void lin_product_kernel(LinProduct<T> q)
@@ -195,8 +101,10 @@ __global__ __launch_bounds__(LIN_T) void lin_product_kernel(LinProduct<T> q)
     using OA = LinOperand<T, AA, TILE>;
     using OB = LinOperand<T, BA, TILE>;
     constexpr int BK = LinTile<T>::BK, STEPS = BK / (sizeof(T) == 2 ? 16 : 8), B = TILE / 64;
-    __shared__ __attribute__((aligned(16))) T sa[OA::SIZE];
-    __shared__ __attribute__((aligned(16))) T sb[OB::SIZE];
+    constexpr int STAGE = (OA::SIZE + OB::SIZE) * (int)sizeof(T), OUT = 4 * 32 * (32 * B + 4) * 4;
+    __shared__ __attribute__((aligned(16))) char raw[STAGE > OUT ? STAGE : OUT];
+    T* const sa = (T*)raw;
+    T* const sb = sa + OA::SIZE;
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int wi = wave / 2 * (TILE / 2), wj = wave % 2 * (TILE / 2);
     const int64_t units = q.tiles_m * q.tiles_n * q.splits;
@@ -242,25 +150,22 @@ __global__ __launch_bounds__(LIN_T) void lin_product_kernel(LinProduct<T> q)
                     for (int j = 0; j < B; ++j) lin_mma(ones(fb[j]), fb[j], col[j]);
             }
         }
-        // register r of a lane: row 8 (r / 4) + 4 (lane / 32) + r % 4, column lane % 32
+        if (DB && sums && lane < 32 && q.db)
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
-            const int n = j0 + wj + j * 32 + lane % 32;
-            if (n >= q.N) continue;
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t m = i0 + wi + i * 32 + 8 * (r / 4) + 4 * (lane / 32) + r % 4;
-                    if (m >= q.M) continue;
-                    if (q.splits > 1) q.part[((int64_t)split * q.M + m) * q.N + n] = acc[i][j][r];
-                    else lin_result<T, TO, MODE>(q, m, n, acc[i][j][r]);
-                }
-            if (DB && sums && lane < 32 && q.db) {
+            for (int j = 0; j < B; ++j) {
+                const int n = j0 + wj + j * 32 + lane;
+                if (n >= q.N) continue;
                 if (q.splits > 1) q.db_part[(int64_t)split * q.N + n] = col[j][0];
                 else q.db[n] = col[j][0];
             }
-        }
+        const int n = j0 + wj + lane % (4 * B) * 8;
+        float bias[8] = {};
+        if (MODE == LIN_FWD && q.bias && n < q.N) load8(q.bias + n, q.N - n, bias);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            lin_rows<T, TO, MODE, B>(acc[i], (float*)raw + wave * 32 * (32 * B + 4), q, split, i0 + wi + i * 32, j0 + wj, bias);
+        __syncthreads();
     }
 }
 
@@ -283,11 +188,22 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main
         }
         return;
     }
-    const int64_t total = q.M * q.N;
+    const int vecs = (q.N + 7) / 8;
+    const int64_t total = q.M * vecs;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)main * 256) {
-        float v = 0.f;
-        for (int s = 0; s < q.splits; ++s) v += q.part[s * total + i];
-        lin_result<T, TO, MODE>(q, i / q.N, (int)(i % q.N), v);
+        const int64_t m = i / vecs;
+        const int n = (int)(i - m * vecs) * 8;
+        float v[8] = {}, bias[8] = {}, res[8] = {};
+        if (MODE == LIN_FWD && q.bias) load8(q.bias + n, q.N - n, bias);
+        if (MODE == LIN_FWD && q.R) load8(q.R + m * q.N + n, q.N - n, res);
+#pragma unroll 4
+        for (int s = 0; s < q.splits; ++s) {
+            float p[8];
+            load8(q.part + (s * q.M + m) * q.N + n, q.N - n, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += p[j];
+        }
+        lin_result<T, TO, MODE>(q, m, n, v, bias, res);
     }
 }
 
@@ -355,21 +271,19 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre
     }
 }
 
+// Whether all rows of X, W, D and their gradients start at multiples of 16 bytes.
+bool lin_aligned(int in, int out, int size) { return in * size % 16 == 0 && out * size % 16 == 0; }
+
 size_t up256l(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Tiles and splits of a product.
-struct LinPlan {
-    int tile;
-    int64_t tiles_m;
-    int tiles_n, kb, kb_split, splits;
-    size_t part_bytes, db_bytes;
-};
-LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes)
+LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool aligned)
 {
     LinPlan p;
+    p.aligned = aligned;
     const int bk = size == 2 ? 64 : 32;
     const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128);
     p.tile = t128 >= 256 ? 128 : 64;
+    if (aligned && M >= 4096 && N >= 512 && K >= 512) p.tile = 256;
     p.tiles_m = (M + p.tile - 1) / p.tile;
     p.tiles_n = (N + p.tile - 1) / p.tile;
     p.kb = (int)((K + bk - 1) / bk);
@@ -406,9 +320,9 @@ LinGate lin_gate(int64_t rows, int N, int size)
 // with it; else q.db_part already holds its parts, if q.db is not null.
 template <typename T, typename TO, bool AA, bool BA, int MODE, bool DB>
 hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int64_t lda, const T* B, const T* B2,
-                   int64_t ldb, void* ws, hipStream_t s)
+                   int64_t ldb, bool aligned, void* ws, hipStream_t s)
 {
-    const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1);
+    const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, aligned);
     q.A = A;
     q.B = B;
     q.B2 = B2;
@@ -429,12 +343,17 @@ hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int
     }
     const int64_t units = p.tiles_m * p.tiles_n * p.splits, most = 1 << 20;
     const unsigned grid = (unsigned)(units < most ? units : most);
-    if (p.tile == 128) lin_product_kernel<T, TO, AA, BA, 128, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
-    else lin_product_kernel<T, TO, AA, BA, 64, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
-    hipError_t e = hipGetLastError();
+    hipError_t e;
+    if (p.aligned) {
+        e = launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
+    } else {
+        if (p.tile == 128) lin_product_kernel<T, TO, AA, BA, 128, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
+        else lin_product_kernel<T, TO, AA, BA, 64, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
+        e = hipGetLastError();
+    }
     const bool join_db = q.db && (!DB || p.splits > 1);
     if (e != hipSuccess || (p.splits == 1 && !join_db)) return e;
-    const int64_t blocks = p.splits > 1 ? (M * N + 255) / 256 : 0;
+    const int64_t blocks = p.splits > 1 ? (M * ((N + 7) / 8) + 255) / 256 : 0;
     const int main = (int)(blocks < 4096 ? blocks : 4096);
     lin_join_kernel<T, TO, MODE><<<(unsigned)(main + (join_db ? (N + 15) / 16 : 0)), 256, 0, s>>>(q, main);
     return hipGetLastError();
@@ -445,10 +364,11 @@ hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int
 size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    if (!bwd) return lin_plan(rows, out, in, size, 1).part_bytes;
+    const bool al = lin_aligned(in, out, size);
+    if (!bwd) return lin_plan(rows, out, in, size, 1, al).part_bytes;
     const LinGate g = lin_gate(rows, out, size);
-    const LinPlan x = lin_plan(rows, in, out, size, 1), w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1),
-                  one = lin_plan(in, out, rows, size, 1);
+    const LinPlan x = lin_plan(rows, in, out, size, 1, al),
+                  w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, al), one = lin_plan(in, out, rows, size, 1, al);
     const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes, plain = one.part_bytes + one.db_bytes;
     const size_t most = gated + (w.part_bytes > x.part_bytes ? w.part_bytes : x.part_bytes);
     return most > plain ? most : plain;
@@ -464,14 +384,15 @@ hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T*
     q.R = R;
     q.pre = pre;
     q.act = LinAct{(int)act, slope};
-    return lin_run<T, T, true, false, LIN_FWD, false>(q, rows, out, in, X, in, W, nullptr, out, ws, s);
+    return lin_run<T, T, true, false, LIN_FWD, false>(q, rows, out, in, X, in, W, nullptr, out,
+                                                 lin_aligned(in, out, sizeof(T)), ws, s);
 }
 
 template <typename T>
 hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T* W, const T* pre, const T* dY,
                              cf_act act, float slope, T* dX, float* dW, float* db, void* ws, hipStream_t s)
 {
-    const bool gated = act == CF_ACT_SILU || slope != 1.f;
+    const bool gated = act == CF_ACT_SILU || slope != 1.f, al = lin_aligned(in, out, sizeof(T));
     const T* D = dY;
     const T* lo = nullptr;
     char* at = (char*)ws;
@@ -497,11 +418,12 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
     if (dX) {
         LinProduct<T> q{};
         q.C = dX;
-        const hipError_t e = lin_run<T, T, true, true, LIN_PLAIN, false>(q, rows, in, out, D, out, W, nullptr, out, at, s);
+        const hipError_t e = lin_run<T, T, true, true, LIN_PLAIN, false>(q, rows, in, out, D, out, W, nullptr, out,
+                                                                              al, at, s);
         if (e != hipSuccess) return e;
     }
-    if (gated) return lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, in, D, lo, out, at, s);
-    return lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, in, D, nullptr, out, at, s);
+    if (gated) return lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, in, D, lo, out, al, at, s);
+    return lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, in, D, nullptr, out, al, at, s);
 }
 
 template hipError_t launch_linear_fwd<float>(int64_t, int, int, const float*, const float*, const float*, cf_act, float,
