@@ -45,14 +45,35 @@ struct RnArgs {
     int64_t gate_step;               // from one sample's gate to the next (0: one for all)
 };
 
+// v plus another lane's: 1, 2: lanes that differ in that bit; 4, 8: after the sums
+// over the bits below, any lane of the other half will do, and mirrored rows of 8
+// and 16 have one; 16, 32: rows and halves of the wave swapped.  One instruction
+// each, where a shuffle goes through LDS.
+template <int BIT> __device__ __forceinline__ float lane_sum(float v)
+{
+    if constexpr (BIT <= 8) {
+        constexpr int ctrl = BIT == 1 ? 0xb1 : BIT == 2 ? 0x4e : BIT == 4 ? 0x141 : 0x140;
+        return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xf, 0xf, true));
+    } else {
+        const unsigned u = __builtin_bit_cast(unsigned, v);
+        const auto w = BIT == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                                 : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        return __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
+}
+
 // Sum of v[0..N) over a row's lanes, in each of them.
 template <int LPR, int N> __device__ __forceinline__ void row_sum(float (&v)[N], float* sh, int& turn)
 {
-    constexpr int W = LPR < 64 ? LPR : 64;
 #pragma unroll
-    for (int m = W / 2; m >= 1; m >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m, 64);
+    for (int i = 0; i < N; ++i) {
+        if (LPR > 1) v[i] = lane_sum<1>(v[i]);
+        if (LPR > 2) v[i] = lane_sum<2>(v[i]);
+        if (LPR > 4) v[i] = lane_sum<4>(v[i]);
+        if (LPR > 8) v[i] = lane_sum<8>(v[i]);
+        if (LPR > 16) v[i] = lane_sum<16>(v[i]);
+        if (LPR > 32) v[i] = lane_sum<32>(v[i]);
+    }
     if (LPR > 64) {
         // two buffers in turn: a wave writes one again only after a barrier that the readers of it have reached
         float* at = sh + turn * 16;
@@ -66,50 +87,108 @@ template <int LPR, int N> __device__ __forceinline__ void row_sum(float (&v)[N],
     }
 }
 
-// A lane's E values of a row: E / V vectors of V, LPR vectors apart.
-template <typename T, int LPR, int E> struct RnLane {
+// A lane's E values of a row: E / V vectors of V, LPR vectors apart.  WHOLE: rows are
+// whole vectors.
+template <typename T, int LPR, int E, bool WHOLE> struct RnLane {
     static constexpr int V = 16 / (int)sizeof(T);
     static constexpr int VECS = E / V;
     static_assert(E % V == 0, "whole vectors");
     int lane, C;
     __device__ __forceinline__ int channel(int i) const { return ((i / V) * LPR + lane) * V + i % V; }
-    __device__ __forceinline__ void load(const T* row, float (&v)[E]) const
+    // Whether value i lies in the row.
+    __device__ __forceinline__ bool inside(int i) const { return channel(WHOLE ? i / V * V : i) < C; }
+    struct Raw {
+        uint4 v[VECS];
+    };
+    // Whole vectors without a branch, the last one of a row from V values before its
+    // end on (lanes past the end read it too); unpack() moves the values to their
+    // places.  Rows of less than V values, which lanes in pairs hold, one by one.
+    // `row`: the values' distance from `from`, which all threads share.
+    __device__ __forceinline__ void fetch(const T* from, uint32_t row, Raw& raw) const
     {
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int c = channel(j * V);
-            T t[V] = {};
-            if (c + V <= C) __builtin_memcpy(t, row + c, 16);
-            else if (c < C)
+            if (!WHOLE && LPR == 2 && C < V) {
+                T t[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < C) t[i] = row[c + i];
+                for (int i = 0; i < V; ++i) t[i] = c + i < C ? from[row + (uint32_t)(c + i)] : (T)0;
+                __builtin_memcpy(&raw.v[j], t, 16);
+            } else {
+                __builtin_memcpy(&raw.v[j], from + (row + (uint32_t)min(c, C - V)), 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(const Raw& raw, float (&v)[E]) const
+    {
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) {
+            const int c = channel(j * V);
+            uint32_t w[4] = {raw.v[j].x, raw.v[j].y, raw.v[j].z, raw.v[j].w};
+            if (WHOLE || C >= V) {
+                const int over = c - min(c, C - V);           // values before this vector's first
+                if (!WHOLE) {
+                    const int bytes = over * (int)sizeof(T);
+                    if (bytes & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = 0;
+                    if (bytes & 8) w[0] = w[2], w[1] = w[3], w[2] = w[3] = 0;
+                    if (sizeof(T) == 2 && (bytes & 2)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = w[i] >> 16 | (i < 3 ? w[i < 3 ? i + 1 : 3] << 16 : 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = over >= V ? 0 : w[i];
+            }
+            T t[V];
+            __builtin_memcpy(t, w, 16);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[j * V + i] = widen(t[i]);
         }
     }
-    __device__ __forceinline__ void store(T* row, const float (&v)[E]) const
+    __device__ __forceinline__ void store(T* from, uint32_t row, const float (&v)[E]) const
     {
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-            const int c = channel(j * V);
+            const int c = channel(j * V), n = C - c;
             T t[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) Elem<T>::store(t, i, v[j * V + i]);
-            if (c + V <= C) __builtin_memcpy(row + c, t, 16);
-            else if (c < C)
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (c + i < C) row[c + i] = t[i];
+            uint32_t w[4];
+            __builtin_memcpy(w, t, 16);
+            if (n >= V) __builtin_memcpy(from + (row + (uint32_t)c), w, 16);
+            else if (!WHOLE && n > 0) {
+                const int bytes = n * (int)sizeof(T);
+                char* p = (char*)(from + (row + (uint32_t)c));
+                if (bytes & 8) {
+                    __builtin_memcpy(p, w, 8);
+                    p += 8, w[0] = w[2], w[1] = w[3];
+                }
+                if (bytes & 4) {
+                    __builtin_memcpy(p, w, 4);
+                    p += 4, w[0] = w[1];
+                }
+                if (sizeof(T) == 2 && (bytes & 2)) __builtin_memcpy(p, w, 2);
+            }
         }
     }
     // A vector of C floats (null: `other`), 0 past its end.
     __device__ __forceinline__ void vec(const float* p, float other, float (&v)[E]) const
     {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = channel(i);
-            v[i] = c < C ? (p ? p[c] : other) : 0.f;
+        for (int j = 0; j < VECS; ++j) {
+            const int c = channel(j * V);
+            float t[V];
+            if (!p) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) t[i] = other;
+            } else if (WHOLE) {
+                __builtin_memcpy(t, p + (uint32_t)min(c, C - V), sizeof(t));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) t[i] = p[(uint32_t)min(c + i, C - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[j * V + i] = inside(j * V + i) ? t[i] : 0.f;
         }
     }
 };
@@ -131,7 +210,7 @@ __device__ __forceinline__ float normalise(float (&v)[E], const L& ln, float inv
         s[0] = s[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            v[i] = ln.channel(i) < ln.C ? v[i] - m : 0.f;
+            v[i] = ln.inside(i) ? v[i] - m : 0.f;
             s[0] += v[i];
             s[1] = fmaf(v[i], v[i], s[1]);
         }
@@ -139,7 +218,7 @@ __device__ __forceinline__ float normalise(float (&v)[E], const L& ln, float inv
         const float m2 = s[0] * inv_c;
         const float rstd = rsqrtf(fmaxf(fmaf(s[1], inv_c, -m2 * m2), 0.f) + eps);
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = ln.channel(i) < ln.C ? (v[i] - m2) * rstd : 0.f;
+        for (int i = 0; i < E; ++i) v[i] = ln.inside(i) ? (v[i] - m2) * rstd : 0.f;
         return rstd;
     }
     float q[1] = {0.f};
@@ -175,15 +254,17 @@ __device__ __forceinline__ void through_norm(float (&d)[E], const float (&hat)[E
     for (int i = 0; i < E; ++i) d[i] = rstd * (fmaf(-hat[i], a, d[i]) - b);
 }
 
-template <typename T, bool LAYER, int LPR, int E>
+template <typename T, bool LAYER, int LPR, int E, bool WHOLE>
 __global__ __launch_bounds__(RN_T) void resnorm_fwd_kernel(RnArgs a, RnSplit q, const T* __restrict__ X,
                                                            const T* __restrict__ F, T* __restrict__ R,
                                                            T* __restrict__ Y)
 {
     __shared__ float sh[32];
     int turn = 0;
-    const RnLane<T, LPR, E> ln{(int)threadIdx.x % LPR, a.C};
+    const RnLane<T, LPR, E, WHOLE> ln{(int)threadIdx.x % LPR, a.C};
     constexpr int ROWS = RN_T / LPR;
+    const int mine = (int)threadIdx.x / LPR;      // this lane's row of the ROWS that a block works on
+    using Raw = typename RnLane<T, LPR, E, WHOLE>::Raw;
     float gp[E], bp[E], ga[E], gb[E];
     ln.vec(a.gpre, 1.f, gp);
     ln.vec(a.bpre, 0.f, bp);
@@ -204,21 +285,26 @@ __global__ __launch_bounds__(RN_T) void resnorm_fwd_kernel(RnArgs a, RnSplit q, 
             last = n;
         }
         const int64_t r0 = q.rows * p / q.parts, r1 = q.rows * (p + 1) / q.parts;
-        for (int64_t r = r0 + (int)threadIdx.x / LPR; r < r1; r += ROWS) {
+        for (int64_t r = r0; r < r1; r += ROWS) {
+            if (r + mine >= r1) break;
             const int64_t at = (n * q.rows + r) * a.C;
+            const uint32_t row = (uint32_t)(mine * a.C);
             float f[E], v[E];
-            ln.load(F + at, f);
-            ln.load(X + at, v);
+            Raw rf, rx;
+            ln.fetch(F + at, row, rf);
+            ln.fetch(X + at, row, rx);
+            ln.unpack(rf, f);
+            ln.unpack(rx, v);
             if (a.gpost) normalise<LAYER, LPR>(f, ln, a.inv_c, a.eps, sh, turn);
 #pragma unroll
             for (int i = 0; i < E; ++i) v[i] = fmaf(a.alpha, v[i], fmaf(f[i], ga[i], gb[i]));
-            ln.store(R + at, v);
+            ln.store(R + at, row, v);
             if (Y) {
                 // (of the unrounded values: one rounding in Y, not two)
                 normalise<LAYER, LPR>(v, ln, a.inv_c, a.eps, sh, turn);
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] = fmaf(v[i], gp[i], bp[i]);
-                ln.store(Y + at, v);
+                ln.store(Y + at, row, v);
             }
         }
     }
@@ -247,43 +333,67 @@ __device__ __forceinline__ void column_sums(float (&v)[E], const L& ln, float* s
         out[c] = (sh[c] + sh[LPR * E + c]) + (sh[2 * LPR * E + c] + sh[3 * LPR * E + c]);
 }
 
+// Waves a SIMD that the backward's registers leave room for.
+template <typename T, int E, bool WHOLE> constexpr int rn_waves()
+{
+    return E == 8 ? (sizeof(T) == 2 && WHOLE ? 4 : 2) : (sizeof(T) == 2 && WHOLE ? 2 : 1);
+}
+
 // vecs: [4][blocks][C], the blocks' sums for dgpre, dbpre, dgpost, dbpost;
 // gates: [samples * parts][C], dgate itself where a sample is one part.
-template <typename T, bool LAYER, int LPR, int E>
-__global__ __launch_bounds__(RN_T) void resnorm_bwd_kernel(RnArgs a, RnSplit q, const T* __restrict__ F,
-                                                           const T* __restrict__ R, const T* __restrict__ dR,
-                                                           const T* __restrict__ dY, T* __restrict__ dX,
-                                                           T* __restrict__ dF, float* __restrict__ vecs,
-                                                           float* __restrict__ gates)
+template <typename T, bool LAYER, int LPR, int E, bool WHOLE>
+__global__ __launch_bounds__(RN_T, (rn_waves<T, E, WHOLE>())) void resnorm_bwd_kernel(
+    RnArgs a, RnSplit q, const T* __restrict__ F, const T* __restrict__ R, const T* __restrict__ dR,
+    const T* __restrict__ dY, T* __restrict__ dX, T* __restrict__ dF, float* __restrict__ vecs, float* __restrict__ gates)
 {
     __shared__ float sh[LPR > 64 ? 32 : 4 * LPR * E];
+    // a thread's sums of gate d fh and gate d over all of its rows (items may have gates of their own)
+    __shared__ float sg[2 * E * RN_T];
     int turn = 0;
-    const RnLane<T, LPR, E> ln{(int)threadIdx.x % LPR, a.C};
+    const RnLane<T, LPR, E, WHOLE> ln{(int)threadIdx.x % LPR, a.C};
     constexpr int ROWS = RN_T / LPR;
+    const int mine = (int)threadIdx.x / LPR;      // this lane's row of the ROWS that a block works on
+    using Raw = typename RnLane<T, LPR, E, WHOLE>::Raw;
     float gp[E];
     ln.vec(a.gpre, 1.f, gp);
-    // sums of dY rh, dY, gate d fh, gate d over the block's rows
-    float t1[E] = {}, t0[E] = {}, g1[E] = {}, g0[E] = {};
+    float t1[E] = {}, t0[E] = {};                       // sums of dY rh, dY over the block's rows
+#pragma unroll
+    for (int i = 0; i < 2 * E; ++i) sg[i * RN_T + (int)threadIdx.x] = 0.f;
     const int64_t items = (int64_t)q.samples * q.parts;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int n = (int)(it / q.parts), p = (int)(it % q.parts);
-        float ga[E], gate[E];
-        ln.vec(a.gate ? a.gate + n * a.gate_step : nullptr, 1.f, gate);
-        ln.vec(a.gpost, 1.f, ga);
+        const float* gate_of = a.gate ? a.gate + n * a.gate_step : nullptr;
+        float ga[E], s1[E] = {}, s0[E] = {};            // sums of d fh (of d F without a post norm) and d over the item's rows
+        {
+            float g[E];
+            ln.vec(gate_of, 1.f, g);
+            ln.vec(a.gpost, 1.f, ga);
 #pragma unroll
-        for (int i = 0; i < E; ++i) ga[i] *= gate[i];
-        // sums of d fh (of d F without a post norm) and d over the item's rows
-        float s1[E] = {}, s0[E] = {};
+            for (int i = 0; i < E; ++i) ga[i] *= g[i];
+        }
         const int64_t r0 = q.rows * p / q.parts, r1 = q.rows * (p + 1) / q.parts;
-        for (int64_t r = r0 + (int)threadIdx.x / LPR; r < r1; r += ROWS) {
+        // the next row's values are under way while this one's are worked on
+        Raw rf, rr, rd, ry;
+        auto fetch = [&](int64_t r) {
             const int64_t at = (n * q.rows + r) * a.C;
+            const uint32_t row = (uint32_t)(min((int64_t)mine, r1 - 1 - r) * a.C);
+            ln.fetch(F + at, row, rf);
+            if (dY) ln.fetch(R + at, row, rr), ln.fetch(dY + at, row, ry);
+            if (dR) ln.fetch(dR + at, row, rd);
+        };
+        fetch(r0);
+        for (int64_t r = r0; r < r1; r += ROWS) {
+            const int64_t at = (n * q.rows + r) * a.C;
+            const uint32_t row = (uint32_t)(mine * a.C);
+            const Raw cf = rf, cr = rr, cd = rd, cy = ry;
+            if (r + ROWS < r1) fetch(r + ROWS);
+            if (r + mine >= r1) break;
             float d[E], f[E];
-            ln.load(F + at, f);
             if (dY) {
                 float v[E], y[E];
-                ln.load(R + at, v);
-                ln.load(dY + at, y);
+                ln.unpack(cr, v);
                 const float rstd = normalise<LAYER, LPR>(v, ln, a.inv_c, a.eps, sh, turn);
+                ln.unpack(cy, y);
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     t1[i] = fmaf(y[i], v[i], t1[i]);
@@ -292,41 +402,44 @@ __global__ __launch_bounds__(RN_T) void resnorm_bwd_kernel(RnArgs a, RnSplit q, 
                 }
                 through_norm<LAYER, LPR>(d, v, rstd, a.inv_c, sh, turn);
                 if (dR) {
-                    ln.load(dR + at, y);
+                    ln.unpack(cd, y);
 #pragma unroll
                     for (int i = 0; i < E; ++i) d[i] += y[i];
                 }
             } else {
-                ln.load(dR + at, d);
+                ln.unpack(cd, d);
             }
-            float x[E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = a.alpha * d[i];
-            ln.store(dX + at, x);
+            for (int i = 0; i < E; ++i) f[i] = a.alpha * d[i];
+            ln.store(dX + at, row, f);
+            ln.unpack(cf, f);
             float rstd = 1.f;
             if (a.gpost) rstd = normalise<LAYER, LPR>(f, ln, a.inv_c, a.eps, sh, turn);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                d[i] = ln.channel(i) < a.C ? d[i] : 0.f;
+                if (LAYER) d[i] = ln.inside(i) ? d[i] : 0.f;      // (what the norm took from all: its mean)
                 s1[i] = fmaf(d[i], f[i], s1[i]);
                 s0[i] += d[i];
                 d[i] *= ga[i];
             }
             if (a.gpost) through_norm<LAYER, LPR>(d, f, rstd, a.inv_c, sh, turn);
-            ln.store(dF + at, d);
+            ln.store(dF + at, row, d);
         }
+        float g[E];
+        ln.vec(gate_of, 1.f, g);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            g1[i] = fmaf(gate[i], s1[i], g1[i]);
-            g0[i] = fmaf(gate[i], s0[i], g0[i]);
+            float* at = sg + 2 * i * RN_T + (int)threadIdx.x;
+            at[0] = fmaf(g[i], s1[i], at[0]);
+            at[RN_T] = fmaf(g[i], s0[i], at[RN_T]);
         }
         if (a.gate) {
-            float po[E], bo[E];
-            ln.vec(a.gpost, 1.f, po);
+            float bo[E];
+            ln.vec(a.gpost, 1.f, g);
             ln.vec(a.bpost, 0.f, bo);
 #pragma unroll
-            for (int i = 0; i < E; ++i) po[i] = fmaf(po[i], s1[i], bo[i] * s0[i]);
-            column_sums<LPR, E>(po, ln, sh, gates + it * a.C);
+            for (int i = 0; i < E; ++i) g[i] = fmaf(g[i], s1[i], bo[i] * s0[i]);
+            column_sums<LPR, E>(g, ln, sh, gates + it * a.C);
         }
     }
     const int64_t block = (int64_t)gridDim.x * a.C;
@@ -336,13 +449,19 @@ __global__ __launch_bounds__(RN_T) void resnorm_bwd_kernel(RnArgs a, RnSplit q, 
         column_sums<LPR, E>(t0, ln, sh, out + block);
     }
     if (a.gpost) {
-        column_sums<LPR, E>(g1, ln, sh, out + 2 * block);
-        column_sums<LPR, E>(g0, ln, sh, out + 3 * block);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            t1[i] = sg[2 * i * RN_T + (int)threadIdx.x];
+            t0[i] = sg[(2 * i + 1) * RN_T + (int)threadIdx.x];
+        }
+        column_sums<LPR, E>(t1, ln, sh, out + 2 * block);
+        column_sums<LPR, E>(t0, ln, sh, out + 3 * block);
     }
 }
 
 // Adds partial sums: job j < 4 takes the blocks' sums of one kind, job 4 + n
-// sample n's parts of dgate.  16 columns a block, 16 threads to a column.
+// sample n's parts of dgate.  16 columns a block, 64 threads to a column: the few
+// blocks that a narrow tensor has are bound by the latency of a thread's loads.
 struct RnJoin {
     const float* vecs;
     const float* gates;
@@ -350,22 +469,28 @@ struct RnJoin {
     float* dgate;
     int C, blocks, parts;
 };
-__global__ __launch_bounds__(256) void resnorm_join_kernel(RnJoin q)
+__global__ __launch_bounds__(1024) void resnorm_join_kernel(RnJoin q)
 {
-    __shared__ double sh[16][17];
+    __shared__ double sh[16][16];
     const int job = (int)blockIdx.y, c = (int)blockIdx.x * 16 + (int)threadIdx.x % 16, k = (int)threadIdx.x / 16;
     if (job < 4 && !q.out[job]) return;
     const int len = job < 4 ? q.blocks : q.parts;
     const float* src = job < 4 ? q.vecs + (int64_t)job * q.blocks * q.C : q.gates + (int64_t)(job - 4) * q.parts * q.C;
     double sum = 0.0;
     if (c < q.C)
-        for (int i = k; i < len; i += 16) sum += (double)src[(int64_t)i * q.C + c];
-    sh[k][threadIdx.x % 16] = sum;
+#pragma unroll 8
+        for (int i = k; i < len; i += 64) sum += (double)src[(int64_t)i * q.C + c];
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if ((threadIdx.x & 63) < 16) sh[threadIdx.x >> 6][threadIdx.x & 15] = sum;
     __syncthreads();
-    if (k == 0 && c < q.C) {
-        for (int i = 1; i < 16; ++i) sum += sh[i][threadIdx.x];
-        (job < 4 ? q.out[job] : q.dgate + (int64_t)(job - 4) * q.C)[c] = (float)sum;
-    }
+    if (threadIdx.x >= 64) return;
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += sh[(threadIdx.x >> 4) * 4 + i][threadIdx.x & 15];
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (threadIdx.x < 16 && c < q.C) (job < 4 ? q.out[job] : q.dgate + (int64_t)(job - 4) * q.C)[c] = (float)sum;
 }
 
 // Samples are told apart only where they have gates of their own.
@@ -385,32 +510,38 @@ RnSplit rn_split(const cf_dims& x, int gate_n, int blocks)
 
 size_t up256r(size_t b) { return (b + 255) & ~(size_t)255; }
 
-template <typename T, bool LAYER, int LPR, int E> struct RnKernels {
+template <typename T, bool LAYER, int LPR, int E, bool WHOLE> struct RnKernels {
     static void fwd(const RnArgs& a, const RnSplit& q, const void* X, const void* F, void* R, void* Y, hipStream_t s)
     {
-        resnorm_fwd_kernel<T, LAYER, LPR, E><<<q.blocks, RN_T, 0, s>>>(a, q, (const T*)X, (const T*)F, (T*)R, (T*)Y);
+        resnorm_fwd_kernel<T, LAYER, LPR, E, WHOLE><<<q.blocks, RN_T, 0, s>>>(a, q, (const T*)X, (const T*)F, (T*)R, (T*)Y);
     }
     static void bwd(const RnArgs& a, const RnSplit& q, const void* F, const void* R, const void* dR, const void* dY,
                     void* dX, void* dF, float* vecs, float* gates, hipStream_t s)
     {
-        resnorm_bwd_kernel<T, LAYER, LPR, E><<<q.blocks, RN_T, 0, s>>>(a, q, (const T*)F, (const T*)R, (const T*)dR,
+        resnorm_bwd_kernel<T, LAYER, LPR, E, WHOLE><<<q.blocks, RN_T, 0, s>>>(a, q, (const T*)F, (const T*)R, (const T*)dR,
                                                                        (const T*)dY, (T*)dX, (T*)dF, vecs, gates);
     }
 };
 
 // Calls f with the kernels of a row of C channels: eight values a lane while a
 // wave or less holds the row, sixteen where that saves the exchange between waves.
-template <typename T, bool LAYER, typename Fn> void rn_pick(int C, Fn f)
+template <typename T, bool LAYER, bool WHOLE, typename Fn> void rn_pick(int C, Fn f)
 {
-    if (C <= 16) f(RnKernels<T, LAYER, 2, 8>());
-    else if (C <= 32) f(RnKernels<T, LAYER, 4, 8>());
-    else if (C <= 64) f(RnKernels<T, LAYER, 8, 8>());
-    else if (C <= 128) f(RnKernels<T, LAYER, 16, 8>());
-    else if (C <= 256) f(RnKernels<T, LAYER, 32, 8>());
-    else if (C <= 512) f(RnKernels<T, LAYER, 64, 8>());
-    else if (C <= 1024) f(RnKernels<T, LAYER, 64, 16>());
-    else if (C <= 2048) f(RnKernels<T, LAYER, 256, 8>());
-    else f(RnKernels<T, LAYER, 256, 16>());
+    if (C <= 16) f(RnKernels<T, LAYER, 2, 8, WHOLE>());
+    else if (C <= 32) f(RnKernels<T, LAYER, 4, 8, WHOLE>());
+    else if (C <= 64) f(RnKernels<T, LAYER, 8, 8, WHOLE>());
+    else if (C <= 128) f(RnKernels<T, LAYER, 16, 8, WHOLE>());
+    else if (C <= 256) f(RnKernels<T, LAYER, 32, 8, WHOLE>());
+    else if (C <= 512) f(RnKernels<T, LAYER, 64, 8, WHOLE>());
+    else if (C <= 1024) f(RnKernels<T, LAYER, 64, 16, WHOLE>());
+    else if (C <= 2048) f(RnKernels<T, LAYER, 256, 8, WHOLE>());
+    else f(RnKernels<T, LAYER, 256, 16, WHOLE>());
+}
+template <typename T, typename Fn> void rn_pick(bool layer, int C, Fn f)
+{
+    const bool whole = C % (16 / (int)sizeof(T)) == 0;
+    if (layer) whole ? rn_pick<T, true, true>(C, f) : rn_pick<T, true, false>(C, f);
+    else whole ? rn_pick<T, false, true>(C, f) : rn_pick<T, false, false>(C, f);
 }
 
 RnArgs rn_args(const cf_dims& x, const ResnormArgs& p)
@@ -445,8 +576,7 @@ hipError_t launch_resnorm_fwd(const cf_dims& x, const ResnormArgs& p, const void
     const RnSplit q = rn_split(x, p.gate_n, RN_FWD_BLOCKS);
     const RnArgs a = rn_args(x, p);
     auto go = [&](auto k) { k.fwd(a, q, X, F, R, Y, s); };
-    if (p.layer) rn_pick<T, true>(a.C, go);
-    else rn_pick<T, false>(a.C, go);
+    rn_pick<T>(p.layer, a.C, go);
     return hipGetLastError();
 }
 
@@ -460,14 +590,13 @@ hipError_t launch_resnorm_bwd(const cf_dims& x, const ResnormArgs& p, const void
     float* parts = (float*)((char*)ws + up256r((size_t)4 * q.blocks * x.c * sizeof(float)));
     float* gates = q.parts == 1 ? g.gate : parts;
     auto go = [&](auto k) { k.bwd(a, q, F, R, dR, dY, dX, dF, vecs, gates, s); };
-    if (p.layer) rn_pick<T, true>(a.C, go);
-    else rn_pick<T, false>(a.C, go);
+    rn_pick<T>(p.layer, a.C, go);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const RnJoin j = {vecs, parts, {dY ? g.gpre : nullptr, dY ? g.bpre : nullptr, g.gpost, g.bpost}, g.gate, a.C,
                       q.blocks, q.parts};
     const int jobs = 4 + (p.gate && q.parts > 1 ? q.samples : 0);
-    resnorm_join_kernel<<<dim3((unsigned)((a.C + 15) / 16), (unsigned)jobs), 256, 0, s>>>(j);
+    resnorm_join_kernel<<<dim3((unsigned)((a.C + 15) / 16), (unsigned)jobs), 1024, 0, s>>>(j);
     return hipGetLastError();
 }
 
