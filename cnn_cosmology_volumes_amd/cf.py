@@ -11,6 +11,7 @@ GPU.  With stream=s they make their outputs in s's memory; order s
 after what wrote the inputs, and the current stream after s before it reads the
 outputs (wait_stream).
 """
+import array
 import ctypes
 import os
 
@@ -514,20 +515,26 @@ def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
         raise ValueError("grads must not be empty, and out be as long")
     if stream is not None:
         return _on_stream(stream, cf_grad_clip, (*grads, *(out or ()), stats, ws), grads, max_norm, out, stats, ws)
+    # (lists at a time: hundreds of tensors take longer here than on the GPU if each is looked at by itself)
     first = grads[0]
     dt, kind = dtype_code(first.dtype), first.dtype
-    for i, t in enumerate(grads):
-        _packed("gradient %d" % i, t, kind)
-        if out is not None:
-            _packed("output %d" % i, out[i], kind, t.shape)
+    every = grads if out is None else [*grads, *out]
+    if not all([t.dtype is kind and t.is_contiguous() for t in every]) or (
+            out is not None and [t.shape for t in grads] != [t.shape for t in out]):
+        for i, t in enumerate(grads):
+            _packed("gradient %d" % i, t, kind)
+            if out is not None:
+                _packed("output %d" % i, out[i], kind, t.shape)
     if stats is not None:
         _packed("stats", stats, torch.float32, (2,))
-    s = _on_gpu(ws, *grads, *(out or ()), stats)
-    n = (ctypes.c_int64 * k)(*[t.numel() for t in grads])
+    at = first.get_device()
+    s = _on_gpu(ws, first, stats, *[t for t in every if t.get_device() != at][:1])
+    n = (ctypes.c_int64 * k).from_buffer(array.array("q", [t.numel() for t in grads]))
+    pointers = lambda ts: (_P * k).from_buffer(array.array("Q", [t.data_ptr() for t in ts]))
     stats = first.new_empty(2, dtype=torch.float32) if stats is None else stats
     L = lib()
     ws = _ws(L.cf_grad_clip_workspace_size(dt, k, n), first.device, ws)
-    check(L.cf_grad_clip(dt, k, n, _pointers(grads), None if out is None else _pointers(out), float(max_norm),
+    check(L.cf_grad_clip(dt, k, n, pointers(grads), None if out is None else pointers(out), float(max_norm),
                          _ptr(stats), _ptr(ws), _wsbytes(ws), s))
     return stats
 

@@ -1294,7 +1294,7 @@ static ResnormArgs resnorm_args(const cf_resnorm_params& p)
 size_t cf_resnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t gate_n)
 {
     if (check_resnorm(dtype, x, gate_n, "cf_resnorm_workspace_size") != CF_OK) return 0;
-    return resnorm_ws_bytes(x, gate_n);
+    return resnorm_ws_bytes(dtype, x, gate_n);
 }
 
 cf_status cf_resnorm_fwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* X, const void* F, void* R,
@@ -1327,7 +1327,7 @@ cf_status cf_resnorm_bwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, 
     if (!al16(F) || !al16(R) || !al16(dR) || !al16(dY) || !al16(dX) || !al16(dF) || !al16(dgpre) || !al16(dbpre) ||
         !al16(dgpost) || !al16(dbpost) || !al16(dgate))
         return fail(CF_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
-    const size_t need = resnorm_ws_bytes(x, p->gate_n);
+    const size_t need = resnorm_ws_bytes(dtype, x, p->gate_n);
     if (ws_bytes < need) return fail(CF_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
     if (!ws || !al16(ws)) return fail(CF_ERR_INVALID, "%s: workspace null or misaligned", fn);
     const size_t bytes = gn_bytes(dtype, x), c = (size_t)x.c * sizeof(float);

@@ -383,7 +383,7 @@ struct ResnormArgs {
 struct ResnormGrads {
     float *gpre, *bpre, *gpost, *bpost, *gate;      // null where there is none
 };
-size_t resnorm_ws_bytes(const cf_dims& x, int gate_n);
+size_t resnorm_ws_bytes(cf_dtype dt, const cf_dims& x, int gate_n);
 template <typename T>
 hipError_t launch_resnorm_fwd(const cf_dims& x, const ResnormArgs& p, const void* X, const void* F, void* R, void* Y,
                               hipStream_t s);

@@ -22,7 +22,7 @@ constexpr int CLIP_T = 256;                 // threads a block
 constexpr int CLIP_V = 4;                   // 16-byte vectors a thread and chunk
 constexpr int CLIP_BYTES = CLIP_T * CLIP_V * 16;
 constexpr int CLIP_LIST = 128;              // tensors a launch (its arguments stay below 4 KB)
-constexpr int CLIP_BLOCKS = 1024;           // most blocks a launch
+constexpr int CLIP_BLOCKS = 2048;           // most blocks a launch, 8 a CU
 
 template <typename T> struct ClipList {
     int count;
@@ -58,41 +58,55 @@ __device__ __forceinline__ double block_sum(double v, double* sh)
     return ((sh[0] + sh[1]) + sh[2]) + sh[3];
 }
 
+// A thread's values of a chunk whose tensor has n left.
+template <typename T> struct ClipVecs {
+    static constexpr int V = 16 / (int)sizeof(T);
+    T v[CLIP_V][V];
+    __device__ __forceinline__ static int place(int k) { return (k * CLIP_T + (int)threadIdx.x) * V; }
+    __device__ __forceinline__ void load(const T* g, int64_t n)
+    {
+        if (n >= CLIP_T * CLIP_V * V) {
+#pragma unroll
+            for (int k = 0; k < CLIP_V; ++k) __builtin_memcpy(v[k], g + place(k), 16);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < CLIP_V; ++k) {
+            const int i = place(k);
+            if (i + V <= n) __builtin_memcpy(v[k], g + i, 16);
+            else
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[k][e] = i + e < n ? g[i + e] : (T)0;
+        }
+    }
+};
+
 template <typename T>
 __global__ __launch_bounds__(CLIP_T) void clip_norm_kernel(ClipList<T> l, double* __restrict__ part)
 {
     constexpr int V = 16 / (int)sizeof(T);
     __shared__ double sh[4];
-    double sum = 0.0;
-    for (int c = (int)blockIdx.x; c < l.chunks; c += (int)gridDim.x) {
+    double sum[CLIP_V] = {};
+    ClipVecs<T> x;
+    auto fetch = [&](int c) {
         const int t = clip_tensor(l, c);
-        const int64_t at = (int64_t)(c - l.start[t]) * (CLIP_T * CLIP_V * V), n = l.n[t] - at;
-        const T* __restrict__ g = l.g[t] + at;
-        T v[CLIP_V][V] = {};
-        if (n >= CLIP_T * CLIP_V * V) {
-#pragma unroll
-            for (int k = 0; k < CLIP_V; ++k) __builtin_memcpy(v[k], g + (k * CLIP_T + (int)threadIdx.x) * V, 16);
-        } else {
-#pragma unroll
-            for (int k = 0; k < CLIP_V; ++k) {
-                const int i = (k * CLIP_T + (int)threadIdx.x) * V;
-                if (i + V <= n) __builtin_memcpy(v[k], g + i, 16);
-                else
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (i + e < n) v[k][e] = g[i + e];
-            }
-        }
+        const int64_t at = (int64_t)(c - l.start[t]) * (CLIP_T * CLIP_V * V);
+        x.load(l.g[t] + at, l.n[t] - at);
+    };
+    fetch((int)blockIdx.x);
+    for (int c = (int)blockIdx.x; c < l.chunks; c += (int)gridDim.x) {
+        const ClipVecs<T> y = x;
+        if (c + (int)gridDim.x < l.chunks) fetch(c + (int)gridDim.x);      // under way while these are added
 #pragma unroll
         for (int k = 0; k < CLIP_V; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const double x = (double)widen(v[k][e]);
-                sum = fma(x, x, sum);
+                const double g = (double)widen(y.v[k][e]);
+                sum[k] = fma(g, g, sum[k]);
             }
     }
-    sum = block_sum(sum, sh);
-    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+    const double total = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), sh);
+    if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
 template <typename T>
@@ -101,7 +115,22 @@ __global__ __launch_bounds__(CLIP_T) void clip_scale_kernel(ClipList<T> l, const
 {
     constexpr int V = 16 / (int)sizeof(T);
     __shared__ double sh[4];
+    // the first chunk's values are under way while the sums are added
+    ClipVecs<T> x;
+    const T* g = nullptr;
+    T* out = nullptr;
+    int64_t n = 0;
+    auto fetch = [&](int b) {
+        const int c = l.chunks - 1 - b, t = clip_tensor(l, c);
+        const int64_t at = (int64_t)(c - l.start[t]) * (CLIP_T * CLIP_V * V);
+        g = l.g[t] + at;
+        out = l.out[t] + at;
+        n = l.n[t] - at;
+        x.load(g, n);
+    };
+    fetch((int)blockIdx.x);
     double sum = 0.0;
+#pragma unroll 4
     for (int i = (int)threadIdx.x; i < parts; i += CLIP_T) sum += part[i];
     const double norm = sqrt(block_sum(sum, sh));
     // (a norm that is not a number gives a factor that is none either)
@@ -110,33 +139,22 @@ __global__ __launch_bounds__(CLIP_T) void clip_scale_kernel(ClipList<T> l, const
         stats[0] = (float)norm;
         stats[1] = factor;
     }
-    for (int b = (int)blockIdx.x; b < l.chunks; b += (int)gridDim.x) {
-        const int c = l.chunks - 1 - b, t = clip_tensor(l, c);
-        const int64_t at = (int64_t)(c - l.start[t]) * (CLIP_T * CLIP_V * V), n = l.n[t] - at;
-        const T* g = l.g[t] + at;
-        T* out = l.out[t] + at;
-        if (factor == 1.f && g == out) continue;
-        T v[CLIP_V][V] = {};
+    for (int b = (int)blockIdx.x;;) {
+        if (factor != 1.f || g != out)
 #pragma unroll
-        for (int k = 0; k < CLIP_V; ++k) {
-            const int i = (k * CLIP_T + (int)threadIdx.x) * V;
-            if (i + V <= n) __builtin_memcpy(v[k], g + i, 16);
-            else
+            for (int k = 0; k < CLIP_V; ++k) {
+                const int i = x.place(k);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (i + e < n) v[k][e] = g[i + e];
-        }
+                for (int e = 0; e < V; ++e) Elem<T>::store(x.v[k], e, widen(x.v[k][e]) * factor);
+                if (i + V <= n) __builtin_memcpy(out + i, x.v[k], 16);
+                else
 #pragma unroll
-        for (int k = 0; k < CLIP_V; ++k) {
-            const int i = (k * CLIP_T + (int)threadIdx.x) * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) Elem<T>::store(v[k], e, widen(v[k][e]) * factor);
-            if (i + V <= n) __builtin_memcpy(out + i, v[k], 16);
-            else
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (i + e < n) out[i + e] = v[k][e];
-        }
+                    for (int e = 0; e < V; ++e)
+                        if (i + e < n) out[i + e] = x.v[k][e];
+            }
+        b += (int)gridDim.x;
+        if (b >= l.chunks) break;
+        fetch(b);
     }
 }
 
@@ -164,8 +182,10 @@ hipError_t launch_grad_clip(int count, const int64_t* n, const void* const* g, v
 {
     double* part = (double*)ws;
     int parts = 0;
+    const int last = (count - 1) / CLIP_LIST * CLIP_LIST;
     for (int pass = 0; pass < 2; ++pass)
-        for (int i = 0; i < count; i += CLIP_LIST) {
+        for (int at = 0; at < count; at += CLIP_LIST) {
+            const int i = pass == 0 ? at : last - at;
             ClipList<T> l;
             l.count = count - i < CLIP_LIST ? count - i : CLIP_LIST;
             l.chunks = 0;

@@ -3,217 +3,127 @@
 // and backward, with D = dY act'(pre):
 //   dX = D W^T,  dW = X^T D,  db = column sums of D.
 //
-// One product kernel serves all three, C [M][N] = sum_k A(m, k) B(k, n), for
-// operands whose values lie along k (X and D in the first two, W in W^T) or
-// across it (W forward, both operands of dW).
+// Three products C [M][N] = sum_k A(m, k) B(k, n) (k_linear_mm.hip), whose operands
+// lie along the reduction (X and D in the first two, W in W^T) or across it (W
+// forward, both operands of dW); few rows have kernels of their own
+// (k_linear_few.hip).  Here: what goes before and after a product, which tile and
+// split it takes, and the calls.
 #include "linear_common.h"
 
 namespace cf {
 namespace {
 
-constexpr int LIN_T = 256;
+size_t up256l(size_t b) { return (b + 255) & ~(size_t)255; }
+int up_vec(int n, int size) { return (n + 16 / size - 1) / (16 / size) * (16 / size); }
 
-// Values from p on, of which n are inside; zeros for the others.
-template <typename T> __device__ __forceinline__ uint4 lin_chunk(const T* p, int64_t n)
-{
-    constexpr int V = LinTile<T>::V;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (n >= V) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (n > 0) {
-        T t[V] = {};
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < n) t[i] = p[i];
-        __builtin_memcpy(&v, t, 16);
-    }
-    return v;
-}
-
-// An operand's piece in LDS: along k [ROWS][BK], across it [BK][ROWS], rows a
-// few banks apart.
-template <typename T, bool ALONG, int ROWS> struct LinOperand {
-    static constexpr int V = LinTile<T>::V, BK = LinTile<T>::BK;
-    static constexpr int PITCH = ALONG ? BK + V : ROWS + (sizeof(T) == 2 ? 32 : 8);
-    static constexpr int SIZE = (ALONG ? ROWS : BK) * PITCH;
-    static constexpr int CHUNKS = ROWS * BK / V / LIN_T;        // a thread's
-    static_assert(ROWS * BK / V % LIN_T == 0, "whole rounds");
-
-    __device__ static __forceinline__ void fetch(uint4 (&reg)[CHUNKS], const T* p, int64_t ld, int64_t r0, int64_t rows,
-                                                 int64_t k0, int64_t K)
-    {
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int c = i * LIN_T + (int)threadIdx.x;
-            if (ALONG) {
-                const int64_t r = r0 + c / (BK / V), k = k0 + c % (BK / V) * V;
-                reg[i] = lin_chunk<T>(p + r * ld + k, r < rows ? K - k : 0);
-            } else {
-                const int64_t k = k0 + c / (ROWS / V), r = r0 + c % (ROWS / V) * V;
-                reg[i] = lin_chunk<T>(p + k * ld + r, k < K ? rows - r : 0);
-            }
-        }
-    }
-    __device__ static __forceinline__ void put(T* s, const uint4 (&reg)[CHUNKS])
-    {
-#pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) {
-            const int c = i * LIN_T + (int)threadIdx.x;
-            const int at = ALONG ? c / (BK / V) * PITCH + c % (BK / V) * V : c / (ROWS / V) * PITCH + c % (ROWS / V) * V;
-            *reinterpret_cast<uint4*>(s + at) = reg[i];
-        }
-    }
-    // bf16: the fragment of a 32 x 32 x 16 product at row r, step ks of the piece:
-    // row r + lane % 32, k = 16 ks + 8 (lane / 32) + 0..7.
-    __device__ static __forceinline__ bf16x8 frag(const uint16_t* s, int r, int ks)
-    {
-        const int lane = (int)threadIdx.x & 63;
-        if (ALONG) return *reinterpret_cast<const bf16x8*>(s + (r + lane % 32) * PITCH + ks * 16 + lane / 32 * 8);
-        // Sixteen lanes read four values of four rows of k each; lane i gets
-        // column i of these 4 x 16 values.
-        const int i = lane & 15, row = r + (lane & 16) + 4 * (i & 3), k = ks * 16 + lane / 32 * 8 + (i >> 2);
-        typedef __attribute__((address_space(3))) s16x4* lds4;
-        union {
-            s16x4 h[2];
-            bf16x8 v;
-        } u;
-        u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(s + k * PITCH + row));
-        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(s + (k + 4) * PITCH + row));
-        return u.v;
-    }
-    // fp32: values of row r + lane % 32 at k = 8 ks + 4 (lane / 32) + 0..3, one for
-    // each of four 32 x 32 x 2 products.
-    __device__ static __forceinline__ f32x4 frag(const float* s, int r, int ks)
-    {
-        const int lane = (int)threadIdx.x & 63, k = ks * 8 + lane / 32 * 4;
-        if (ALONG) return *reinterpret_cast<const f32x4*>(s + (r + lane % 32) * PITCH + k);
-        f32x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = s[(k + j) * PITCH + r + lane % 32];
-        return v;
-    }
-};
-
-// TILE x TILE of the result a block, four waves of TILE/2 x TILE/2.
-template <typename T, typename TO, bool AA, bool BA, int TILE, int MODE, bool DB>
-__global__ __launch_bounds__(LIN_T) void lin_product_kernel(LinProduct<T> q)
-{
-    using OA = LinOperand<T, AA, TILE>;
-    using OB = LinOperand<T, BA, TILE>;
-    constexpr int BK = LinTile<T>::BK, STEPS = BK / (sizeof(T) == 2 ? 16 : 8), B = TILE / 64;
-    constexpr int STAGE = (OA::SIZE + OB::SIZE) * (int)sizeof(T), OUT = 4 * 32 * (32 * B + 4) * 4;
-    __shared__ __attribute__((aligned(16))) char raw[STAGE > OUT ? STAGE : OUT];
-    T* const sa = (T*)raw;
-    T* const sb = sa + OA::SIZE;
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int wi = wave / 2 * (TILE / 2), wj = wave % 2 * (TILE / 2);
-    const int64_t units = q.tiles_m * q.tiles_n * q.splits;
-    for (int64_t u = xcd_remap(blockIdx.x, gridDim.x); u < units; u += gridDim.x) {
-        const int split = (int)(u % q.splits);
-        const int64_t t = u / q.splits, ti = t / q.tiles_n;
-        const int tj = (int)(t % q.tiles_n);
-        const int64_t i0 = ti * TILE;
-        const int j0 = tj * TILE;
-        const int b0 = split * q.kb_split, total = q.B2 ? 2 * q.kb : q.kb;
-        const int b1 = min(b0 + q.kb_split, total);
-        f32x16 acc[B][B] = {};
-        f32x16 col[B] = {};
-        const bool sums = DB && ti == 0 && wi == 0;
-        uint4 ra[OA::CHUNKS], rb[OB::CHUNKS];
-        auto fetch = [&](int b) {
-            const bool second = b >= q.kb;
-            const int64_t k0 = (int64_t)(second ? b - q.kb : b) * BK;
-            OA::fetch(ra, q.A, q.lda, i0, q.M, k0, q.K);
-            OB::fetch(rb, second ? q.B2 : q.B, q.ldb, j0, q.N, k0, q.K);
-        };
-        if (b0 < b1) fetch(b0);
-        for (int b = b0; b < b1; ++b) {
-            __syncthreads();
-            OA::put(sa, ra);
-            OB::put(sb, rb);
-            __syncthreads();
-            if (b + 1 < b1) fetch(b + 1);
-#pragma unroll
-            for (int ks = 0; ks < STEPS; ++ks) {
-                decltype(OA::frag(sa, 0, 0)) fa[B], fb[B];
-#pragma unroll
-                for (int i = 0; i < B; ++i) {
-                    fa[i] = OA::frag(sa, wi + i * 32, ks);
-                    fb[i] = OB::frag(sb, wj + i * 32, ks);
-                }
-#pragma unroll
-                for (int i = 0; i < B; ++i)
-#pragma unroll
-                    for (int j = 0; j < B; ++j) lin_mma(fa[i], fb[j], acc[i][j]);
-                if (DB && sums)
-#pragma unroll
-                    for (int j = 0; j < B; ++j) lin_mma(ones(fb[j]), fb[j], col[j]);
-            }
-        }
-        if (DB && sums && lane < 32 && q.db)
-#pragma unroll
-            for (int j = 0; j < B; ++j) {
-                const int n = j0 + wj + j * 32 + lane;
-                if (n >= q.N) continue;
-                if (q.splits > 1) q.db_part[(int64_t)split * q.N + n] = col[j][0];
-                else q.db[n] = col[j][0];
-            }
-        const int n = j0 + wj + lane % (4 * B) * 8;
-        float bias[8] = {};
-        if (MODE == LIN_FWD && q.bias && n < q.N) load8(q.bias + n, q.N - n, bias);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-            lin_rows<T, TO, MODE, B>(acc[i], (float*)raw + wave * 32 * (32 * B + 4), q, split, i0 + wi + i * 32, j0 + wj, bias);
-        __syncthreads();
-    }
-}
-
-// Adds the splits' sums in order, and in the blocks past `main` those of db, 16
-// columns a block and 16 threads to a column.
-template <typename T, typename TO, int MODE>
+// Adds the splits' sums, and in the blocks past `main` those of db, 16 columns a
+// block and 16 threads to a column.  32 vectors of eight columns a block, and GROUPS
+// threads to each, which take every GROUPS-th split: the few results of a long
+// reduction are bound by the latency of a thread's loads.
+template <typename T, typename TO, int MODE, int GROUPS>
 __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main)
 {
-    __shared__ double sh[16][17];
+    constexpr int VECS = 256 / GROUPS;
+    __shared__ union {
+        double col[16][17];
+        float part[GROUPS][VECS][8];
+    } sh;
     if ((int)blockIdx.x >= main) {
         const int c = ((int)blockIdx.x - main) * 16 + (int)threadIdx.x % 16, k = (int)threadIdx.x / 16;
         double sum = 0.0;
         if (c < q.N)
+#pragma unroll 4
             for (int i = k; i < q.db_parts; i += 16) sum += (double)q.db_part[(int64_t)i * q.N + c];
-        sh[k][threadIdx.x % 16] = sum;
+        sh.col[k][threadIdx.x % 16] = sum;
         __syncthreads();
         if (k == 0 && c < q.N) {
-            for (int i = 1; i < 16; ++i) sum += sh[i][threadIdx.x];
+            for (int i = 1; i < 16; ++i) sum += sh.col[i][threadIdx.x];
             q.db[c] = (float)sum;
         }
         return;
     }
-    const int vecs = (q.N + 7) / 8;
+    const int vecs = (q.N + 7) / 8, mine = (int)threadIdx.x % VECS, group = (int)threadIdx.x / VECS;
     const int64_t total = q.M * vecs;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)main * 256) {
-        const int64_t m = i / vecs;
+    for (int64_t i0 = (int64_t)blockIdx.x * VECS; i0 < total; i0 += (int64_t)main * VECS) {
+        const int64_t i = i0 + mine, m = i / vecs;
         const int n = (int)(i - m * vecs) * 8;
-        float v[8] = {}, bias[8] = {}, res[8] = {};
-        if (MODE == LIN_FWD && q.bias) load8(q.bias + n, q.N - n, bias);
-        if (MODE == LIN_FWD && q.R) load8(q.R + m * q.N + n, q.N - n, res);
-#pragma unroll 4
-        for (int s = 0; s < q.splits; ++s) {
-            float p[8];
-            load8(q.part + (s * q.M + m) * q.N + n, q.N - n, p);
+        float v[8] = {};
+        if (i < total) {
+            const float* p = q.part + (group * q.M + m) * q.N + n;
+            const int64_t step = GROUPS * q.M * q.N;
+            auto add = [&](const Lin8<float>& t) {
+                float u[8];
+                t.get(u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += p[j];
+                for (int j = 0; j < 8; ++j) v[j] += u[j];
+            };
+            if (q.N - n >= 8) {
+#pragma unroll 4
+                for (int s = group; s < q.splits; s += GROUPS, p += step) {
+                    Lin8<float> t;
+                    t.load(p);
+                    add(t);
+                }
+            } else {
+                for (int s = group; s < q.splits; s += GROUPS, p += step) {
+                    Lin8<float> t;
+                    t.load(p, q.N - n);
+                    add(t);
+                }
+            }
         }
-        lin_result<T, TO, MODE>(q, m, n, v, bias, res);
+        if (GROUPS > 1) {
+            __syncthreads();
+            __builtin_memcpy(sh.part[group][mine], v, 32);
+            __syncthreads();
+            if (group) continue;
+#pragma unroll
+            for (int g = 1; g < GROUPS; ++g)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += sh.part[g][mine][j];
+        }
+        if (i >= total) continue;
+        float bias[8] = {};
+        Lin8<T> res = {};
+        if (MODE != LIN_PLAIN && q.bias) load8<false>(q.bias + n, q.N - n, bias);
+        if (MODE == LIN_FWD_RES) {
+            if (q.N - n >= 8) res.load(q.R + m * q.N + n);
+            else res.load(q.R + m * q.N + n, q.N - n);
+        }
+        lin_result<false, T, TO, MODE>(q, m * q.N + n, n, v, bias, res);
     }
 }
 
-// D = dY act'(pre): fp32, or as bf16 hi and lo = D - hi, which together keep 16
-// bits or more: dW is fp32 and would show the rounding of hi alone (2^-9 of every
-// term).  dX, rounded to bf16 itself, takes hi alone.
+// Copies of matrices whose rows are not whole vectors, with rows that are: the
+// products' loads take 16 bytes at multiples of 16.  (Reading such rows as they are,
+// value by value at their ends and through registers, took 7429 x 333 x 1001 82 us
+// in fp32 and 32 in bf16.)
+struct LinPack {
+    const void* from[3];
+    void* to[3];
+    int64_t vecs[3];        // of a copy
+    int cols[3];
+};
+template <typename T> __global__ __launch_bounds__(256) void lin_pack_kernel(LinPack q)
+{
+    constexpr int V = LinTile<T>::V;
+    const int job = (int)blockIdx.y, cols = q.cols[job], each = (cols + V - 1) / V;
+    const T* from = (const T*)q.from[job];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < q.vecs[job]; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / each;
+        const int c = (int)(i - r * each) * V;
+        const uint4 v = lin_chunk<T>(from + r * cols + c, cols - c, cols >= V);
+        __builtin_memcpy((T*)q.to[job] + i * V, &v, 16);
+    }
+}
+
+// D = dY act'(pre) with rows of `ld` values: fp32, or as bf16 hi and lo = D - hi,
+// which together keep 16 bits or more: dW is fp32 and would show the rounding of hi
+// alone (2^-9 of every term).  dX, rounded to bf16 itself, takes hi alone.
 // A block takes a range of rows, 2^lg lanes to a row, and leaves the column sums of D.
 template <typename T>
 __global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre, const T* __restrict__ dY, T* hi, T* lo,
-                                                       int64_t rows, int N, int lg, LinAct act, float* db_part)
+                                                       int64_t rows, int N, int ld, int lg, LinAct act, float* db_part)
 {
     constexpr int V = LinTile<T>::V;
     __shared__ float sh[256 * V];
@@ -222,20 +132,10 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre
     float sum[V] = {};
     if (c < N)
         for (int64_t r = r0 + ((int)threadIdx.x >> lg); r < r1; r += 256 >> lg) {
-            const int64_t at = r * N + c;
-            T z[V] = {}, d[V] = {}, h[V], l[V];
-            const bool whole = c + V <= N;
-            if (whole) {
-                __builtin_memcpy(z, pre + at, 16);
-                __builtin_memcpy(d, dY + at, 16);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (c + j < N) {
-                        z[j] = pre[at + j];
-                        d[j] = dY[at + j];
-                    }
-            }
+            const uint4 zv = lin_chunk<T>(pre + r * N + c, N - c, N >= V), dv = lin_chunk<T>(dY + r * N + c, N - c, N >= V);
+            T z[V], d[V], h[V], l[V];
+            __builtin_memcpy(z, &zv, 16);
+            __builtin_memcpy(d, &dv, 16);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float v = widen(d[j]) * lin_dact(act, widen(z[j]));
@@ -245,17 +145,8 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre
                 const float rest = v - widen(h[j]);
                 if (sizeof(T) == 2) Elem<T>::store(l, j, __builtin_isfinite(widen(h[j])) ? rest : 0.f);
             }
-            if (whole) {
-                __builtin_memcpy(hi + at, h, 16);
-                if (sizeof(T) == 2) __builtin_memcpy(lo + at, l, 16);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (c + j < N) {
-                        hi[at + j] = h[j];
-                        if (sizeof(T) == 2) lo[at + j] = l[j];
-                    }
-            }
+            __builtin_memcpy(hi + r * ld + c, h, 16);
+            if (sizeof(T) == 2) __builtin_memcpy(lo + r * ld + c, l, 16);
         }
     if (!db_part) return;
 #pragma unroll
@@ -269,32 +160,6 @@ __global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre
         for (int g = 0; g < 256 >> lg; ++g) v += sh[j * 256 + (g << lg) + k];
         db_part[(int64_t)blockIdx.x * N + col] = v;
     }
-}
-
-// Whether all rows of X, W, D and their gradients start at multiples of 16 bytes.
-bool lin_aligned(int in, int out, int size) { return in * size % 16 == 0 && out * size % 16 == 0; }
-
-size_t up256l(size_t b) { return (b + 255) & ~(size_t)255; }
-
-LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool aligned)
-{
-    LinPlan p;
-    p.aligned = aligned;
-    const int bk = size == 2 ? 64 : 32;
-    const int64_t t128 = (M + 127) / 128 * ((N + 127) / 128);
-    p.tile = t128 >= 256 ? 128 : 64;
-    if (aligned && M >= 4096 && N >= 512 && K >= 512) p.tile = 256;
-    p.tiles_m = (M + p.tile - 1) / p.tile;
-    p.tiles_n = (N + p.tile - 1) / p.tile;
-    p.kb = (int)((K + bk - 1) / bk);
-    const int64_t tiles = p.tiles_m * p.tiles_n, total = (int64_t)p.kb * passes;
-    int64_t want = tiles >= 256 ? 1 : (512 + tiles - 1) / tiles;
-    want = want < (total + 3) / 4 ? want : (total + 3) / 4;
-    p.kb_split = (int)((total + want - 1) / want);
-    p.splits = (int)((total + p.kb_split - 1) / p.kb_split);
-    p.part_bytes = p.splits > 1 ? up256l((size_t)p.splits * (size_t)M * N * 4) : 0;
-    p.db_bytes = p.splits > 1 ? up256l((size_t)p.splits * N * 4) : 0;
-    return p;
 }
 
 // Lanes of a row (log2), columns of blocks and parts of the rows of lin_gate_kernel.
@@ -311,18 +176,69 @@ LinGate lin_gate(int64_t rows, int N, int size)
     g.cols = (vecs + (1 << g.lg) - 1) >> g.lg;
     const int64_t most = (1024 + g.cols - 1) / g.cols, each = 4 * (256 >> g.lg), want = (rows + each - 1) / each;
     g.parts = (int)(want < most ? want : most);
-    g.bytes = up256l((size_t)rows * N * size);
+    g.bytes = up256l((size_t)rows * up_vec(N, size) * size);
     g.db_bytes = up256l((size_t)g.parts * N * 4);
     return g;
+}
+
+// Tile and splits of a product by estimated time, in us: a block's pieces of the
+// reduction and what it does besides (first loads, results), in as many rounds as the
+// blocks that the chip holds at once leave, and the joining of splits (their bytes at
+// 4.5 TB/s, a launch).  Fitted to these, tiles of 64 x 64 / 128 x 128 / 256 x 128 / 256 x 256:
+//   bf16  32768 x 2048 x 2048 - / 352 / 307 / 264 us   32768 x 512 x 1024 81 / 54 / 49 / 52
+//         262144 x 128 x 512 223 / 166 / 144 / 135     8192 x 1024 x 1024 38 / 27 / 26 / 33
+//         262144 x 64 x 64 23 / 33 / - / -
+//         dW of 32768 x 512 x 1024 in two parts, 8 / 8 / 16 / 32 splits: - / 103 / 94 / 92
+//   fp32  4096 x 2048 x 2048 291 / 264 / 256 / 479     7429 x 333 x 1001 51 / 51 / 54 / 93
+// sums: with db, whose sums take the registers that the largest tiles would need.
+LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
+{
+    struct Tile {
+        int tm, tn, slots;
+        double alone;                    // a piece's time where a CU has a block for itself, of that with its full share
+        double piece[2], rest[2];        // bf16, fp32
+    };
+    static const Tile tiles[4] = {{64, 64, 1280, 0.4, {0.61, 1.05}, {5.5, 5.0}},
+                                  {128, 128, 512, 0.5, {0.64, 2.0}, {6.5, 12.0}},
+                                  {256, 128, 512, 0.5, {1.09, 3.9}, {10.5, 14.0}},
+                                  {256, 256, 256, 1.0, {0.85, 3.7}, {11.0, 25.0}}};
+    const int bk = LIN_PIECE / size, kb = (int)((K + bk - 1) / bk), f32 = size == 4;
+    const int64_t total = (int64_t)kb * passes;
+    LinPlan best{};
+    double least = 0.0;
+    for (const Tile& t : tiles) {
+        if (sums && t.tm == 256) break;
+        const int64_t tm = (M + t.tm - 1) / t.tm;
+        const int tn = (N + t.tn - 1) / t.tn;
+        for (int64_t want = 1; want <= 1024 && (want == 1 || total / want >= 4); want *= 2) {
+            const int64_t each = (total + want - 1) / want, splits = (total + each - 1) / each, units = tm * tn * splits;
+            const double full = (double)units / t.slots;
+            const double share = full >= 1.0 ? 1.0 : full > t.alone ? full : t.alone;
+            // (many small blocks: one begins as another ends)
+            const double rounds = full <= 1.0 ? 1.0 : t.tm == 64 ? full + 0.5 : (double)((units + t.slots - 1) / t.slots);
+            double us = rounds * (each * t.piece[f32] * share + t.rest[f32]);
+            if (splits > 1) us += 4.0 + (double)M * N * 8.0 * splits / 4.5e6;
+            if (!best.tm || us < least) {
+                least = us;
+                best = LinPlan{t.tm, t.tn, tm, tn, kb, (int)each, (int)splits, 0, 0};
+            }
+            if (full > 4.0) break;
+        }
+    }
+    if (best.splits > 1) {
+        best.part_bytes = up256l((size_t)best.splits * (size_t)M * N * 4);
+        best.db_bytes = up256l((size_t)best.splits * N * 4);
+    }
+    return best;
 }
 
 // The product over K of B (and then of B2, if there is one).  DB: q.db is formed
 // with it; else q.db_part already holds its parts, if q.db is not null.
 template <typename T, typename TO, bool AA, bool BA, int MODE, bool DB>
 hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int64_t lda, const T* B, const T* B2,
-                   int64_t ldb, bool aligned, void* ws, hipStream_t s)
+                   int64_t ldb, void* ws, hipStream_t s)
 {
-    const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, aligned);
+    const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB);
     q.A = A;
     q.B = B;
     q.B2 = B2;
@@ -341,37 +257,80 @@ hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int
         q.db_part = (float*)((char*)ws + p.part_bytes);
         q.db_parts = p.splits;
     }
-    const int64_t units = p.tiles_m * p.tiles_n * p.splits, most = 1 << 20;
-    const unsigned grid = (unsigned)(units < most ? units : most);
-    hipError_t e;
-    if (p.aligned) {
-        e = launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
-    } else {
-        if (p.tile == 128) lin_product_kernel<T, TO, AA, BA, 128, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
-        else lin_product_kernel<T, TO, AA, BA, 64, MODE, DB><<<grid, LIN_T, 0, s>>>(q);
-        e = hipGetLastError();
-    }
+    const hipError_t e = launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
     const bool join_db = q.db && (!DB || p.splits > 1);
     if (e != hipSuccess || (p.splits == 1 && !join_db)) return e;
-    const int64_t blocks = p.splits > 1 ? (M * ((N + 7) / 8) + 255) / 256 : 0;
+    const bool many = p.splits >= 16;
+    const int64_t vecs = p.splits > 1 ? M * ((N + 7) / 8) : 0, blocks = (vecs + (many ? 31 : 255)) / (many ? 32 : 256);
     const int main = (int)(blocks < 4096 ? blocks : 4096);
-    lin_join_kernel<T, TO, MODE><<<(unsigned)(main + (join_db ? (N + 15) / 16 : 0)), 256, 0, s>>>(q, main);
+    const unsigned grid = (unsigned)(main + (join_db ? (N + 15) / 16 : 0));
+    if (many) lin_join_kernel<T, TO, MODE, 8><<<grid, 256, 0, s>>>(q, main);
+    else lin_join_kernel<T, TO, MODE, 1><<<grid, 256, 0, s>>>(q, main);
     return hipGetLastError();
 }
+
+// Takes copies of matrices in turn from the workspace.
+template <typename T> struct LinCopies {
+    LinPack pack{};
+    int count = 0;
+    int64_t most = 0;
+    char* at;
+    // The matrix, or where its copy will be; cols becomes the distance of its rows.
+    const T* take(const T* m, int64_t rows, int cols)
+    {
+        const int ld = up_vec(cols, (int)sizeof(T));
+        if (ld == cols) return m;
+        const int64_t vecs = rows * (ld * (int)sizeof(T) / 16);
+        pack.from[count] = m;
+        pack.to[count] = at;
+        pack.vecs[count] = vecs;
+        pack.cols[count++] = cols;
+        most = vecs > most ? vecs : most;
+        T* to = (T*)at;
+        at += up256l((size_t)vecs * 16);
+        return to;
+    }
+    hipError_t run(hipStream_t s)
+    {
+        if (!count) return hipSuccess;
+        const int64_t blocks = (most + 255) / 256;
+        lin_pack_kernel<T><<<dim3((unsigned)(blocks < 8192 ? blocks : 8192), (unsigned)count), 256, 0, s>>>(pack);
+        return hipGetLastError();
+    }
+};
+size_t copy_bytes(int64_t rows, int cols, int size)
+{
+    const int ld = up_vec(cols, size);
+    return ld == cols ? 0 : up256l((size_t)rows * ld * size);
+}
+
+// Whether the forward of few rows is one launch of lin_few_fwd_kernel: its blocks
+// take a whole reduction each, which is too long where few columns leave few of them
+// (1 x 16384 x 128 bf16: 24 us, split and joined 9; 8 x 2048 x 256 fp32: 9 and 11).
+bool lin_few_fwd(int64_t rows, int in, int out, int size)
+{
+    return rows <= LIN_FEW && (out * size >= 32 * 64 || in <= 4096);
+}
+// And the backward: more than 8 rows of large matrices are products (16 x 4096 x 4096
+// bf16 52 us with these, 60 in one launch; 16 x 2048 x 2048 fp32 32 and 28).
+bool lin_few_bwd(int64_t rows, int in, int out) { return rows <= 8 || (rows <= LIN_FEW && (int64_t)in * out <= 1 << 22); }
+
+bool lin_gated(cf_act act, float slope) { return act == CF_ACT_SILU || slope != 1.f; }
 
 }  // namespace
 
 size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    const bool al = lin_aligned(in, out, size);
-    if (!bwd) return lin_plan(rows, out, in, size, 1, al).part_bytes;
+    if (bwd ? lin_few_bwd(rows, in, out) : lin_few_fwd(rows, in, out, size)) return 0;
+    const size_t copies = copy_bytes(rows, in, size) + copy_bytes(in, out, size);
+    if (!bwd) return copies + lin_plan(rows, out, in, size, 1, false).part_bytes;
     const LinGate g = lin_gate(rows, out, size);
-    const LinPlan x = lin_plan(rows, in, out, size, 1, al),
-                  w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, al), one = lin_plan(in, out, rows, size, 1, al);
-    const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes, plain = one.part_bytes + one.db_bytes;
-    const size_t most = gated + (w.part_bytes > x.part_bytes ? w.part_bytes : x.part_bytes);
-    return most > plain ? most : plain;
+    const LinPlan x = lin_plan(rows, in, out, size, 1, false),
+                  w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, false), one = lin_plan(in, out, rows, size, 1, true);
+    const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes + (w.part_bytes > x.part_bytes ? w.part_bytes : x.part_bytes);
+    const size_t both = one.part_bytes + one.db_bytes, plain = copy_bytes(rows, out, size) + (both > x.part_bytes ? both : x.part_bytes);
+    return copies + (gated > plain ? gated : plain);
 }
 
 template <typename T>
@@ -384,18 +343,43 @@ hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T*
     q.R = R;
     q.pre = pre;
     q.act = LinAct{(int)act, slope};
-    return lin_run<T, T, true, false, LIN_FWD, false>(q, rows, out, in, X, in, W, nullptr, out,
-                                                 lin_aligned(in, out, sizeof(T)), ws, s);
+    if (lin_few_fwd(rows, in, out, (int)sizeof(T))) {
+        q.A = X;
+        q.B = W;
+        q.M = rows;
+        q.N = out;
+        q.K = in;
+        return launch_lin_few_fwd(q, s);
+    }
+    LinCopies<T> copies;
+    copies.at = (char*)ws;
+    X = copies.take(X, rows, in);
+    W = copies.take(W, in, out);
+    const hipError_t e = copies.run(s);
+    if (e != hipSuccess) return e;
+    const int ldi = up_vec(in, sizeof(T)), ldo = up_vec(out, sizeof(T));
+    return R ? lin_run<T, T, true, false, LIN_FWD_RES, false>(q, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s)
+             : lin_run<T, T, true, false, LIN_FWD, false>(q, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
 }
 
 template <typename T>
 hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T* W, const T* pre, const T* dY,
                              cf_act act, float slope, T* dX, float* dW, float* db, void* ws, hipStream_t s)
 {
-    const bool gated = act == CF_ACT_SILU || slope != 1.f, al = lin_aligned(in, out, sizeof(T));
-    const T* D = dY;
+    const bool gated = lin_gated(act, slope);
+    const LinAct a = {(int)act, slope};
+    if (lin_few_bwd(rows, in, out))
+        return launch_lin_few_bwd((int)rows, in, out, X, W, pre, dY, a, gated, dX, dW, db, s);
+    const int ldi = up_vec(in, sizeof(T)), ldo = up_vec(out, sizeof(T));
+    LinCopies<T> copies;
+    copies.at = (char*)ws;
+    X = copies.take(X, rows, in);
+    if (dX) W = copies.take(W, in, out);
+    const T* D = gated ? nullptr : copies.take(dY, rows, out);
     const T* lo = nullptr;
-    char* at = (char*)ws;
+    hipError_t e = copies.run(s);
+    if (e != hipSuccess) return e;
+    char* at = copies.at;
     LinProduct<T> w{};
     w.C = dW;
     w.db = db;
@@ -408,9 +392,9 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
         w.db_part = (float*)at;
         w.db_parts = g.parts;
         at += g.db_bytes;
-        lin_gate_kernel<T><<<dim3((unsigned)g.parts, (unsigned)g.cols), 256, 0, s>>>(
-            pre, dY, hi, rest, rows, out, g.lg, LinAct{(int)act, slope}, db ? w.db_part : nullptr);
-        const hipError_t e = hipGetLastError();
+        lin_gate_kernel<T><<<dim3((unsigned)g.parts, (unsigned)g.cols), 256, 0, s>>>(pre, dY, hi, rest, rows, out, ldo, g.lg, a,
+                                                                                    db ? w.db_part : nullptr);
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
         D = hi;
         if (sizeof(T) == 2) lo = rest;
@@ -418,12 +402,11 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
     if (dX) {
         LinProduct<T> q{};
         q.C = dX;
-        const hipError_t e = lin_run<T, T, true, true, LIN_PLAIN, false>(q, rows, in, out, D, out, W, nullptr, out,
-                                                                              al, at, s);
+        e = lin_run<T, T, true, true, LIN_PLAIN, false>(q, rows, in, out, D, ldo, W, nullptr, ldo, at, s);
         if (e != hipSuccess) return e;
     }
-    if (gated) return lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, in, D, lo, out, al, at, s);
-    return lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, in, D, nullptr, out, al, at, s);
+    if (gated) return lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, ldi, D, lo, ldo, at, s);
+    return lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, ldi, D, nullptr, ldo, at, s);
 }
 
 template hipError_t launch_linear_fwd<float>(int64_t, int, int, const float*, const float*, const float*, cf_act, float,

@@ -27,7 +27,6 @@ namespace {
 
 constexpr int RN_T = 256;             // threads a block
 constexpr int RN_FWD_BLOCKS = 2048;   // blocks of a forward launch, 8 a CU
-constexpr int RN_BWD_BLOCKS = 1024;   // and of a backward one: each leaves C sums of five kinds
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
@@ -500,12 +499,20 @@ RnSplit rn_split(const cf_dims& x, int gate_n, int blocks)
     const int64_t vox = x.d * x.h * x.w;
     q.samples = gate_n > 1 ? gate_n : 1;
     q.rows = gate_n > 1 ? vox : x.n * vox;
-    const int64_t want = (blocks + q.samples - 1) / q.samples;
+    const int64_t want = blocks / q.samples > 1 ? blocks / q.samples : 1;
     const int64_t few = (q.rows + 3) / 4;          // at least four rows a part
     q.parts = (int)(want < few ? want : few);
     const int64_t items = (int64_t)q.samples * q.parts;
-    q.blocks = (int)(items < blocks + blocks / 2 ? items : blocks);
+    q.blocks = (int)(items < blocks ? items : blocks);
     return q;
+}
+
+// Blocks of a backward launch: as many as the chip holds at once, since each
+// leaves C sums of five kinds.
+int rn_bwd_blocks(cf_dtype dt, const cf_dims& x)
+{
+    const bool wide = dt == CF_F32 || x.c % 8, long_lane = (x.c > 512 && x.c <= 1024) || x.c > 2048;
+    return 256 * (long_lane ? (wide ? 1 : 2) : (wide ? 2 : 4));
 }
 
 size_t up256r(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -562,9 +569,9 @@ RnArgs rn_args(const cf_dims& x, const ResnormArgs& p)
 
 }  // namespace
 
-size_t resnorm_ws_bytes(const cf_dims& x, int gate_n)
+size_t resnorm_ws_bytes(cf_dtype dt, const cf_dims& x, int gate_n)
 {
-    const RnSplit q = rn_split(x, gate_n, RN_BWD_BLOCKS);
+    const RnSplit q = rn_split(x, gate_n, rn_bwd_blocks(dt, x));
     const size_t gates = gate_n ? (size_t)q.samples * q.parts * x.c * sizeof(float) : 0;
     return up256r((size_t)4 * q.blocks * x.c * sizeof(float)) + up256r(gates);
 }
@@ -584,7 +591,7 @@ template <typename T>
 hipError_t launch_resnorm_bwd(const cf_dims& x, const ResnormArgs& p, const void* F, const void* R, const void* dR,
                               const void* dY, void* dX, void* dF, const ResnormGrads& g, void* ws, hipStream_t s)
 {
-    const RnSplit q = rn_split(x, p.gate_n, RN_BWD_BLOCKS);
+    const RnSplit q = rn_split(x, p.gate_n, rn_bwd_blocks(sizeof(T) == 4 ? CF_F32 : CF_BF16, x));
     const RnArgs a = rn_args(x, p);
     float* vecs = (float*)ws;
     float* parts = (float*)((char*)ws + up256r((size_t)4 * q.blocks * x.c * sizeof(float)));

@@ -27,6 +27,7 @@ ACT = {"lrelu": cf.CF_ACT_LRELU, "silu": cf.CF_ACT_SILU}
 TINY = 1e-37
 
 SIZES = [
+    (1, 33, 17), (3, 4096, 5), (4, 515, 300), (7, 1000, 1001), (8, 64, 4096), (13, 333, 129), (16, 2048, 512), (16, 40, 9000),
     (1, 1, 1), (1, 2048, 2048), (1, 16384, 128), (2, 3, 5), (8, 2048, 256), (16, 64, 3), (17, 129, 33),
     (5, 1, 70), (70, 7, 1), (63, 64, 65), (64, 64, 64), (65, 63, 127), (128, 128, 128), (129, 130, 131),
     (200, 8, 1024), (1000, 333, 1001), (1001, 1000, 8), (2048, 72, 40), (4099, 96, 96), (33000, 16, 24),

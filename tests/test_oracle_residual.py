@@ -100,11 +100,11 @@ def test_linear_bwd_refuses(kw):
 def test_linear_workspaces():
     size = lambda *a: int(cf.lib().cf_linear_workspace_size(*a))  # noqa: E731
     assert size(cf.CF_F32, 0, 4, 4, 0) == 0 and size(5, 4, 4, 4, 0) == 0 and size(cf.CF_F32, 4, 4, 70000, 1) == 0
-    need = size(cf.CF_BF16, 8, 16384, 128, 0)          # few rows, a long reduction: split
+    need = size(cf.CF_BF16, 24, 16384, 128, 0)         # a long reduction: split
     assert need > 0
-    assert lin_fwd(rows=8, fin=16384, fout=128, wsb=need - 1) == cf.CF_ERR_WORKSPACE
-    assert lin_fwd(rows=8, fin=16384, fout=128, wsb=need, ws=None) == cf.CF_ERR_INVALID
-    assert lin_fwd(rows=8, fin=16384, fout=128, wsb=need, ws=0x7000008) == cf.CF_ERR_INVALID
+    assert lin_fwd(rows=24, fin=16384, fout=128, wsb=need - 1) == cf.CF_ERR_WORKSPACE
+    assert lin_fwd(rows=24, fin=16384, fout=128, wsb=need, ws=None) == cf.CF_ERR_INVALID
+    assert lin_fwd(rows=24, fin=16384, fout=128, wsb=need, ws=0x7000008) == cf.CF_ERR_INVALID
     need = size(cf.CF_BF16, 100, 64, 32, 1)
     assert need >= 2 * 2 * 100 * 32                    # the gated gradient in two parts
     assert lin_bwd(wsb=need - 1) == cf.CF_ERR_WORKSPACE
@@ -123,7 +123,7 @@ def test_linear_overlaps():
         refused(lin_fwd(pre=other))
     refused(lin_fwd(pre=0x6000000))
     # a reduction that is split: its workspace counts
-    refused(lin_fwd(rows=8, fin=16384, fout=128, R=None, ws=0x2000000 + (4 << 20) - 16, Y=0x9000000, wsb=1 << 30))
+    refused(lin_fwd(rows=24, fin=16384, fout=128, R=None, ws=0x2000000 + (4 << 20) - 16, Y=0x9000000, wsb=1 << 30))
     for other in (0x1000000, 0x2000000 + wb - 16, 0x3000000, 0x4000000 + yb - 16):
         for name in ("dX", "dW", "db", "ws"):
             refused(lin_bwd(**{name: other}))
