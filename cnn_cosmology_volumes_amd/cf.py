@@ -151,9 +151,9 @@ _SIG = {
     "cf_resnorm_fwd": ([ctypes.c_int, cf_dims, ctypes.POINTER(cf_resnorm_params), _P, _P, _P, _P, _P], ctypes.c_int),
     "cf_resnorm_bwd": ([ctypes.c_int, cf_dims, ctypes.POINTER(cf_resnorm_params)] + [_P] * 12 + [ctypes.c_size_t, _P],
                        ctypes.c_int),
-    "cf_grad_clip_workspace_size": ([ctypes.c_int, ctypes.c_int32, _PI64], ctypes.c_size_t),
-    "cf_grad_clip": ([ctypes.c_int, ctypes.c_int32, _PI64, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.c_float, _P, _P,
-                      ctypes.c_size_t, _P], ctypes.c_int),
+    "cf_grad_clip_workspace_size": ([ctypes.c_int, ctypes.c_int32, _P], ctypes.c_size_t),
+    "cf_grad_clip": ([ctypes.c_int, ctypes.c_int32, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+                     ctypes.c_int),
     "cf_net_param_count": ([ctypes.POINTER(cf_net_desc), ctypes.POINTER(ctypes.c_int64)], ctypes.c_int32),
     "cf_net_train_step_workspace_size": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32], ctypes.c_size_t),
     "cf_net_train_step": ([ctypes.POINTER(cf_net_desc), ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.POINTER(_P),
@@ -209,6 +209,7 @@ def _ptr(t):
 
 # (torch.cuda.current_stream builds a Stream object, which takes longer than a small kernel's launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None):
@@ -519,8 +520,9 @@ def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
     first = grads[0]
     dt, kind = dtype_code(first.dtype), first.dtype
     every = grads if out is None else [*grads, *out]
-    if not all([t.dtype is kind and t.is_contiguous() for t in every]) or (
-            out is not None and [t.shape for t in grads] != [t.shape for t in out]):
+    sizes = [t.numel() for t in every]
+    if {t.dtype for t in every} != {kind} or not all(map(torch.Tensor.is_contiguous, every)) or (
+            out is not None and sizes[:k] != sizes[k:]):
         for i, t in enumerate(grads):
             _packed("gradient %d" % i, t, kind)
             if out is not None:
@@ -529,13 +531,13 @@ def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
         _packed("stats", stats, torch.float32, (2,))
     at = first.get_device()
     s = _on_gpu(ws, first, stats, *[t for t in every if t.get_device() != at][:1])
-    n = (ctypes.c_int64 * k).from_buffer(array.array("q", [t.numel() for t in grads]))
-    pointers = lambda ts: (_P * k).from_buffer(array.array("Q", [t.data_ptr() for t in ts]))
+    counts, pointers = array.array("q", sizes), array.array("Q", map(torch.Tensor.data_ptr, every))
+    n, p = counts.buffer_info()[0], pointers.buffer_info()[0]
     stats = first.new_empty(2, dtype=torch.float32) if stats is None else stats
     L = lib()
     ws = _ws(L.cf_grad_clip_workspace_size(dt, k, n), first.device, ws)
-    check(L.cf_grad_clip(dt, k, n, pointers(grads), None if out is None else pointers(out), float(max_norm),
-                         _ptr(stats), _ptr(ws), _wsbytes(ws), s))
+    check(L.cf_grad_clip(dt, k, n, p, None if out is None else p + 8 * k, float(max_norm), _ptr(stats), _ptr(ws),
+                         _wsbytes(ws), s))
     return stats
 
 
@@ -658,8 +660,8 @@ def _on_gpu(ws, first, *others):
             raise ValueError("ws must be on the tensors' GPU: %s and %s" % (ws.device, first.device))
     if at < 0:
         raise ValueError("tensors must be on a GPU")
-    if torch.cuda.current_device() != at:
-        raise ValueError("tensors and stream must be on the current GPU: %d and %d" % (at, torch.cuda.current_device()))
+    if _current_device() != at:
+        raise ValueError("tensors and stream must be on the current GPU: %d and %d" % (at, _current_device()))
     return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(at)
 
 
@@ -743,10 +745,11 @@ def cf_linear_workspace_size(dtype, rows, fin, fout, backward):
 
 def _linear_sizes(X, W):
     """(rows, in, out) of X [..., in] and W [in, out]."""
-    _packed("X", X)
     if W.dim() != 2 or X.dim() < 1 or X.shape[-1] != W.shape[0]:
         raise ValueError("X must be [..., in] and W [in, out], not %s and %s" % (tuple(X.shape), tuple(W.shape)))
-    _packed("W", W, X.dtype)
+    if W.dtype != X.dtype or not (X.is_contiguous() and W.is_contiguous()):
+        _packed("X", X)
+        _packed("W", W, X.dtype)
     fin, fout = W.shape
     return X.numel() // max(1, fin), fin, fout
 
@@ -765,9 +768,12 @@ def cf_linear_fwd(X, W, bias=None, act=CF_ACT_LRELU, slope=1.0, R=None, need_pre
     shape = X.shape[:-1] + (fout,)
     if bias is not None:
         _packed("bias", bias, torch.float32, (fout,))
-    for name, t in (("R", R), ("pre", pre), ("Y", Y)):
-        if t is not None:
-            _packed(name, t, X.dtype, shape)
+    if R is not None:
+        _packed("R", R, X.dtype, shape)
+    if pre is not None:
+        _packed("pre", pre, X.dtype, shape)
+    if Y is not None:
+        _packed("Y", Y, X.dtype, shape)
     s = _on_gpu(ws, X, W, bias, R, pre, Y)
     Y = X.new_empty(shape) if Y is None else Y
     pre = X.new_empty(shape) if pre is None and need_pre else pre
@@ -815,15 +821,19 @@ def cf_resnorm_workspace_size(dtype, xshape, gate_n):
 
 
 def _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha):
-    for name, t in (("gpre", gpre), ("bpre", bpre), ("gpost", gpost), ("bpost", bpost)):
-        if t is not None:
-            _packed(name, t, torch.float32, (d.c,))
+    if gpre is not None:
+        _packed("gpre", gpre, torch.float32, (d.c,))
+    if bpre is not None:
+        _packed("bpre", bpre, torch.float32, (d.c,))
+    if gpost is not None:
+        _packed("gpost", gpost, torch.float32, (d.c,))
+    if bpost is not None:
+        _packed("bpost", bpost, torch.float32, (d.c,))
     gate_n = 0
     if gate is not None:
         gate_n = gate.shape[0] if gate.dim() == 2 else 1
         _packed("gate", gate, torch.float32, (gate_n, d.c) if gate.dim() == 2 else (d.c,))
-    return cf_resnorm_params(int(kind), float(eps), float(alpha), _ptr(gpre), _ptr(bpre), _ptr(gpost), _ptr(bpost),
-                             _ptr(gate), gate_n)
+    return cf_resnorm_params(kind, eps, alpha, _ptr(gpre), _ptr(bpre), _ptr(gpost), _ptr(bpost), _ptr(gate), gate_n)
 
 
 def cf_resnorm_fwd(X, F, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None, gate=None, alpha=1.0, need_y=True,
@@ -838,9 +848,10 @@ def cf_resnorm_fwd(X, F, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None
     dt, d = dtype_code(X.dtype), cf_dims(*X.shape)
     _packed("X", X)
     _packed("F", F, X.dtype, X.shape)
-    for name, t in (("R", R), ("Y", Y)):
-        if t is not None:
-            _packed(name, t, X.dtype, X.shape)
+    if R is not None:
+        _packed("R", R, X.dtype, X.shape)
+    if Y is not None:
+        _packed("Y", Y, X.dtype, X.shape)
     p = _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha)
     s = _on_gpu(None, X, F, gpre, bpre, gpost, bpost, gate, R, Y)
     R = torch.empty_like(X) if R is None else R

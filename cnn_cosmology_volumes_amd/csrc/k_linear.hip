@@ -13,6 +13,12 @@
 namespace cf {
 namespace {
 
+// a / b, b below 2^31: 64-bit division is some hundred instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b)
+{
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 size_t up256l(size_t b) { return (b + 255) & ~(size_t)255; }
 int up_vec(int n, int size) { return (n + 16 / size - 1) / (16 / size) * (16 / size); }
 
@@ -45,7 +51,7 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main
     const int vecs = (q.N + 7) / 8, mine = (int)threadIdx.x % VECS, group = (int)threadIdx.x / VECS;
     const int64_t total = q.M * vecs;
     for (int64_t i0 = (int64_t)blockIdx.x * VECS; i0 < total; i0 += (int64_t)main * VECS) {
-        const int64_t i = i0 + mine, m = i / vecs;
+        const int64_t i = i0 + mine, m = quotient(i, vecs);
         const int n = (int)(i - m * vecs) * 8;
         float v[8] = {};
         if (i < total) {
@@ -110,7 +116,7 @@ template <typename T> __global__ __launch_bounds__(256) void lin_pack_kernel(Lin
     const int job = (int)blockIdx.y, cols = q.cols[job], each = (cols + V - 1) / V;
     const T* from = (const T*)q.from[job];
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < q.vecs[job]; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / each;
+        const int64_t r = quotient(i, each);
         const int c = (int)(i - r * each) * V;
         const uint4 v = lin_chunk<T>(from + r * cols + c, cols - c, cols >= V);
         __builtin_memcpy((T*)q.to[job] + i * V, &v, 16);
@@ -174,7 +180,7 @@ LinGate lin_gate(int64_t rows, int N, int size)
     g.lg = 0;
     while (g.lg < 8 && 1 << g.lg < vecs) ++g.lg;
     g.cols = (vecs + (1 << g.lg) - 1) >> g.lg;
-    const int64_t most = (1024 + g.cols - 1) / g.cols, each = 4 * (256 >> g.lg), want = (rows + each - 1) / each;
+    const int64_t most = (1024 + g.cols - 1) / g.cols, each = 256 >> g.lg, want = (rows + each - 1) / each;
     g.parts = (int)(want < most ? want : most);
     g.bytes = up256l((size_t)rows * up_vec(N, size) * size);
     g.db_bytes = up256l((size_t)g.parts * N * 4);
