@@ -11,6 +11,10 @@
 // are reproducible bit for bit.  The second launch takes the chunks from the
 // last to the first: what the first read last may still lie in the last-level
 // cache.
+//
+// What bounds it: memory.  75.4 M fp32 values in 192 tensors take 181 us, which is
+// their 302 MB read twice and written once at 5 TB/s; 5.0 M values in 11 tensors
+// take 15.5 us in the two kernels and 17.6 with the call, which is then the host's.
 #include "cf_internal.h"
 
 #include <math.h>

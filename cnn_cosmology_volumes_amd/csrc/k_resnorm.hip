@@ -20,6 +20,13 @@
 // A block takes a range of one sample's rows; the column sums of the blocks are
 // added by a second launch, in a fixed order and in fp64: results are
 // reproducible bit for bit.
+//
+// What bounds it: memory.  Forward, 8 x 64^3 x 64 bf16: 1.07 GB in 221 us (4.9 TB/s).
+// Backward, 8 x 32^3 x 256 bf16: 805 MB in 175 us (4.6 TB/s) and 6 us for the join.
+// There a lane has some 350 instructions a row, so that arithmetic alone is half of
+// the time: the next row's loads are under way during it (239 us without), and sums
+// between lanes are one instruction a step (shuffles go through LDS).
+// 3 x 37 x 29 x 31 x 60 fp32: 33 us (4.3 TB/s) and 4.
 #include "cf_internal.h"
 
 namespace cf {

@@ -245,3 +245,11 @@ def test_past_2_31_elements():
         s = torch.sigmoid(p)
         total += (d * s * (1 + p * (1 - s))).sum(0)
     assert float((db.double() - total).abs().max() / total.abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,fin,fout", [(16700, 264, 776), (33001, 136, 520), (16640, 512, 256), (9000, 1000, 1001)])
+def test_large_tiles(rows, fin, fout, dtype):
+    """Sizes that take the largest tiles, whole ones and ones that the result cuts."""
+    both(rows, fin, fout, dtype, "silu", 0.0)
+    both(rows, fin, fout, dtype, "lrelu", 1.0, bias=False, residual=False, seed=1)
