@@ -26,16 +26,16 @@ int up_vec(int n, int size) { return (n + 16 / size - 1) / (16 / size) * (16 / s
 // block and 16 threads to a column.  32 vectors of eight columns a block, and GROUPS
 // threads to each, which take every GROUPS-th split: the few results of a long
 // reduction are bound by the latency of a thread's loads.
+union LinJoinShared {
+    double col[16][17];
+    float part[256][8];
+};
 template <typename T, typename TO, int MODE, int GROUPS>
-__global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main)
+__device__ __forceinline__ void lin_join(const LinProduct<T>& q, int block, int main, LinJoinShared& sh)
 {
     constexpr int VECS = 256 / GROUPS;
-    __shared__ union {
-        double col[16][17];
-        float part[GROUPS][VECS][8];
-    } sh;
-    if ((int)blockIdx.x >= main) {
-        const int c = ((int)blockIdx.x - main) * 16 + (int)threadIdx.x % 16, k = (int)threadIdx.x / 16;
+    if (block >= main) {
+        const int c = (block - main) * 16 + (int)threadIdx.x % 16, k = (int)threadIdx.x / 16;
         double sum = 0.0;
         if (c < q.N)
 #pragma unroll 4
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main
     }
     const int vecs = (q.N + 7) / 8, mine = (int)threadIdx.x % VECS, group = (int)threadIdx.x / VECS;
     const int64_t total = q.M * vecs;
-    for (int64_t i0 = (int64_t)blockIdx.x * VECS; i0 < total; i0 += (int64_t)main * VECS) {
+    for (int64_t i0 = (int64_t)block * VECS; i0 < total; i0 += (int64_t)main * VECS) {
         const int64_t i = i0 + mine, m = quotient(i, vecs);
         const int n = (int)(i - m * vecs) * 8;
         float v[8] = {};
@@ -80,13 +80,13 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main
         }
         if (GROUPS > 1) {
             __syncthreads();
-            __builtin_memcpy(sh.part[group][mine], v, 32);
+            __builtin_memcpy(sh.part[group * VECS + mine], v, 32);
             __syncthreads();
             if (group) continue;
 #pragma unroll
             for (int g = 1; g < GROUPS; ++g)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += sh.part[g][mine][j];
+                for (int j = 0; j < 8; ++j) v[j] += sh.part[g * VECS + mine][j];
         }
         if (i >= total) continue;
         float bias[8] = {};
@@ -100,6 +100,21 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main
     }
 }
 
+template <typename T, typename TO, int MODE, int GROUPS>
+__global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main)
+{
+    __shared__ LinJoinShared sh;
+    lin_join<T, TO, MODE, GROUPS>(q, (int)blockIdx.x, main, sh);
+}
+// Those of dX in the first blocks, and of dW and db: a launch less.
+template <typename T, int GX, int GW>
+__global__ __launch_bounds__(256) void lin_join_bwd_kernel(LinProduct<T> x, int main_x, LinProduct<T> w, int main_w)
+{
+    __shared__ LinJoinShared sh;
+    if ((int)blockIdx.x < main_x) lin_join<T, T, LIN_PLAIN, GX>(x, (int)blockIdx.x, main_x, sh);
+    else lin_join<T, float, LIN_PLAIN, GW>(w, (int)blockIdx.x - main_x, main_w, sh);
+}
+
 // Copies of matrices whose rows are not whole vectors, with rows that are: the
 // products' loads take 16 bytes at multiples of 16.  (Reading such rows as they are,
 // value by value at their ends and through registers, took 7429 x 333 x 1001 82 us
@@ -109,13 +124,16 @@ struct LinPack {
     void* to[3];
     int64_t vecs[3];        // of a copy
     int cols[3];
+    int blocks[3];
 };
-template <typename T> __global__ __launch_bounds__(256) void lin_pack_kernel(LinPack q)
+template <typename T> __device__ __forceinline__ void lin_pack(const LinPack& q, int block)
 {
     constexpr int V = LinTile<T>::V;
-    const int job = (int)blockIdx.y, cols = q.cols[job], each = (cols + V - 1) / V;
+    int job = 0;
+    while (block >= q.blocks[job]) block -= q.blocks[job++];
+    const int cols = q.cols[job], each = (cols + V - 1) / V;
     const T* from = (const T*)q.from[job];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < q.vecs[job]; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < q.vecs[job]; i += (int64_t)q.blocks[job] * 256) {
         const int64_t r = quotient(i, each);
         const int c = (int)(i - r * each) * V;
         const uint4 v = lin_chunk<T>(from + r * cols + c, cols - c, cols >= V);
@@ -125,50 +143,66 @@ template <typename T> __global__ __launch_bounds__(256) void lin_pack_kernel(Lin
 
 // D = dY act'(pre) with rows of `ld` values: fp32, or as bf16 hi and lo = D - hi,
 // which together keep 16 bits or more: dW is fp32 and would show the rounding of hi
-// alone (2^-9 of every term).  dX, rounded to bf16 itself, takes hi alone.
+// alone (2^-9 of every term).  dX, rounded to bf16 itself, takes hi alone; a slope
+// of 0 or a power of two leaves no lo (null).
 // A block takes a range of rows, 2^lg lanes to a row, and leaves the column sums of D.
-template <typename T>
-__global__ __launch_bounds__(256) void lin_gate_kernel(const T* __restrict__ pre, const T* __restrict__ dY, T* hi, T* lo,
-                                                       int64_t rows, int N, int ld, int lg, LinAct act, float* db_part)
+template <typename T> struct LinGated {
+    const T *pre, *dY;
+    T *hi, *lo;
+    int64_t rows;
+    int N, ld, lg, parts, blocks;
+    LinAct act;
+    float* db_part;
+};
+template <typename T> __device__ __forceinline__ void lin_gate_rows(const LinGated<T>& q, int block)
 {
     constexpr int V = LinTile<T>::V;
     __shared__ float sh[256 * V];
-    const int lane = (int)threadIdx.x & ((1 << lg) - 1), c = (((int)blockIdx.y << lg) + lane) * V;
-    const int64_t r0 = rows * blockIdx.x / gridDim.x, r1 = rows * (blockIdx.x + 1) / gridDim.x;
+    const int part = block % q.parts, column = block / q.parts;
+    const int lane = (int)threadIdx.x & ((1 << q.lg) - 1), c = ((column << q.lg) + lane) * V;
+    const int64_t r0 = q.rows * part / q.parts, r1 = q.rows * (part + 1) / q.parts;
     float sum[V] = {};
-    if (c < N)
-        for (int64_t r = r0 + ((int)threadIdx.x >> lg); r < r1; r += 256 >> lg) {
-            const uint4 zv = lin_chunk<T>(pre + r * N + c, N - c, N >= V), dv = lin_chunk<T>(dY + r * N + c, N - c, N >= V);
+    if (c < q.N)
+        for (int64_t r = r0 + ((int)threadIdx.x >> q.lg); r < r1; r += 256 >> q.lg) {
+            const uint4 zv = lin_chunk<T>(q.pre + r * q.N + c, q.N - c, q.N >= V);
+            const uint4 dv = lin_chunk<T>(q.dY + r * q.N + c, q.N - c, q.N >= V);
             T z[V], d[V], h[V], l[V];
             __builtin_memcpy(z, &zv, 16);
             __builtin_memcpy(d, &dv, 16);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float v = widen(d[j]) * lin_dact(act, widen(z[j]));
+                const float v = widen(d[j]) * lin_dact(q.act, widen(z[j]));
                 sum[j] += v;
                 Elem<T>::store(h, j, v);
                 // (an infinite hi stands for itself: inf - inf would make NaN of it)
                 const float rest = v - widen(h[j]);
                 if (sizeof(T) == 2) Elem<T>::store(l, j, __builtin_isfinite(widen(h[j])) ? rest : 0.f);
             }
-            __builtin_memcpy(hi + r * ld + c, h, 16);
-            if (sizeof(T) == 2) __builtin_memcpy(lo + r * ld + c, l, 16);
+            __builtin_memcpy(q.hi + r * q.ld + c, h, 16);
+            if (sizeof(T) == 2 && q.lo) __builtin_memcpy(q.lo + r * q.ld + c, l, 16);
         }
-    if (!db_part) return;
+    if (!q.db_part) return;
 #pragma unroll
     for (int j = 0; j < V; ++j) sh[j * 256 + (int)threadIdx.x] = sum[j];
     __syncthreads();
     // sum j of the lanes of one column lies at j 256 + lane, 2^lg apart
-    for (int i = (int)threadIdx.x; i < V << lg; i += 256) {
-        const int j = i >> lg, k = i & ((1 << lg) - 1), col = (((int)blockIdx.y << lg) + k) * V + j;
-        if (col >= N) continue;
+    for (int i = (int)threadIdx.x; i < V << q.lg; i += 256) {
+        const int j = i >> q.lg, k = i & ((1 << q.lg) - 1), col = ((column << q.lg) + k) * V + j;
+        if (col >= q.N) continue;
         float v = 0.f;
-        for (int g = 0; g < 256 >> lg; ++g) v += sh[j * 256 + (g << lg) + k];
-        db_part[(int64_t)blockIdx.x * N + col] = v;
+        for (int g = 0; g < 256 >> q.lg; ++g) v += sh[j * 256 + (g << q.lg) + k];
+        q.db_part[(int64_t)part * q.N + col] = v;
     }
 }
 
-// Lanes of a row (log2), columns of blocks and parts of the rows of lin_gate_kernel.
+// What a product needs beforehand: D, if there is an activation, and the copies.
+template <typename T> __global__ __launch_bounds__(256) void lin_before_kernel(LinGated<T> g, LinPack p)
+{
+    if ((int)blockIdx.x < g.blocks) lin_gate_rows<T>(g, (int)blockIdx.x);
+    else lin_pack<T>(p, (int)blockIdx.x - g.blocks);
+}
+
+// Lanes of a row (log2), columns of blocks and parts of the rows of lin_gate_rows.
 struct LinGate {
     int lg, cols, parts;
     size_t bytes, db_bytes;      // of hi or lo, of the column sums
@@ -238,13 +272,23 @@ LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
     return best;
 }
 
-// The product over K of B (and then of B2, if there is one).  DB: q.db is formed
-// with it; else q.db_part already holds its parts, if q.db is not null.
+// A product whose sums, or whose db, are still to be joined: blocks of the join, whose
+// GROUPS is 8 if `many`.
+template <typename T> struct LinJoin {
+    LinProduct<T> q{};
+    int main = 0, all = 0;
+    bool many = false;
+};
+
+// The product over K of B (and then of B2, if there is one), and what is to be joined
+// after it.  DB: q.db is formed with it; else q.db_part already holds its parts, if
+// q.db is not null.
 template <typename T, typename TO, bool AA, bool BA, int MODE, bool DB>
-hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int64_t lda, const T* B, const T* B2,
+hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, int64_t lda, const T* B, const T* B2,
                    int64_t ldb, void* ws, hipStream_t s)
 {
     const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB);
+    LinProduct<T>& q = join.q;
     q.A = A;
     q.B = B;
     q.B2 = B2;
@@ -263,44 +307,56 @@ hipError_t lin_run(LinProduct<T> q, int64_t M, int N, int64_t K, const T* A, int
         q.db_part = (float*)((char*)ws + p.part_bytes);
         q.db_parts = p.splits;
     }
-    const hipError_t e = launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
-    const bool join_db = q.db && (!DB || p.splits > 1);
-    if (e != hipSuccess || (p.splits == 1 && !join_db)) return e;
-    const bool many = p.splits >= 16;
-    const int64_t vecs = p.splits > 1 ? M * ((N + 7) / 8) : 0, blocks = (vecs + (many ? 31 : 255)) / (many ? 32 : 256);
-    const int main = (int)(blocks < 4096 ? blocks : 4096);
-    const unsigned grid = (unsigned)(main + (join_db ? (N + 15) / 16 : 0));
-    if (many) lin_join_kernel<T, TO, MODE, 8><<<grid, 256, 0, s>>>(q, main);
-    else lin_join_kernel<T, TO, MODE, 1><<<grid, 256, 0, s>>>(q, main);
+    join.many = p.splits >= 16;
+    const int64_t vecs = p.splits > 1 ? M * ((N + 7) / 8) : 0, blocks = (vecs + (join.many ? 31 : 255)) / (join.many ? 32 : 256);
+    join.main = (int)(blocks < 4096 ? blocks : 4096);
+    join.all = join.main + (q.db && (!DB || p.splits > 1) ? (N + 15) / 16 : 0);
+    return launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
+}
+
+template <typename T, typename TO, int MODE> hipError_t run_join(const LinJoin<T>& j, hipStream_t s)
+{
+    if (!j.all) return hipSuccess;
+    if (j.many) lin_join_kernel<T, TO, MODE, 8><<<(unsigned)j.all, 256, 0, s>>>(j.q, j.main);
+    else lin_join_kernel<T, TO, MODE, 1><<<(unsigned)j.all, 256, 0, s>>>(j.q, j.main);
+    return hipGetLastError();
+}
+template <typename T> hipError_t run_join_bwd(const LinJoin<T>& x, const LinJoin<T>& w, hipStream_t s)
+{
+    if (!x.all) return run_join<T, float, LIN_PLAIN>(w, s);
+    if (!w.all) return run_join<T, T, LIN_PLAIN>(x, s);
+    const unsigned grid = (unsigned)(x.all + w.all);
+    if (x.many && w.many) lin_join_bwd_kernel<T, 8, 8><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
+    else if (x.many) lin_join_bwd_kernel<T, 8, 1><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
+    else if (w.many) lin_join_bwd_kernel<T, 1, 8><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
+    else lin_join_bwd_kernel<T, 1, 1><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
     return hipGetLastError();
 }
 
 // Takes copies of matrices in turn from the workspace.
 template <typename T> struct LinCopies {
     LinPack pack{};
-    int count = 0;
-    int64_t most = 0;
+    int count = 0, blocks = 0;
     char* at;
-    // The matrix, or where its copy will be; cols becomes the distance of its rows.
+    // The matrix, or where its copy will be.
     const T* take(const T* m, int64_t rows, int cols)
     {
         const int ld = up_vec(cols, (int)sizeof(T));
         if (ld == cols) return m;
-        const int64_t vecs = rows * (ld * (int)sizeof(T) / 16);
+        const int64_t vecs = rows * (ld * (int)sizeof(T) / 16), want = (vecs + 255) / 256;
         pack.from[count] = m;
         pack.to[count] = at;
         pack.vecs[count] = vecs;
-        pack.cols[count++] = cols;
-        most = vecs > most ? vecs : most;
+        pack.cols[count] = cols;
+        blocks += pack.blocks[count++] = (int)(want < 8192 ? want : 8192);
         T* to = (T*)at;
         at += up256l((size_t)vecs * 16);
         return to;
     }
-    hipError_t run(hipStream_t s)
+    hipError_t run(const LinGated<T>& g, hipStream_t s)
     {
-        if (!count) return hipSuccess;
-        const int64_t blocks = (most + 255) / 256;
-        lin_pack_kernel<T><<<dim3((unsigned)(blocks < 8192 ? blocks : 8192), (unsigned)count), 256, 0, s>>>(pack);
+        if (!g.blocks && !blocks) return hipSuccess;
+        lin_before_kernel<T><<<(unsigned)(g.blocks + blocks), 256, 0, s>>>(g, pack);
         return hipGetLastError();
     }
 };
@@ -334,16 +390,19 @@ size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
     const LinGate g = lin_gate(rows, out, size);
     const LinPlan x = lin_plan(rows, in, out, size, 1, false),
                   w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, false), one = lin_plan(in, out, rows, size, 1, true);
-    const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes + (w.part_bytes > x.part_bytes ? w.part_bytes : x.part_bytes);
-    const size_t both = one.part_bytes + one.db_bytes, plain = copy_bytes(rows, out, size) + (both > x.part_bytes ? both : x.part_bytes);
-    return copies + (gated > plain ? gated : plain);
+    const LinPlan exact = lin_plan(in, out, rows, size, 1, false);
+    const size_t parts = w.part_bytes > exact.part_bytes ? w.part_bytes : exact.part_bytes;
+    const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes + parts;
+    const size_t plain = copy_bytes(rows, out, size) + one.part_bytes + one.db_bytes;
+    return copies + x.part_bytes + (gated > plain ? gated : plain);
 }
 
 template <typename T>
 hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T* W, const float* bias, cf_act act,
                              float slope, const T* R, T* pre, T* Y, void* ws, hipStream_t s)
 {
-    LinProduct<T> q{};
+    LinJoin<T> y;
+    LinProduct<T>& q = y.q;
     q.C = Y;
     q.bias = bias;
     q.R = R;
@@ -361,11 +420,15 @@ hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T*
     copies.at = (char*)ws;
     X = copies.take(X, rows, in);
     W = copies.take(W, in, out);
-    const hipError_t e = copies.run(s);
+    hipError_t e = copies.run(LinGated<T>{}, s);
     if (e != hipSuccess) return e;
     const int ldi = up_vec(in, sizeof(T)), ldo = up_vec(out, sizeof(T));
-    return R ? lin_run<T, T, true, false, LIN_FWD_RES, false>(q, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s)
-             : lin_run<T, T, true, false, LIN_FWD, false>(q, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
+    if (R) {
+        e = lin_run<T, T, true, false, LIN_FWD_RES, false>(y, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
+        return e != hipSuccess ? e : run_join<T, T, LIN_FWD_RES>(y, s);
+    }
+    e = lin_run<T, T, true, false, LIN_FWD, false>(y, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
+    return e != hipSuccess ? e : run_join<T, T, LIN_FWD>(y, s);
 }
 
 template <typename T>
@@ -383,36 +446,41 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
     if (dX) W = copies.take(W, in, out);
     const T* D = gated ? nullptr : copies.take(dY, rows, out);
     const T* lo = nullptr;
-    hipError_t e = copies.run(s);
-    if (e != hipSuccess) return e;
     char* at = copies.at;
-    LinProduct<T> w{};
-    w.C = dW;
-    w.db = db;
+    LinJoin<T> x, w;
+    x.q.C = dX;
+    w.q.C = dW;
+    w.q.db = db;
+    LinGated<T> gate{};
     if (gated) {
+        // (dY times 0 or a power of two is a bf16 value itself)
+        int exponent;
+        const bool exact = act == CF_ACT_LRELU && (slope == 0.f || frexpf(slope, &exponent) == 0.5f);
         const LinGate g = lin_gate(rows, out, (int)sizeof(T));
         T* hi = (T*)at;
         at += g.bytes;
-        T* rest = (T*)at;
-        if (sizeof(T) == 2) at += g.bytes;
-        w.db_part = (float*)at;
-        w.db_parts = g.parts;
+        T* rest = nullptr;
+        if (sizeof(T) == 2 && !exact) {
+            rest = (T*)at;
+            at += g.bytes;
+        }
+        w.q.db_part = (float*)at;
+        w.q.db_parts = g.parts;
         at += g.db_bytes;
-        lin_gate_kernel<T><<<dim3((unsigned)g.parts, (unsigned)g.cols), 256, 0, s>>>(pre, dY, hi, rest, rows, out, ldo, g.lg, a,
-                                                                                    db ? w.db_part : nullptr);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        gate = LinGated<T>{pre, dY, hi, rest, rows, out, ldo, g.lg, g.parts, g.parts * g.cols, a, db ? w.q.db_part : nullptr};
         D = hi;
-        if (sizeof(T) == 2) lo = rest;
+        lo = rest;
     }
+    hipError_t e = copies.run(gate, s);
+    if (e != hipSuccess) return e;
     if (dX) {
-        LinProduct<T> q{};
-        q.C = dX;
-        e = lin_run<T, T, true, true, LIN_PLAIN, false>(q, rows, in, out, D, ldo, W, nullptr, ldo, at, s);
+        e = lin_run<T, T, true, true, LIN_PLAIN, false>(x, rows, in, out, D, ldo, W, nullptr, ldo, at, s);
         if (e != hipSuccess) return e;
+        if (x.q.splits > 1) at += up256l((size_t)x.q.splits * (size_t)rows * in * 4);
     }
-    if (gated) return lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, ldi, D, lo, ldo, at, s);
-    return lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, ldi, D, nullptr, ldo, at, s);
+    e = gated ? lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, ldi, D, lo, ldo, at, s)
+              : lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, ldi, D, nullptr, ldo, at, s);
+    return e != hipSuccess ? e : run_join_bwd(x, w, s);
 }
 
 template hipError_t launch_linear_fwd<float>(int64_t, int, int, const float*, const float*, const float*, cf_act, float,
