@@ -23,23 +23,33 @@ size_t up256l(size_t b) { return (b + 255) & ~(size_t)255; }
 int up_vec(int n, int size) { return (n + 16 / size - 1) / (16 / size) * (16 / size); }
 
 // Adds the splits' sums, and in the blocks past `main` those of db, 16 columns a
-// block and 16 threads to a column.  32 vectors of eight columns a block, and GROUPS
-// threads to each, which take every GROUPS-th split: the few results of a long
-// reduction are bound by the latency of a thread's loads.
+// block and 16 threads to a column.  Results are taken as vectors of eight columns,
+// 2^lg threads to each, which take every 2^lg-th split: the few results of a long
+// reduction are bound by the latency of a thread's loads, so several of them are
+// under way.
+// (dW and db of 380581 x 2 x 1 bf16, 992 splits: 54 us with eight threads and a load
+// at a time.)
 union LinJoinShared {
     double col[16][17];
     float part[256][8];
 };
-template <typename T, typename TO, int MODE, int GROUPS>
-__device__ __forceinline__ void lin_join(const LinProduct<T>& q, int block, int main, LinJoinShared& sh)
+template <typename T, typename TO, int MODE>
+__device__ __forceinline__ void lin_join(const LinProduct<T>& q, int block, int main, int lg, LinJoinShared& sh)
 {
-    constexpr int VECS = 256 / GROUPS;
     if (block >= main) {
         const int c = (block - main) * 16 + (int)threadIdx.x % 16, k = (int)threadIdx.x / 16;
         double sum = 0.0;
         if (c < q.N)
-#pragma unroll 4
-            for (int i = k; i < q.db_parts; i += 16) sum += (double)q.db_part[(int64_t)i * q.N + c];
+            for (int i = k; i < q.db_parts; i += 256) {
+                float t[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const int at = i + u * 16 < q.db_parts ? i + u * 16 : q.db_parts - 1;
+                    t[u] = q.db_part[(int64_t)at * q.N + c];
+                }
+#pragma unroll
+                for (int u = 0; u < 16; ++u) sum += i + u * 16 < q.db_parts ? (double)t[u] : 0.0;
+            }
         sh.col[k][threadIdx.x % 16] = sum;
         __syncthreads();
         if (k == 0 && c < q.N) {
@@ -48,45 +58,43 @@ __device__ __forceinline__ void lin_join(const LinProduct<T>& q, int block, int 
         }
         return;
     }
-    const int vecs = (q.N + 7) / 8, mine = (int)threadIdx.x % VECS, group = (int)threadIdx.x / VECS;
+    const int groups = 1 << lg, each = 256 >> lg;
+    const int vecs = (q.N + 7) / 8, mine = (int)threadIdx.x & (each - 1), group = (int)threadIdx.x >> (8 - lg);
     const int64_t total = q.M * vecs;
-    for (int64_t i0 = (int64_t)block * VECS; i0 < total; i0 += (int64_t)main * VECS) {
+    for (int64_t i0 = (int64_t)block * each; i0 < total; i0 += (int64_t)main * each) {
         const int64_t i = i0 + mine, m = quotient(i, vecs);
         const int n = (int)(i - m * vecs) * 8;
         float v[8] = {};
         if (i < total) {
-            const float* p = q.part + (group * q.M + m) * q.N + n;
-            const int64_t step = GROUPS * q.M * q.N;
-            auto add = [&](const Lin8<float>& t) {
-                float u[8];
-                t.get(u);
+            const float* p = q.part + m * q.N + n;
+            const int64_t step = q.M * q.N;
+            const bool whole = q.N - n >= 8;
+            for (int s = group; s < q.splits; s += 4 * groups) {
+                Lin8<float> t[4] = {};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += u[j];
-            };
-            if (q.N - n >= 8) {
-#pragma unroll 4
-                for (int s = group; s < q.splits; s += GROUPS, p += step) {
-                    Lin8<float> t;
-                    t.load(p);
-                    add(t);
+                for (int u = 0; u < 4; ++u) {
+                    if (s + u * groups >= q.splits) continue;
+                    if (whole) t[u].load(p + (s + u * groups) * step);
+                    else t[u].load(p + (s + u * groups) * step, q.N - n);
                 }
-            } else {
-                for (int s = group; s < q.splits; s += GROUPS, p += step) {
-                    Lin8<float> t;
-                    t.load(p, q.N - n);
-                    add(t);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float w[8];
+                    t[u].get(w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += w[j];
                 }
             }
         }
-        if (GROUPS > 1) {
+        if (lg) {
             __syncthreads();
-            __builtin_memcpy(sh.part[group * VECS + mine], v, 32);
+            __builtin_memcpy(sh.part[threadIdx.x], v, 32);
             __syncthreads();
             if (group) continue;
+#pragma unroll 4
+            for (int g = 1; g < groups; ++g)
 #pragma unroll
-            for (int g = 1; g < GROUPS; ++g)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += sh.part[g * VECS + mine][j];
+                for (int j = 0; j < 8; ++j) v[j] += sh.part[g * each + mine][j];
         }
         if (i >= total) continue;
         float bias[8] = {};
@@ -100,19 +108,20 @@ __device__ __forceinline__ void lin_join(const LinProduct<T>& q, int block, int 
     }
 }
 
-template <typename T, typename TO, int MODE, int GROUPS>
-__global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main)
+template <typename T, typename TO, int MODE>
+__global__ __launch_bounds__(256) void lin_join_kernel(LinProduct<T> q, int main, int lg)
 {
     __shared__ LinJoinShared sh;
-    lin_join<T, TO, MODE, GROUPS>(q, (int)blockIdx.x, main, sh);
+    lin_join<T, TO, MODE>(q, (int)blockIdx.x, main, lg, sh);
 }
 // Those of dX in the first blocks, and of dW and db: a launch less.
-template <typename T, int GX, int GW>
-__global__ __launch_bounds__(256) void lin_join_bwd_kernel(LinProduct<T> x, int main_x, LinProduct<T> w, int main_w)
+template <typename T>
+__global__ __launch_bounds__(256) void lin_join_bwd_kernel(LinProduct<T> x, int main_x, int lg_x, LinProduct<T> w, int main_w,
+                                                           int lg_w)
 {
     __shared__ LinJoinShared sh;
-    if ((int)blockIdx.x < main_x) lin_join<T, T, LIN_PLAIN, GX>(x, (int)blockIdx.x, main_x, sh);
-    else lin_join<T, float, LIN_PLAIN, GW>(w, (int)blockIdx.x - main_x, main_w, sh);
+    if ((int)blockIdx.x < main_x) lin_join<T, T, LIN_PLAIN>(x, (int)blockIdx.x, main_x, lg_x, sh);
+    else lin_join<T, float, LIN_PLAIN>(w, (int)blockIdx.x - main_x, main_w, lg_w, sh);
 }
 
 // Copies of matrices whose rows are not whole vectors, with rows that are: the
@@ -272,12 +281,11 @@ LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
     return best;
 }
 
-// A product whose sums, or whose db, are still to be joined: blocks of the join, whose
-// GROUPS is 8 if `many`.
+// A product whose sums, or whose db, are still to be joined: blocks of the join for the
+// sums and of all, threads to a vector (log2).
 template <typename T> struct LinJoin {
     LinProduct<T> q{};
-    int main = 0, all = 0;
-    bool many = false;
+    int main = 0, all = 0, lg = 0;
 };
 
 // The product over K of B (and then of B2, if there is one), and what is to be joined
@@ -307,8 +315,9 @@ hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, in
         q.db_part = (float*)((char*)ws + p.part_bytes);
         q.db_parts = p.splits;
     }
-    join.many = p.splits >= 16;
-    const int64_t vecs = p.splits > 1 ? M * ((N + 7) / 8) : 0, blocks = (vecs + (join.many ? 31 : 255)) / (join.many ? 32 : 256);
+    if (p.splits >= 16)
+        for (join.lg = 3; join.lg < 6 && 4 << join.lg < p.splits;) ++join.lg;
+    const int64_t vecs = p.splits > 1 ? M * ((N + 7) / 8) : 0, blocks = (vecs + (255 >> join.lg)) >> (8 - join.lg);
     join.main = (int)(blocks < 4096 ? blocks : 4096);
     join.all = join.main + (q.db && (!DB || p.splits > 1) ? (N + 15) / 16 : 0);
     return launch_lin_mm<T, TO, AA, BA, MODE, DB>(p, q, s);
@@ -317,19 +326,14 @@ hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, in
 template <typename T, typename TO, int MODE> hipError_t run_join(const LinJoin<T>& j, hipStream_t s)
 {
     if (!j.all) return hipSuccess;
-    if (j.many) lin_join_kernel<T, TO, MODE, 8><<<(unsigned)j.all, 256, 0, s>>>(j.q, j.main);
-    else lin_join_kernel<T, TO, MODE, 1><<<(unsigned)j.all, 256, 0, s>>>(j.q, j.main);
+    lin_join_kernel<T, TO, MODE><<<(unsigned)j.all, 256, 0, s>>>(j.q, j.main, j.lg);
     return hipGetLastError();
 }
 template <typename T> hipError_t run_join_bwd(const LinJoin<T>& x, const LinJoin<T>& w, hipStream_t s)
 {
     if (!x.all) return run_join<T, float, LIN_PLAIN>(w, s);
     if (!w.all) return run_join<T, T, LIN_PLAIN>(x, s);
-    const unsigned grid = (unsigned)(x.all + w.all);
-    if (x.many && w.many) lin_join_bwd_kernel<T, 8, 8><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
-    else if (x.many) lin_join_bwd_kernel<T, 8, 1><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
-    else if (w.many) lin_join_bwd_kernel<T, 1, 8><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
-    else lin_join_bwd_kernel<T, 1, 1><<<grid, 256, 0, s>>>(x.q, x.main, w.q, w.main);
+    lin_join_bwd_kernel<T><<<(unsigned)(x.all + w.all), 256, 0, s>>>(x.q, x.main, x.lg, w.q, w.main, w.lg);
     return hipGetLastError();
 }
 
