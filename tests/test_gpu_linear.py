@@ -253,3 +253,11 @@ def test_large_tiles(rows, fin, fout, dtype):
     """Sizes that take the largest tiles, whole ones and ones that the result cuts."""
     both(rows, fin, fout, dtype, "silu", 0.0)
     both(rows, fin, fout, dtype, "lrelu", 1.0, bias=False, residual=False, seed=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,fin,fout", [(70000, 2, 1), (45001, 13, 13), (60000, 254, 16), (20001, 64, 9)])
+def test_narrow(rows, fin, fout, dtype):
+    """Long reductions to few results: hundreds of splits, joined by many threads a result."""
+    both(rows, fin, fout, dtype, "silu", 0.0)
+    both(rows, fin, fout, dtype, "lrelu", 1.0, residual=False, seed=1)
