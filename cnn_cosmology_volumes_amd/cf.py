@@ -751,6 +751,8 @@ def _linear_sizes(X, W):
         _packed("X", X)
         _packed("W", W, X.dtype)
     fin, fout = W.shape
+    if max(fin, fout) >> 31:      # (the library's sizes are 32 bits: they would wrap)
+        raise ValueError("in or out too large: %s" % (tuple(W.shape),))
     return X.numel() // max(1, fin), fin, fout
 
 
@@ -820,6 +822,12 @@ def cf_resnorm_workspace_size(dtype, xshape, gate_n):
     return int(lib().cf_resnorm_workspace_size(dtype, dims(xshape), int(gate_n)))
 
 
+def _resnorm_dims(X):
+    if X.dim() != 5 or max(X.shape) >> 31:      # (the library's sizes are 32 bits: they would wrap)
+        raise ValueError("not an NDHWC tensor that the library takes: %s" % (tuple(X.shape),))
+    return cf_dims(*X.shape)
+
+
 def _resnorm_params(d, kind, eps, gpre, bpre, gpost, bpost, gate, alpha):
     if gpre is not None:
         _packed("gpre", gpre, torch.float32, (d.c,))
@@ -845,7 +853,7 @@ def cf_resnorm_fwd(X, F, kind, eps, gpre=None, bpre=None, gpost=None, bpost=None
     if stream is not None:
         return _on_stream(stream, cf_resnorm_fwd, (X, F, gpre, bpre, gpost, bpost, gate, R, Y), X, F, kind, eps, gpre,
                           bpre, gpost, bpost, gate, alpha, need_y, R, Y)
-    dt, d = dtype_code(X.dtype), cf_dims(*X.shape)
+    dt, d = dtype_code(X.dtype), _resnorm_dims(X)
     _packed("X", X)
     _packed("F", F, X.dtype, X.shape)
     if R is not None:
@@ -868,7 +876,7 @@ def cf_resnorm_bwd(F, R, dR, dY, kind, eps, gpre=None, bpre=None, gpost=None, bp
     if stream is not None:
         return _on_stream(stream, cf_resnorm_bwd, (F, R, dR, dY, gpre, bpre, gpost, bpost, gate, dX, dF, ws), F, R, dR,
                           dY, kind, eps, gpre, bpre, gpost, bpost, gate, alpha, dX, dF, ws)
-    dt, d = dtype_code(F.dtype), cf_dims(*F.shape)
+    dt, d = dtype_code(F.dtype), _resnorm_dims(F)
     _packed("F", F)
     for name, t in (("R", R), ("dR", dR), ("dY", dY), ("dX", dX), ("dF", dF)):
         if t is not None:

@@ -328,3 +328,21 @@ def test_one_tensor_elsewhere(where):
     if where in ("g1", "o1", "stats", "ws"):
         with pytest.raises(ValueError, match="GPU"):
             cf.cf_grad_clip([t("", 4), t("g1", 5)], 1.0, out=[t("", 4), t("o1", 5)], stats=t("stats", 2), ws=ws)
+
+
+def test_bindings_refuse_sizes_past_32_bits():
+    """2^32 + 8 would be 8 to the library."""
+    big, bf = (1 << 32) + 8, torch.bfloat16
+    new = lambda *shape: torch.empty(shape, dtype=bf, device="meta")
+    with pytest.raises(ValueError, match="too large"):
+        cf.cf_linear_fwd(new(1, big), new(big, 8))
+    with pytest.raises(ValueError, match="too large"):
+        cf.cf_linear_bwd(new(1, 8), new(8, big), None, new(1, big))
+    x = new(1, 1, 1, big, 1)
+    with pytest.raises(ValueError, match="NDHWC"):
+        cf.cf_resnorm_fwd(x, x, cf.CF_NORM_RMS, 1e-6)
+    with pytest.raises(ValueError, match="NDHWC"):
+        cf.cf_resnorm_bwd(x, x, x, x, cf.CF_NORM_RMS, 1e-6)
+    flat = new(4, 8)
+    with pytest.raises(ValueError, match="NDHWC"):
+        cf.cf_resnorm_fwd(flat, flat, cf.CF_NORM_RMS, 1e-6)
