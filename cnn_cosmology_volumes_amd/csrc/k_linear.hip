@@ -152,8 +152,8 @@ template <typename T> __device__ __forceinline__ void lin_pack(const LinPack& q,
 
 // D = dY act'(pre) with rows of `ld` values: fp32, or as bf16 hi and lo = D - hi,
 // which together keep 16 bits or more: dW is fp32 and would show the rounding of hi
-// alone (2^-9 of every term).  dX, rounded to bf16 itself, takes hi alone; a slope
-// of 0 or a power of two leaves no lo (null).
+// alone (2^-9 of every term), and dX, whose own rounding is no larger, would be off by
+// 2.4e-3 for 1.7e-3.  A slope of 0 or a power of two leaves no lo (null).
 // A block takes a range of rows, 2^lg lanes to a row, and leaves the column sums of D.
 template <typename T> struct LinGated {
     const T *pre, *dY;
@@ -288,18 +288,22 @@ template <typename T> struct LinJoin {
     int main = 0, all = 0, lg = 0;
 };
 
-// The product over K of B (and then of B2, if there is one), and what is to be joined
-// after it.  DB: q.db is formed with it; else q.db_part already holds its parts, if
+// The product over K (and then over K again, of A2 and B2, if there are), and what is
+// to be joined after it.  DB: q.db is formed with it; else q.db_part already holds its parts, if
 // q.db is not null.
 template <typename T, typename TO, bool AA, bool BA, int MODE, bool DB>
-hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, int64_t lda, const T* B, const T* B2,
-                   int64_t ldb, void* ws, hipStream_t s)
+hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, const T* A2, int64_t lda, const T* B,
+                   const T* B2, int64_t ldb, void* ws, hipStream_t s)
 {
-    const LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB);
+    // (a dX in two passes takes the tiles and the number of splits of one)
+    LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB);
+    if (A2) p.kb_split *= 2;
     LinProduct<T>& q = join.q;
     q.A = A;
     q.B = B;
-    q.B2 = B2;
+    q.A2 = A2 ? A2 : A;
+    q.B2 = B2 ? B2 : B;
+    q.passes = A2 || B2 ? 2 : 1;
     q.M = M;
     q.N = N;
     q.K = K;
@@ -428,10 +432,10 @@ hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T*
     if (e != hipSuccess) return e;
     const int ldi = up_vec(in, sizeof(T)), ldo = up_vec(out, sizeof(T));
     if (R) {
-        e = lin_run<T, T, true, false, LIN_FWD_RES, false>(y, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
+        e = lin_run<T, T, true, false, LIN_FWD_RES, false>(y, rows, out, in, X, nullptr, ldi, W, nullptr, ldo, copies.at, s);
         return e != hipSuccess ? e : run_join<T, T, LIN_FWD_RES>(y, s);
     }
-    e = lin_run<T, T, true, false, LIN_FWD, false>(y, rows, out, in, X, ldi, W, nullptr, ldo, copies.at, s);
+    e = lin_run<T, T, true, false, LIN_FWD, false>(y, rows, out, in, X, nullptr, ldi, W, nullptr, ldo, copies.at, s);
     return e != hipSuccess ? e : run_join<T, T, LIN_FWD>(y, s);
 }
 
@@ -478,12 +482,12 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
     hipError_t e = copies.run(gate, s);
     if (e != hipSuccess) return e;
     if (dX) {
-        e = lin_run<T, T, true, true, LIN_PLAIN, false>(x, rows, in, out, D, ldo, W, nullptr, ldo, at, s);
+        e = lin_run<T, T, true, true, LIN_PLAIN, false>(x, rows, in, out, D, lo, ldo, W, nullptr, ldo, at, s);
         if (e != hipSuccess) return e;
         if (x.q.splits > 1) at += up256l((size_t)x.q.splits * (size_t)rows * in * 4);
     }
-    e = gated ? lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, ldi, D, lo, ldo, at, s)
-              : lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, ldi, D, nullptr, ldo, at, s);
+    e = gated ? lin_run<T, float, false, false, LIN_PLAIN, false>(w, in, out, rows, X, nullptr, ldi, D, lo, ldo, at, s)
+              : lin_run<T, float, false, false, LIN_PLAIN, true>(w, in, out, rows, X, nullptr, ldi, D, nullptr, ldo, at, s);
     return e != hipSuccess ? e : run_join_bwd(x, w, s);
 }
 

@@ -199,7 +199,7 @@ __global__ __launch_bounds__((64 * MmShape<TM, TN>::WAVES), (MmShape<TM, TN>::BL
         const int r = (int)(t - band * 4 * q.tiles_n), h = (int)min((int64_t)4, q.tiles_m - 4 * band);
         const int64_t ti = 4 * band + r % h, i0 = ti * TM;
         const int tj = r / h, j0 = tj * TN;
-        const int b0 = split * q.kb_split, b1 = min(b0 + q.kb_split, q.B2 ? 2 * q.kb : q.kb);
+        const int b0 = split * q.kb_split, b1 = min(b0 + q.kb_split, q.passes * q.kb);
         uint32_t offa[OA::LOADS], offb[OB::LOADS];
         int ka[OA::LOADS], kb[OB::LOADS];
         OA::offsets(offa, ka, q.lda, q.M - i0);
@@ -208,7 +208,7 @@ __global__ __launch_bounds__((64 * MmShape<TM, TN>::WAVES), (MmShape<TM, TN>::BL
             const bool second = b >= q.kb;
             const int64_t k0 = (int64_t)(second ? b - q.kb : b) * OA::BK;
             const int left = b < b1 ? (int)min(q.K - k0, (int64_t)OA::BK) : 0;
-            OA::load(stage, q.A + (AA ? i0 * q.lda + k0 : k0 * q.lda + i0), offa, ka, left);
+            OA::load(stage, (second ? q.A2 : q.A) + (AA ? i0 * q.lda + k0 : k0 * q.lda + i0), offa, ka, left);
             OB::load(stage + OA::CHUNKS, (second ? q.B2 : q.B) + (BA ? j0 * q.ldb + k0 : k0 * q.ldb + j0), offb, kb, left);
         };
         f32x16 acc[MI][NJ] = {};

@@ -41,7 +41,9 @@ enum LinMode {
 template <typename T> struct LinProduct {
     const T* A;
     const T* B;
-    const T* B2;            // k >= K: B2(k - K, n) with A(m, k - K), or null
+    const T* A2;            // a second pass over K, of A2 and B2, where passes is 2
+    const T* B2;
+    int passes;
     int64_t M, K;
     int N;
     int64_t lda, ldb;

@@ -309,9 +309,8 @@ cf_status cf_linear_fwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, c
  *   dX[r,i] = sum_o D[r,o] W[i,o]   (dtype; skipped when dX is NULL)
  *   dW[i,o] = sum_r X[r,i] D[r,o];  db[o] = sum_r D[r,o]   (fp32)
  * db may be NULL; pre may be NULL for CF_ACT_LRELU with slope 1.  R's gradient
- * is dY itself.  For CF_BF16 dX may take D rounded to bf16, dW and db take it with
- * 16 bits or more.  dX, dW and db may not overlap any other argument
- * (CF_ERR_INVALID). */
+ * is dY itself.  For CF_BF16 all three take D with 16 bits or more.  dX, dW and db
+ * may not overlap any other argument (CF_ERR_INVALID). */
 cf_status cf_linear_bwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
                         const void* pre, const void* dY, cf_act act, float slope, void* dX, float* dW, float* db,
                         void* ws, size_t ws_bytes, hipStream_t stream);
