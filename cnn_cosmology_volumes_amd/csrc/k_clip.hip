@@ -7,13 +7,15 @@
 // square of any fp32 value is finite and normal there, so neither large nor
 // small gradients need a scale of their own) and leaves one sum a block.  In the
 // second every block adds these sums in the same order, so that all get the same
-// factor without a launch between, and scales its chunks.  No atomics: results
+// factor without a launch between, and scales its chunks, by products in fp64: a
+// factor in fp32 would be one more rounding, and below 2^-126 it has few digits (values
+// of 1e30 and a limit of 1e-12: 1e-42).  No atomics: results
 // are reproducible bit for bit.  The second launch takes the chunks from the
 // last to the first: what the first read last may still lie in the last-level
 // cache.
 //
-// What bounds it: memory.  75.4 M fp32 values in 192 tensors take 181 us, which is
-// their 302 MB read twice and written once at 5 TB/s; 5.0 M values in 11 tensors
+// What bounds it: memory.  75.4 M fp32 values in 192 tensors take 184 us (181 with a
+// factor in fp32), which is their 302 MB read twice and written once at 4.9 TB/s; 5.0 M values in 11 tensors
 // take 15.5 us in the two kernels and 17.6 with the call, which is then the host's.
 #include "cf_internal.h"
 
@@ -138,18 +140,18 @@ __global__ __launch_bounds__(CLIP_T) void clip_scale_kernel(ClipList<T> l, const
     for (int i = (int)threadIdx.x; i < parts; i += CLIP_T) sum += part[i];
     const double norm = sqrt(block_sum(sum, sh));
     // (a norm that is not a number gives a factor that is none either)
-    const float factor = norm <= (double)max_norm ? 1.f : max_norm < INFINITY ? (float)((double)max_norm / norm) : 1.f;
+    const double factor = norm <= (double)max_norm ? 1.0 : max_norm < INFINITY ? (double)max_norm / norm : 1.0;
     if (stats && blockIdx.x == 0 && threadIdx.x == 0) {
         stats[0] = (float)norm;
-        stats[1] = factor;
+        stats[1] = (float)factor;
     }
     for (int b = (int)blockIdx.x;;) {
-        if (factor != 1.f || g != out)
+        if (factor != 1.0 || g != out)
 #pragma unroll
             for (int k = 0; k < CLIP_V; ++k) {
                 const int i = x.place(k);
 #pragma unroll
-                for (int e = 0; e < V; ++e) Elem<T>::store(x.v[k], e, widen(x.v[k][e]) * factor);
+                for (int e = 0; e < V; ++e) Elem<T>::store(x.v[k], e, (float)((double)widen(x.v[k][e]) * factor));
                 if (i + V <= n) __builtin_memcpy(out + i, x.v[k], 16);
                 else
 #pragma unroll

@@ -335,7 +335,9 @@ size_t cf_grad_clip_workspace_size(cf_dtype dtype, int32_t ntensors, const int64
  * factor 0 (infinite gradients become NaN), one that is NaN the factor NaN.
  * stats: two device floats, the norm and the factor, or NULL.  Squares are added
  * in fp64 and in a fixed order: they neither overflow nor vanish, and results are
- * reproducible bit for bit. */
+ * reproducible bit for bit.  The factor that values are scaled by is fp64; stats
+ * holds it and the norm rounded to fp32 (a norm past fp32's range as infinity, with
+ * a factor that is not 0). */
 cf_status cf_grad_clip(cf_dtype dtype, int32_t ntensors, const int64_t* n, const void* const* g, void* const* out,
                        float max_norm, float* stats, void* ws, size_t ws_bytes, hipStream_t stream);
 
