@@ -520,9 +520,8 @@ def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
     first = grads[0]
     dt, kind = dtype_code(first.dtype), first.dtype
     every = grads if out is None else [*grads, *out]
-    sizes = [t.numel() for t in every]
     if {t.dtype for t in every} != {kind} or not all(map(torch.Tensor.is_contiguous, every)) or (
-            out is not None and sizes[:k] != sizes[k:]):
+            out is not None and not all(map(torch.Tensor.is_same_size, grads, out))):
         for i, t in enumerate(grads):
             _packed("gradient %d" % i, t, kind)
             if out is not None:
@@ -531,7 +530,7 @@ def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
         _packed("stats", stats, torch.float32, (2,))
     at = first.get_device()
     s = _on_gpu(ws, first, stats, *[t for t in every if t.get_device() != at][:1])
-    counts, pointers = array.array("q", sizes), array.array("Q", map(torch.Tensor.data_ptr, every))
+    counts, pointers = array.array("q", map(torch.Tensor.numel, grads)), array.array("Q", map(torch.Tensor.data_ptr, every))
     n, p = counts.buffer_info()[0], pointers.buffer_info()[0]
     stats = first.new_empty(2, dtype=torch.float32) if stats is None else stats
     L = lib()

@@ -1,0 +1,27 @@
+"""cf_grad_clip's checks of its lists: one rule for every tensor, whatever else is in the list."""
+import pytest
+import torch
+
+from cnn_cosmology_volumes_amd import cf
+
+
+@pytest.mark.parametrize("others", [[], [torch.zeros(4)], [torch.zeros(4, dtype=torch.bfloat16)]], ids=["alone", "fine", "type"])
+@pytest.mark.parametrize("grad,out", [((2, 3), (6,)), ((6,), (2, 3)), ((2, 3), (3, 2)), ((1,), ()), ((5,), (6,))], ids=str)
+def test_an_outputs_shape_is_its_gradients(grad, out, others):
+    """An output of as many values but another shape is refused, beside tensors of a wrong type or alone."""
+    g, o = [torch.zeros(grad), *others], [torch.zeros(out), *others]
+    with pytest.raises(ValueError, match="output 0 must have shape"):
+        cf.cf_grad_clip(g, 1.0, out=o)
+    if not others:
+        with pytest.raises(ValueError, match="output 1 must have shape"):
+            cf.cf_grad_clip([torch.zeros(4), *g], 1.0, out=[torch.zeros(4), *o])
+
+
+def test_the_first_that_is_wrong_is_named():
+    g = [torch.zeros(2, 3), torch.zeros(4)]
+    with pytest.raises(TypeError, match="output 1"):
+        cf.cf_grad_clip(g, 1.0, out=[torch.zeros(2, 3), torch.zeros(4, dtype=torch.bfloat16)])
+    with pytest.raises(ValueError, match="output 0 must be contiguous"):
+        cf.cf_grad_clip(g, 1.0, out=[torch.zeros(3, 2).t(), torch.zeros(4)])
+    with pytest.raises(ValueError, match="GPU"):
+        cf.cf_grad_clip(g, 1.0, out=[torch.zeros(2, 3), torch.zeros(4)])
