@@ -180,7 +180,7 @@ template <typename T> __device__ __forceinline__ void lin_gate_rows(const LinGat
             __builtin_memcpy(d, &dv, 16);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float v = widen(d[j]) * lin_dact(q.act, widen(z[j]));
+                const float v = widen(d[j]) * lin_dact<T>(q.act, widen(z[j]));
                 sum[j] += v;
                 Elem<T>::store(h, j, v);
                 // (an infinite hi stands for itself: inf - inf would make NaN of it)

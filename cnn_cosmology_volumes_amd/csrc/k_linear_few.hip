@@ -92,7 +92,7 @@ __global__ __launch_bounds__(few_threads<ROWS>()) void lin_few_fwd_kernel(LinPro
         const int64_t at = (int64_t)r * q.N + c;
         if (q.bias) v += q.bias[c];
         if (q.pre) Elem<T>::store(q.pre, at, v);
-        v = lin_act(q.act, v);
+        v = lin_act<T>(q.act, v);
         if (q.R) v += widen(q.R[at]);
         Elem<T>::store((T*)q.C, at, v);
     }
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void lin_few_bwd_kernel(FewBwd<T> q
             __builtin_memcpy(z, &zv[m], 16);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float v = q.gated ? widen(d[j]) * lin_dact(q.act, widen(z[j])) : widen(d[j]);
+                const float v = q.gated ? widen(d[j]) * lin_dact<T>(q.act, widen(z[j])) : widen(d[j]);
                 sd[r][j / 4][lane][j % 4] = r < q.rows ? v : 0.f;
             }
         }

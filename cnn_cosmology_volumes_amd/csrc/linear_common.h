@@ -17,16 +17,36 @@ struct LinAct {
     int act;
     float slope;
 };
-__device__ __forceinline__ float lin_act(const LinAct& a, float z)
+// 1 / (1 + exp(-z)), and 1 minus that.  For fp32 results from the exponential of -|z|,
+// which neither overflows nor loses digits to its argument's rounding (that of
+// __expf is off by u |z|, 60 u at z = -80), so that both are within some 6 u = 6 2^-24.
+// For bf16 results, of 8 bits (D: 16), __expf's digits are enough.
+template <typename T> __device__ __forceinline__ void lin_sigmoid(float z, float& s, float& rest)
 {
-    if (a.act == CF_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __expf(-z));
-    return z > 0.f ? z : a.slope * z;
+    if constexpr (sizeof(T) == 4) {
+        const float e = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + e);
+        s = z < 0.f ? e * r : r;
+        rest = z < 0.f ? r : e * r;
+    } else {
+        s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
+        rest = 1.f - s;
+    }
 }
-__device__ __forceinline__ float lin_dact(const LinAct& a, float z)
+template <typename T> __device__ __forceinline__ float lin_act(const LinAct& a, float z)
 {
     if (a.act == CF_ACT_SILU) {
-        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
-        return s * fmaf(z, 1.f - s, 1.f);
+        float s, rest;
+        lin_sigmoid<T>(z, s, rest);
+        return z * s;
+    }
+    return z > 0.f ? z : a.slope * z;
+}
+template <typename T> __device__ __forceinline__ float lin_dact(const LinAct& a, float z)
+{
+    if (a.act == CF_ACT_SILU) {
+        float s, rest;
+        lin_sigmoid<T>(z, s, rest);
+        return s * fmaf(z, rest, 1.f);
     }
     return z > 0.f ? 1.f : a.slope;
 }
@@ -212,10 +232,10 @@ __device__ __forceinline__ void lin_result(const LinProduct<T>& q, int64_t at, i
         if (q.pre) store8<WHOLE>(q.pre + at, q.N - n, v);
         if (q.act.act == CF_ACT_SILU) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lin_act(LinAct{CF_ACT_SILU, 0.f}, v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = lin_act<T>(LinAct{CF_ACT_SILU, 0.f}, v[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lin_act(LinAct{CF_ACT_LRELU, q.act.slope}, v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = lin_act<T>(LinAct{CF_ACT_LRELU, q.act.slope}, v[i]);
         }
     }
     if (MODE == LIN_FWD_RES) {
