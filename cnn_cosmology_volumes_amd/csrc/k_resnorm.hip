@@ -286,7 +286,7 @@ __global__ __launch_bounds__(RN_T) void resnorm_fwd_kernel(RnArgs a, RnSplit q, 
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 ga[i] *= g[i];
-                gb[i] *= g[i];
+                if (a.bpost) gb[i] *= g[i];      // (no offset: 0, also where the gate is infinite)
             }
             last = n;
         }
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(RN_T, (rn_waves<T, E, WHOLE>())) void resnorm_bwd_k
             ln.vec(a.gpost, 1.f, g);
             ln.vec(a.bpost, 0.f, bo);
 #pragma unroll
-            for (int i = 0; i < E; ++i) g[i] = fmaf(g[i], s1[i], bo[i] * s0[i]);
+            for (int i = 0; i < E; ++i) g[i] = a.bpost ? fmaf(g[i], s1[i], bo[i] * s0[i]) : g[i] * s1[i];
             column_sums<LPR, E>(g, ln, sh, gates + it * a.C);
         }
     }
