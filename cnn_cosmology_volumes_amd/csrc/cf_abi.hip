@@ -1353,8 +1353,13 @@ static cf_status check_clip(cf_dtype dtype, int32_t nt, const int64_t* n, const 
     if (!n) return fail(CF_ERR_INVALID, "%s: null host argument", fn);
     if (nt < 1 || nt > CF_MAX_CLIP_TENSORS)
         return fail(CF_ERR_INVALID, "%s: ntensors must be 1..%d (got %d)", fn, CF_MAX_CLIP_TENSORS, nt);
-    for (int i = 0; i < nt; ++i)
+    int64_t total = 0;
+    for (int i = 0; i < nt; ++i) {
         if (n[i] <= 0 || n[i] > ((int64_t)1 << 36)) return fail(CF_ERR_INVALID, "%s: n[%d] out of range", fn, i);
+        total += n[i];
+    }
+    // (a launch counts its chunks of 2^12 values or more in 31 bits)
+    if (total > kMaxElems) return fail(CF_ERR_INVALID, "%s: tensors too large", fn);
     return CF_OK;
 }
 

@@ -329,10 +329,11 @@ size_t cf_grad_clip_workspace_size(cf_dtype dtype, int32_t ntensors, const int64
  *   factor = max_norm / norm where norm > max_norm, else 1
  *   out[i] = factor g[i]
  * n, g and out are HOST arrays; g[i] and out[i] are DEVICE pointers to n[i]
- * values (dtype).  out may be NULL, or out[i] = g[i]: in place; no other overlap
- * of out[i] with any argument (CF_ERR_INVALID).  max_norm >= 0; INFINITY
- * measures the norm alone (the factor is 1).  A norm that is infinite gives the
- * factor 0 (infinite gradients become NaN), one that is NaN the factor NaN.
+ * values (dtype), n[i] at most 2^36 and 2^40 together.  out may be NULL, or
+ * out[i] = g[i]: in place; no other overlap of out[i] with any argument
+ * (CF_ERR_INVALID).  max_norm >= 0; INFINITY measures the norm alone (the factor
+ * is 1).  A norm that is infinite gives the factor 0 (infinite gradients become
+ * NaN), one that is NaN the factor NaN.
  * stats: two device floats, the norm and the factor, or NULL.  Squares are added
  * in fp64 and in a fixed order: they neither overflow nor vanish, and results are
  * reproducible bit for bit.  The factor that values are scaled by is fp64; stats

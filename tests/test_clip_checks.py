@@ -1,4 +1,6 @@
 """cf_grad_clip's checks of its lists: one rule for every tensor, whatever else is in the list."""
+import ctypes
+
 import pytest
 import torch
 
@@ -25,3 +27,10 @@ def test_the_first_that_is_wrong_is_named():
         cf.cf_grad_clip(g, 1.0, out=[torch.zeros(3, 2).t(), torch.zeros(4)])
     with pytest.raises(ValueError, match="GPU"):
         cf.cf_grad_clip(g, 1.0, out=[torch.zeros(2, 3), torch.zeros(4)])
+
+
+def test_lists_that_are_too_large_together():
+    """128 tensors of 2^36 values are each allowed, but their chunks together are 2^31."""
+    size = lambda count: cf.lib().cf_grad_clip_workspace_size(cf.CF_F32, count, (ctypes.c_int64 * 128)(*[1 << 36] * 128))  # noqa: E731
+    assert size(16) > 0 and size(17) == 0 and size(128) == 0
+    assert b"too large" in cf.lib().cf_last_error()
