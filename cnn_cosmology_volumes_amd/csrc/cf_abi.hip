@@ -1195,6 +1195,21 @@ size_t cf_linear_workspace_size(cf_dtype dtype, int64_t rows, int32_t in, int32_
     return linear_ws_bytes(dtype, rows, in, out, backward != 0);
 }
 
+// For the tests, which look that they reach every kernel; no part of the ABI.
+extern "C" cf_status cf_internal_linear_tiles(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, int32_t product,
+                                              int32_t* tiles)
+{
+    const char* fn = "cf_internal_linear_tiles";
+    cf_status st = check_linear(dtype, rows, in, out, fn);
+    if (st != CF_OK) return st;
+    if (product < 0 || product > 4 || !tiles) return fail(CF_ERR_INVALID, "%s: unknown product", fn);
+    const LinTiles t = linear_tiles(dtype, rows, in, out, product);
+    tiles[0] = t.tm;
+    tiles[1] = t.tn;
+    tiles[2] = t.splits;
+    return CF_OK;
+}
+
 cf_status cf_linear_fwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
                         const float* bias, cf_act act, float slope, const void* R, void* pre, void* Y, void* ws,
                         size_t ws_bytes, hipStream_t stream)

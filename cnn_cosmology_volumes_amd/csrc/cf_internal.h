@@ -366,6 +366,11 @@ hipError_t launch_muon(const NsShapes& l, const NsCoef& c, const MuonArgs& h, fl
 
 // Linear layers over rows (k_linear.hip).  T = float or uint16_t (bf16).
 size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd);
+// The tile that a product takes and its splits; zeros where the kernels of few rows take it.
+struct LinTiles {
+    int tm, tn, splits;
+};
+LinTiles linear_tiles(cf_dtype dt, int64_t rows, int in, int out, int product);
 template <typename T>
 hipError_t launch_linear_fwd(int64_t rows, int in, int out, const T* X, const T* W, const float* bias, cf_act act,
                              float slope, const T* R, T* pre, T* Y, void* ws, hipStream_t s);

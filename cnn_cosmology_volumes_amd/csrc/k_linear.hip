@@ -238,34 +238,49 @@ LinGate lin_gate(int64_t rows, int N, int size)
 //         262144 x 128 x 512 223 / 166 / 144 / 135     8192 x 1024 x 1024 38 / 27 / 26 / 33
 //         262144 x 64 x 64 23 / 33 / - / -
 //         dW of 32768 x 512 x 1024 in two parts, 8 / 8 / 16 / 32 splits: - / 103 / 94 / 92
-//   fp32  4096 x 2048 x 2048 291 / 264 / 256 / 479     7429 x 333 x 1001 51 / 51 / 54 / 93
-// sums: with db, whose sums take the registers that the largest tiles would need.
+//   fp32  32768 x 2048 x 2048 2158 / 2005 / 1929 us    4096 x 2048 x 2048 276 / 257 / 255
+//         40102 x 128 x 1456 218 / 205 / 205           8192 x 1024 x 1024 148 / 135 / 136
+//         416890 x 32 x 176 191 / 191 / 185            16640 x 512 x 256 52 / 72 / 84
+//         262144 x 64 x 64 45 / 74 / 71                7429 x 333 x 1001 65 / 66 / 69
+//         3000 x 1500 x 1500 134 / 190 / -             32768 x 1024 x 128 90 / 81 / -
+//         dW of 32768 x 512 x 1024, 8 / 16 / 16 splits: 342 / 339 / 340, with db 392 / 374 / -
+// In fp32 a piece is bound by the matrix cores, so that the CU with the most blocks
+// counts; in bf16 by its loads, and the chip's mean does.  256 x 256 is for bf16: in
+// fp32 it was not ahead by 2% anywhere (32768 x 2048 x 2048 1953, 8192 x 1024 x 1024
+// 158).  Over 40 fp32 sizes, these among them, the tile taken is 2% slower than the
+// fastest one by geometric mean, 14% at most (5000 x 1024 x 1024 dW with db).
+// sums: with db, whose sums take the registers that the largest tiles would need, and
+// matrix instructions of their own.
 LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
 {
     struct Tile {
         int tm, tn, slots;
-        double alone;                    // a piece's time where a CU has a block for itself, of that with its full share
-        double piece[2], rest[2];        // bf16, fp32
+        double alone;                    // bf16: a piece's time where a CU has a block for itself, of that with its full share
+        double crowd[5];                 // fp32: a piece's time with so many blocks on a CU, of that with all
+        double piece[2], rest[2], sums;  // bf16, fp32; a piece with db's sums (fp32)
     };
-    static const Tile tiles[4] = {{64, 64, 1280, 0.4, {0.61, 1.05}, {5.5, 5.0}},
-                                  {128, 128, 512, 0.5, {0.64, 2.0}, {6.5, 12.0}},
-                                  {256, 128, 512, 0.5, {1.09, 3.9}, {10.5, 14.0}},
-                                  {256, 256, 256, 1.0, {0.85, 3.7}, {11.0, 25.0}}};
+    static const Tile tiles[4] = {{64, 64, 1280, 0.4, {0.28, 0.43, 0.7, 0.95, 1.0}, {0.61, 1.27}, {5.5, 9.0}, 1.25},
+                                  {128, 128, 512, 0.5, {0.53, 1.0}, {0.64, 1.92}, {6.5, 12.0}, 1.1},
+                                  {256, 128, 512, 0.5, {0.53, 1.0}, {1.09, 3.62}, {10.5, 22.0}, 1.0},
+                                  {256, 256, 256, 1.0, {}, {0.85, 0.0}, {11.0, 0.0}, 1.0}};
     const int bk = LIN_PIECE / size, kb = (int)((K + bk - 1) / bk), f32 = size == 4;
     const int64_t total = (int64_t)kb * passes;
     LinPlan best{};
     double least = 0.0;
     for (const Tile& t : tiles) {
-        if (sums && t.tm == 256) break;
+        if ((sums && t.tm == 256) || (f32 && t.tn == 256)) break;
         const int64_t tm = (M + t.tm - 1) / t.tm;
         const int tn = (N + t.tn - 1) / t.tn;
         for (int64_t want = 1; want <= 1024 && (want == 1 || total / want >= 4); want *= 2) {
             const int64_t each = (total + want - 1) / want, splits = (total + each - 1) / each, units = tm * tn * splits;
             const double full = (double)units / t.slots;
-            const double share = full >= 1.0 ? 1.0 : full > t.alone ? full : t.alone;
+            double share = full >= 1.0 ? 1.0 : full > t.alone ? full : t.alone;
+            if (f32 && full < 1.0) share = t.crowd[(units - 1) / 256];
             // (many small blocks: one begins as another ends)
-            const double rounds = full <= 1.0 ? 1.0 : t.tm == 64 ? full + 0.5 : (double)((units + t.slots - 1) / t.slots);
-            double us = rounds * (each * t.piece[f32] * share + t.rest[f32]);
+            const double rounds = full <= 1.0  ? 1.0
+                                  : t.tm == 64 ? full + (f32 ? 0.0 : 0.5)
+                                               : (double)((units + t.slots - 1) / t.slots);
+            double us = rounds * (each * t.piece[f32] * share * (f32 && sums ? t.sums : 1.0) + t.rest[f32]);
             if (splits > 1) us += 4.0 + (double)M * N * 8.0 * splits / 4.5e6;
             if (!best.tm || us < least) {
                 least = us;
@@ -403,6 +418,18 @@ size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
     const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes + parts;
     const size_t plain = copy_bytes(rows, out, size) + one.part_bytes + one.db_bytes;
     return copies + x.part_bytes + (gated > plain ? gated : plain);
+}
+
+// (in a table of tiles and splits, product 0: forward, 1: dX, 2: dW without an activation, 3: dW with D in one part,
+// 4: with D in two)
+LinTiles linear_tiles(cf_dtype dt, int64_t rows, int in, int out, int product)
+{
+    const int size = dt == CF_F32 ? 4 : 2;
+    if (product == 0 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out)) return LinTiles{0, 0, 0};
+    const LinPlan p = product == 0   ? lin_plan(rows, out, in, size, 1, false)
+                      : product == 1 ? lin_plan(rows, in, out, size, 1, false)
+                                     : lin_plan(in, out, rows, size, product == 4 && size == 2 ? 2 : 1, product == 2);
+    return LinTiles{p.tm, p.tn, p.splits};
 }
 
 template <typename T>

@@ -367,9 +367,14 @@ hipError_t launch_lin_mm(const LinPlan& p, const LinProduct<T>& q, hipStream_t s
         lin_mm_kernel<T, TO, AA, BA, TM, TN, MODE, DB><<<grid, (64 * MmShape<TM, TN>::WAVES), 0, s>>>(q);
     };
     if constexpr (!DB) {
+        if constexpr (sizeof(T) == 2) {
+            if (p.tn == 256) {
+                go(std::integral_constant<int, 256>(), std::integral_constant<int, 256>());
+                return hipGetLastError();
+            }
+        }
         if (p.tm == 256) {
-            if (p.tn == 256) go(std::integral_constant<int, 256>(), std::integral_constant<int, 256>());
-            else go(std::integral_constant<int, 256>(), std::integral_constant<int, 128>());
+            go(std::integral_constant<int, 256>(), std::integral_constant<int, 128>());
             return hipGetLastError();
         }
     }
