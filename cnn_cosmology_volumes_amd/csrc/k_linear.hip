@@ -390,11 +390,19 @@ size_t copy_bytes(int64_t rows, int cols, int size)
 }
 
 // Whether the forward of few rows is one launch of lin_few_fwd_kernel: its blocks
-// take a whole reduction each, which is too long where few columns leave few of them
-// (1 x 16384 x 128 bf16: 24 us, split and joined 9; 8 x 2048 x 256 fp32: 9 and 11).
+// take a whole reduction each, which is too long for long rows of X.  One launch / a
+// product, in us, captured into a graph (a call by itself takes 10 and 15 at least):
+//   1 row, bf16    2048 x 1024  6.4 / 7.8   4096 x 2048 11.2 / 10.6  8192 x 2048 19 / 13  65536 x 1024 199 / 34
+//   8 rows, fp32   2048 x 256     9 / 11    4096 x 1024 14.5 / 13.8  8192 x 1024 25 / 18  65536 x 512 242 / 48
+// Rows of W that are not whole vectors would be copied for the product; up to 4
+// rows of X and where its columns leave blocks enough, the launch goes on for less:
+//   1 row, bf16    8192 x 1537    20 / 27    16384 x 2047  54 / 42   16384 x 4095  62 / 75
+//   1 row, fp32    8192 x 515     19 / 29    16384 x 1537  53 / 73   65536 x 2047 229 / 336
+//   8 rows, fp32   8192 x 515     52 / 28    16384 x 2047 130 / 87
 bool lin_few_fwd(int64_t rows, int in, int out, int size)
 {
-    return rows <= LIN_FEW && (out * size >= 32 * 64 || in <= 4096);
+    if (rows > LIN_FEW) return false;
+    return in <= 4096 || (rows <= 4 && out * size % 16 && out * size >= (in <= 8192 ? 1024 : 6144));
 }
 // And the backward: more than 8 rows of large matrices are products (16 x 4096 x 4096
 // bf16 52 us with these, 60 in one launch; 16 x 2048 x 2048 fp32 32 and 28).

@@ -37,3 +37,19 @@ def test_few_rows_take_no_tile():
     f = cf.lib().cf_internal_linear_tiles
     assert f(cf.CF_F32, 100, 64, 64, 5, (ctypes.c_int32 * 3)()) == cf.CF_ERR_INVALID
     assert f(cf.CF_F32, 0, 64, 64, 0, (ctypes.c_int32 * 3)()) == cf.CF_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", [cf.CF_F32, cf.CF_BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 3, 4, 8, 16])
+def test_long_rows_are_products(rows, dtype):
+    """A block of the kernels of few rows takes a whole reduction: 65536 x 1024 in bf16 was 6 times
+    as long as the product.  Rows of W that would be copied first are worth it for few rows."""
+    few = lambda fin, fout: tiles(dtype, rows, fin, fout, FWD) == (0, 0, 0)  # noqa: E731
+    for fin in (16384, 65536):
+        for fout in (16, 128, 1024, 4096, 65536):
+            assert not few(fin, fout)
+    assert few(512, 512) and few(2048, 2048) and few(4096, 17)
+    assert few(8192, 2047) == (rows <= 4) == few(16384, 4095)
+    assert not few(16384, 515)
+    need = cf.cf_linear_workspace_size(dtype, rows, 65536, 1024, False)
+    assert need >= 2 * 4 * rows * 1024 and need % 16 == 0      # (parts of the product's splits)
