@@ -404,9 +404,21 @@ bool lin_few_fwd(int64_t rows, int in, int out, int size)
     if (rows > LIN_FEW) return false;
     return in <= 4096 || (rows <= 4 && out * size % 16 && out * size >= (in <= 8192 ? 1024 : 6144));
 }
-// And the backward: more than 8 rows of large matrices are products (16 x 4096 x 4096
-// bf16 52 us with these, 60 in one launch; 16 x 2048 x 2048 fp32 32 and 28).
-bool lin_few_bwd(int64_t rows, int in, int out) { return rows <= 8 || (rows <= LIN_FEW && (int64_t)in * out <= 1 << 22); }
+// And the backward: a block takes 8 or 16 rows of W over all columns, which is too
+// long where there are few rows of W and many columns; very many rows of W leave each
+// block little beside its own start.  One launch / products, in us, captured into a
+// graph (a call by itself takes 10 and 20 at least):
+//   1 row, bf16    2048 x 1024  9.2 / 17   1024 x 4096 24 / 24   512 x 16384 79 / 29   16 x 65536 319 / 22
+//   8 rows, fp32   2047 x 2047   20 / 30   1024 x 4096 31 / 26   512 x 16384 106 / 33  16 x 65536 422 / 26
+//   8 rows         bf16 4096 x 16384 121 / 125, 65536 x 128 68 / 26; fp32 3001 x 4097 35 / 58, 65536 x 512 ahead
+// More than 8 rows have longer sums, and their products are no longer:
+//   16 rows        bf16 2048 x 1024 11 / 17, 4096 x 4096 67 / 39, 16384 x 128 41 / 15; fp32 1024 x 2048 28 / 19
+bool lin_few_bwd(int64_t rows, int in, int out, int size)
+{
+    if (rows > LIN_FEW) return false;
+    if (rows > 8) return in <= 4096 && out * size <= 4096 && (int64_t)in * out <= 1 << 22;
+    return (out <= 2048 || 4 * in >= out) && (in <= 16384 || (size == 4 && out >= 512));
+}
 
 bool lin_gated(cf_act act, float slope) { return act == CF_ACT_SILU || slope != 1.f; }
 
@@ -415,7 +427,7 @@ bool lin_gated(cf_act act, float slope) { return act == CF_ACT_SILU || slope != 
 size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    if (bwd ? lin_few_bwd(rows, in, out) : lin_few_fwd(rows, in, out, size)) return 0;
+    if (bwd ? lin_few_bwd(rows, in, out, size) : lin_few_fwd(rows, in, out, size)) return 0;
     const size_t copies = copy_bytes(rows, in, size) + copy_bytes(in, out, size);
     if (!bwd) return copies + lin_plan(rows, out, in, size, 1, false).part_bytes;
     const LinGate g = lin_gate(rows, out, size);
@@ -433,7 +445,7 @@ size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
 LinTiles linear_tiles(cf_dtype dt, int64_t rows, int in, int out, int product)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    if (product == 0 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out)) return LinTiles{0, 0, 0};
+    if (product == 0 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out, size)) return LinTiles{0, 0, 0};
     const LinPlan p = product == 0   ? lin_plan(rows, out, in, size, 1, false)
                       : product == 1 ? lin_plan(rows, in, out, size, 1, false)
                                      : lin_plan(in, out, rows, size, product == 4 && size == 2 ? 2 : 1, product == 2);
@@ -480,7 +492,7 @@ hipError_t launch_linear_bwd(int64_t rows, int in, int out, const T* X, const T*
 {
     const bool gated = lin_gated(act, slope);
     const LinAct a = {(int)act, slope};
-    if (lin_few_bwd(rows, in, out))
+    if (lin_few_bwd(rows, in, out, (int)sizeof(T)))
         return launch_lin_few_bwd((int)rows, in, out, X, W, pre, dY, a, gated, dX, dW, db, s);
     const int ldi = up_vec(in, sizeof(T)), ldo = up_vec(out, sizeof(T));
     LinCopies<T> copies;

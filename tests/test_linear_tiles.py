@@ -53,3 +53,16 @@ def test_long_rows_are_products(rows, dtype):
     assert not few(16384, 515)
     need = cf.cf_linear_workspace_size(dtype, rows, 65536, 1024, False)
     assert need >= 2 * 4 * rows * 1024 and need % 16 == 0      # (parts of the product's splits)
+
+
+@pytest.mark.parametrize("dtype", [cf.CF_F32, cf.CF_BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 4, 8, 16])
+def test_wide_and_tall_backwards_are_products(rows, dtype):
+    """A block of the backward of few rows takes a few rows of W over all columns: 16 x 65536 was 13 to 23 times
+    as long as the products, 65536 x 16 up to 8 times."""
+    few = lambda fin, fout: tiles(dtype, rows, fin, fout, DW_ONE) == (0, 0, 0) == tiles(dtype, rows, fin, fout, DX)  # noqa: E731
+    for fin, fout in ((16, 16384), (16, 65536), (512, 16384), (1024, 65536), (65536, 16), (65536, 128), (2048, 16384)):
+        assert not few(fin, fout)
+    assert few(128, 128) and few(2048, 1024) and few(1, 1) and few(4096, 512)
+    assert few(4096, 4096) == (rows <= 8) == few(4096, 2049)
+    assert few(65536, 512) == (rows <= 8 and dtype == cf.CF_F32)
