@@ -822,8 +822,8 @@ def cf_resnorm_workspace_size(dtype, xshape, gate_n):
 
 
 def _resnorm_dims(X):
-    if X.dim() != 5 or max(X.shape) >> 31:      # (the library's sizes are 32 bits: they would wrap)
-        raise ValueError("not an NDHWC tensor that the library takes: %s" % (tuple(X.shape),))
+    if X.dim() != 5 or max(X.shape) > 1 << 30:      # (the library's limit, before memory is made for the outputs)
+        raise ValueError("X and F must be NDHWC tensors, 2^30 at most along a dimension, not %s" % (tuple(X.shape),))
     return cf_dims(*X.shape)
 
 
