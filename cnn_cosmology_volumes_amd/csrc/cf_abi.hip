@@ -1202,7 +1202,7 @@ extern "C" cf_status cf_internal_linear_tiles(cf_dtype dtype, int64_t rows, int3
     const char* fn = "cf_internal_linear_tiles";
     cf_status st = check_linear(dtype, rows, in, out, fn);
     if (st != CF_OK) return st;
-    if (product < 0 || product > 4 || !tiles) return fail(CF_ERR_INVALID, "%s: unknown product", fn);
+    if (product < 0 || product > 5 || !tiles) return fail(CF_ERR_INVALID, "%s: unknown product", fn);
     const LinTiles t = linear_tiles(dtype, rows, in, out, product);
     tiles[0] = t.tm;
     tiles[1] = t.tn;

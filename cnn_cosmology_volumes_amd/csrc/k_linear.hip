@@ -244,25 +244,28 @@ LinGate lin_gate(int64_t rows, int N, int size)
 //         262144 x 64 x 64 45 / 74 / 71                7429 x 333 x 1001 65 / 66 / 69
 //         3000 x 1500 x 1500 134 / 190 / -             32768 x 1024 x 128 90 / 81 / -
 //         dW of 32768 x 512 x 1024, 8 / 16 / 16 splits: 342 / 339 / 340, with db 392 / 374 / -
+//         with residuals 40102 x 128 x 1456 234 / 244 / 286, 65536 x 256 x 256 94 / 91 / 98
 // In fp32 a piece is bound by the matrix cores, so that the CU with the most blocks
 // counts; in bf16 by its loads, and the chip's mean does.  256 x 256 is for bf16: in
 // fp32 it was not ahead by 2% anywhere (32768 x 2048 x 2048 1953, 8192 x 1024 x 1024
 // 158).  Over 40 fp32 sizes, these among them, the tile taken is 2% slower than the
 // fastest one by geometric mean, 14% at most (5000 x 1024 x 1024 dW with db).
 // sums: with db, whose sums take the registers that the largest tiles would need, and
-// matrix instructions of their own.
-LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
+// matrix instructions of their own.  residual: fp32 residuals on their way take
+// registers too (of tiles of 256 x 128 some go through scratch memory).
+LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums, bool residual)
 {
     struct Tile {
         int tm, tn, slots;
         double alone;                    // bf16: a piece's time where a CU has a block for itself, of that with its full share
         double crowd[5];                 // fp32: a piece's time with so many blocks on a CU, of that with all
-        double piece[2], rest[2], sums;  // bf16, fp32; a piece with db's sums (fp32)
+        double piece[2], rest[2];        // bf16, fp32
+        double sums, residual;           // fp32: a piece with db's sums, of that without; more for residuals
     };
-    static const Tile tiles[4] = {{64, 64, 1280, 0.4, {0.28, 0.43, 0.7, 0.95, 1.0}, {0.61, 1.27}, {5.5, 9.0}, 1.25},
-                                  {128, 128, 512, 0.5, {0.53, 1.0}, {0.64, 1.92}, {6.5, 12.0}, 1.1},
-                                  {256, 128, 512, 0.5, {0.53, 1.0}, {1.09, 3.62}, {10.5, 22.0}, 1.0},
-                                  {256, 256, 256, 1.0, {}, {0.85, 0.0}, {11.0, 0.0}, 1.0}};
+    static const Tile tiles[4] = {{64, 64, 1280, 0.4, {0.28, 0.43, 0.7, 0.95, 1.0}, {0.61, 1.27}, {5.5, 9.0}, 1.25, 1.5},
+                                  {128, 128, 512, 0.5, {0.53, 1.0}, {0.64, 1.92}, {6.5, 12.0}, 1.1, 5.0},
+                                  {256, 128, 512, 0.5, {0.53, 1.0}, {1.09, 3.62}, {10.5, 22.0}, 1.0, 20.0},
+                                  {256, 256, 256, 1.0, {}, {0.85, 0.0}, {11.0, 0.0}, 1.0, 0.0}};
     const int bk = LIN_PIECE / size, kb = (int)((K + bk - 1) / bk), f32 = size == 4;
     const int64_t total = (int64_t)kb * passes;
     LinPlan best{};
@@ -280,7 +283,7 @@ LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums)
             const double rounds = full <= 1.0  ? 1.0
                                   : t.tm == 64 ? full + (f32 ? 0.0 : 0.5)
                                                : (double)((units + t.slots - 1) / t.slots);
-            double us = rounds * (each * t.piece[f32] * share * (f32 && sums ? t.sums : 1.0) + t.rest[f32]);
+            double us = rounds * (each * t.piece[f32] * share * (f32 && sums ? t.sums : 1.0) + t.rest[f32] + (f32 && residual ? t.residual : 0.0));
             if (splits > 1) us += 4.0 + (double)M * N * 8.0 * splits / 4.5e6;
             if (!best.tm || us < least) {
                 least = us;
@@ -311,7 +314,7 @@ hipError_t lin_run(LinJoin<T>& join, int64_t M, int N, int64_t K, const T* A, co
                    const T* B2, int64_t ldb, void* ws, hipStream_t s)
 {
     // (a dX in two passes takes the tiles and the number of splits of one)
-    LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB);
+    LinPlan p = lin_plan(M, N, K, (int)sizeof(T), B2 ? 2 : 1, DB, MODE == LIN_FWD_RES);
     if (A2) p.kb_split *= 2;
     LinProduct<T>& q = join.q;
     q.A = A;
@@ -429,26 +432,32 @@ size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
     const int size = dt == CF_F32 ? 4 : 2;
     if (bwd ? lin_few_bwd(rows, in, out, size) : lin_few_fwd(rows, in, out, size)) return 0;
     const size_t copies = copy_bytes(rows, in, size) + copy_bytes(in, out, size);
-    if (!bwd) return copies + lin_plan(rows, out, in, size, 1, false).part_bytes;
+    if (!bwd) {
+        const size_t with = lin_plan(rows, out, in, size, 1, false, true).part_bytes,
+                     without = lin_plan(rows, out, in, size, 1, false, false).part_bytes;
+        return copies + (with > without ? with : without);
+    }
     const LinGate g = lin_gate(rows, out, size);
-    const LinPlan x = lin_plan(rows, in, out, size, 1, false),
-                  w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, false), one = lin_plan(in, out, rows, size, 1, true);
-    const LinPlan exact = lin_plan(in, out, rows, size, 1, false);
+    const LinPlan x = lin_plan(rows, in, out, size, 1, false, false),
+                  w = lin_plan(in, out, rows, size, size == 2 ? 2 : 1, false, false),
+                  one = lin_plan(in, out, rows, size, 1, true, false);
+    const LinPlan exact = lin_plan(in, out, rows, size, 1, false, false);
     const size_t parts = w.part_bytes > exact.part_bytes ? w.part_bytes : exact.part_bytes;
     const size_t gated = g.bytes * (size == 2 ? 2 : 1) + g.db_bytes + parts;
     const size_t plain = copy_bytes(rows, out, size) + one.part_bytes + one.db_bytes;
     return copies + x.part_bytes + (gated > plain ? gated : plain);
 }
 
-// (in a table of tiles and splits, product 0: forward, 1: dX, 2: dW without an activation, 3: dW with D in one part,
-// 4: with D in two)
+// product 0: forward, 1: dX, 2: dW without an activation, 3: dW with D in one part, 4: with D in two, 5: forward with
+// a residual
 LinTiles linear_tiles(cf_dtype dt, int64_t rows, int in, int out, int product)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    if (product == 0 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out, size)) return LinTiles{0, 0, 0};
-    const LinPlan p = product == 0   ? lin_plan(rows, out, in, size, 1, false)
-                      : product == 1 ? lin_plan(rows, in, out, size, 1, false)
-                                     : lin_plan(in, out, rows, size, product == 4 && size == 2 ? 2 : 1, product == 2);
+    if (product == 0 || product == 5 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out, size)) return LinTiles{0, 0, 0};
+    const LinPlan p =
+        product == 0 || product == 5 ? lin_plan(rows, out, in, size, 1, false, product == 5)
+        : product == 1               ? lin_plan(rows, in, out, size, 1, false, false)
+                                     : lin_plan(in, out, rows, size, product == 4 && size == 2 ? 2 : 1, product == 2, false);
     return LinTiles{p.tm, p.tn, p.splits};
 }
 

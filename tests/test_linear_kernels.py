@@ -10,18 +10,21 @@ import pytest
 import torch
 
 from cnn_cosmology_volumes_amd import cf
-from test_linear_tiles import DW, DW_ONE, DW_TWO, DX, FWD, tiles
+from test_linear_tiles import DW, DW_ONE, DW_TWO, DX, FWD, FWD_RES, tiles
 
 BF, F32 = torch.bfloat16, torch.float32
 U, TINY = 2.0 ** -24, 1e-37
 T64, T128, T256X128, T256 = (64, 64), (128, 128), (256, 128), (256, 256)
-NAMES = ["fwd", "dX", "dW", "dW_one", "dW_two"]
+NAMES = ["fwd", "dX", "dW", "dW_one", "dW_two", "fwd_res"]
 
 # type, product, tile, whether the reduction is split: rows, in, out
 CASES = {
     (F32, FWD, T64, False): (107, 204, 104), (F32, FWD, T64, True): (101, 248, 106),
     (F32, FWD, T128, False): (12307, 241, 196), (F32, FWD, T128, True): (3745, 4981, 205),
     (F32, FWD, T256X128, False): (54546, 100, 197), (F32, FWD, T256X128, True): (15315, 6949, 193),
+    (F32, FWD_RES, T64, False): (103, 101, 77), (F32, FWD_RES, T64, True): (100, 242, 78),
+    (F32, FWD_RES, T128, False): (32602, 101, 202), (F32, FWD_RES, T128, True): (3916, 7281, 197),
+    (F32, FWD_RES, T256X128, False): (41954, 580, 323), (F32, FWD_RES, T256X128, True): (30977, 7629, 194),
     (F32, DX, T64, False): (101, 104, 231), (F32, DX, T64, True): (106, 103, 247),
     (F32, DX, T128, False): (9804, 257, 242), (F32, DX, T128, True): (3723, 194, 4846),
     (F32, DX, T256X128, False): (54205, 204, 100), (F32, DX, T256X128, True): (15420, 198, 6133),
@@ -49,6 +52,8 @@ CASES = {
     (BF, DW_TWO, T256X128, False): (131, 7211, 1036), (BF, DW_TWO, T256X128, True): (37234, 1162, 130),
     (BF, DW_TWO, T256, False): (131, 1546, 7741), (BF, DW_TWO, T256, True): (42110, 388, 388),
 }
+# (bf16's tiles do not go by residuals)
+CASES.update({(BF, FWD_RES, k[2], k[3]): size for k, size in list(CASES.items()) if k[:2] == (BF, FWD)})
 KEYS = list(CASES)
 IDS = ["%s-%s-%dx%d-%s" % ("bf16" if k[0] == BF else "f32", NAMES[k[1]], *k[2], "split" if k[3] else "whole") for k in KEYS]
 # sizes that are whole vectors (no copies) and, the last two, whole tiles
@@ -62,10 +67,10 @@ def test_the_sizes_reach_every_kernel():
         tm, tn, splits = tiles(cf.dtype_code(dtype), *size, product)
         assert ((tm, tn), splits > 1) == (tile, split), (key, size, tm, tn, splits)
         rows, fin, fout = size
-        m, n = ((rows, fout), (rows, fin), (fin, fout))[min(product, 2)]
+        m, n = {FWD: (rows, fout), FWD_RES: (rows, fout), DX: (rows, fin)}.get(product, (fin, fout))
         assert m > tm and n > tn and m % tm and n % tn
     for dtype in (F32, BF):
-        for product in (FWD, DX, DW, DW_ONE) + ((DW_TWO,) if dtype == BF else ()):
+        for product in (FWD, FWD_RES, DX, DW, DW_ONE) + ((DW_TWO,) if dtype == BF else ()):
             reached = {(k[2], k[3]) for k in KEYS if k[:2] == (dtype, product)}
             every = [T64, T128] + ([T256X128] if product != DW else []) + ([T256] if product != DW and dtype == BF else [])
             assert reached == {(t, s) for t in every for s in (False, True)}
@@ -76,7 +81,7 @@ def test_no_size_takes_another_kernel():
     sizes = [17, 60, 300, 1000, 4096, 20000, 100000, 400000, 1 << 20]
     widths = [1, 5, 16, 60, 128, 200, 512, 1000, 2048, 4096, 9000, 65536]
     for dtype in (F32, BF):
-        for product in (FWD, DX, DW, DW_ONE, DW_TWO)[:5 if dtype == BF else 4]:
+        for product in (FWD, FWD_RES, DX, DW, DW_ONE, DW_TWO)[:6 if dtype == BF else 5]:
             for rows in sizes:
                 for fin in widths:
                     for fout in widths:
@@ -99,20 +104,21 @@ def within(got, want, tol):
     assert worst <= 1.0, worst
 
 
-def check_forward(x, w, b, r):
+def check_forward(x, w, b, r=None):
+    """With pre kept, and without (pre is not an argument of the tiles' choice)."""
     silu = cf.CF_ACT_SILU
     xd, wd, bd = x.double(), w.double(), b.double()
     mag = xd.abs() @ wd.abs()
     z = xd @ wd + bd
     a = z * torch.sigmoid(z)
     ep = (x.shape[1] + 2) * U * mag + U * (z.abs() + bd.abs())
-    ea = 1.1 * ep + U * (8 + 2 * z.abs()) * a.abs()
+    want = a if r is None else a + r.double()
+    ey = 1.1 * ep + U * (8 + 2 * z.abs()) * a.abs() + U * want.abs()
     pre, y = cf.cf_linear_fwd(x, w, b, silu, R=r)
     within(pre, z, ep)
-    within(y, a + r.double(), ea + U * (a + r.double()).abs())
-    none, y = cf.cf_linear_fwd(x, w, b, silu, need_pre=False)
-    assert none is None
-    within(y, a, ea + U * a.abs())
+    within(y, want, ey)
+    none, served = cf.cf_linear_fwd(x, w, b, silu, R=r, need_pre=False)
+    assert none is None and torch.equal(served, y)
 
 
 def check_backward(x, w, pre, dy, act, slope):
@@ -140,8 +146,8 @@ def check_backward(x, w, pre, dy, act, slope):
 def test_kernel(key):
     dtype, product, _, _ = key
     x, w, b, r, pre, dy = made(*CASES[key], dtype)
-    if product == FWD:
-        check_forward(x, w, b, r)
+    if product in (FWD, FWD_RES):
+        check_forward(x, w, b, r if product == FWD_RES else None)
     if product in (DX, DW_TWO):
         check_backward(x, w, pre, dy, cf.CF_ACT_SILU, 0.0)
     if product in (DX, DW):
@@ -155,6 +161,7 @@ def test_kernel(key):
 @pytest.mark.parametrize("size", MORE, ids=str)
 def test_rows_of_whole_vectors(size, dtype):
     x, w, b, r, pre, dy = made(*size, dtype)
+    check_forward(x, w, b)
     check_forward(x, w, b, r)
     check_backward(x, w, pre, dy, cf.CF_ACT_SILU, 0.0)
     check_backward(x, w, pre, dy, cf.CF_ACT_LRELU, 1.0)

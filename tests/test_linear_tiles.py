@@ -5,7 +5,7 @@ import pytest
 
 from cnn_cosmology_volumes_amd import cf
 
-FWD, DX, DW, DW_ONE, DW_TWO = range(5)      # dW: without an activation, with D in one part, in two
+FWD, DX, DW, DW_ONE, DW_TWO, FWD_RES = range(6)      # dW: without an activation, with D in one part, in two
 
 
 def tiles(dtype, rows, fin, fout, product):
@@ -32,10 +32,22 @@ def test_fp32_takes_a_tile_near_the_fastest(size):
     assert splits == 1 and taken <= 1.04 * min(MEASURED[size])
 
 
+WITH_RESIDUAL = {(40102, 128, 1456): (234, 244, 286), (32768, 512, 512): (167, 163, 162), (32768, 2048, 2048): (2157, 2017, 1956),
+                 (65536, 256, 256): (94, 91, 98), (262144, 128, 512): (493, 491, 538), (8192, 1024, 1024): (155, 146, 151),
+                 (7429, 333, 1001): (69, 72, 82), (20000, 700, 700): (196, 207, 211)}
+
+
+@pytest.mark.parametrize("size", sorted(WITH_RESIDUAL), ids=str)
+def test_fp32_with_residuals_takes_a_tile_near_the_fastest(size):
+    tm, tn, splits = tiles(cf.CF_F32, *size, FWD_RES)
+    taken = WITH_RESIDUAL[size][[(64, 64), (128, 128), (256, 128)].index((tm, tn))]
+    assert splits == 1 and taken <= 1.04 * min(WITH_RESIDUAL[size])
+
+
 def test_few_rows_take_no_tile():
     assert tiles(cf.CF_F32, 1, 2048, 2048, FWD) == (0, 0, 0) == tiles(cf.CF_BF16, 8, 512, 512, DX)
     f = cf.lib().cf_internal_linear_tiles
-    assert f(cf.CF_F32, 100, 64, 64, 5, (ctypes.c_int32 * 3)()) == cf.CF_ERR_INVALID
+    assert f(cf.CF_F32, 100, 64, 64, 6, (ctypes.c_int32 * 3)()) == cf.CF_ERR_INVALID
     assert f(cf.CF_F32, 0, 64, 64, 0, (ctypes.c_int32 * 3)()) == cf.CF_ERR_INVALID
 
 
