@@ -15,6 +15,8 @@ typedef uint16_t bf16_t;   // bfloat16 storage word
 
 // ---------------------------------------------------------------- bf16 <-> f32
 __device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
 
 // Round to nearest even (the hardware conversion on gfx950).
 __device__ __forceinline__ uint16_t f2bf(float f) {

@@ -39,9 +39,6 @@ template <typename T> struct ClipList {
     int start[CLIP_LIST + 1];               // first chunk of each tensor
 };
 
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
-
 // The tensor that holds chunk c.
 template <typename T> __device__ __forceinline__ int clip_tensor(const ClipList<T>& l, int c)
 {

@@ -28,8 +28,6 @@
 namespace cf {
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
 constexpr int MM_PIECE = LIN_PIECE;
 constexpr uint32_t MM_OUTSIDE = 0x80000000u;      // an offset past every descriptor's range
 
@@ -39,19 +37,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_rsrc(const void* p)
 }
 
 // A tile of TM x TN: WAVES waves, WC of them side by side, of 32 MI x 32 NJ; stages of
-// pieces; blocks that a CU holds.
+// pieces; waves a SIMD that registers are kept for.  A CU's 160 KB of LDS hold the
+// stages of 5, 2, 2 and 1 blocks (32, 64, 72 and 128 KB each), which are the slots that
+// lin_plan counts; 64 x 64 with residuals or db's sums takes 97 registers and runs 4.
 template <int TM, int TN> struct MmShape;
 template <> struct MmShape<64, 64> {
-    static constexpr int WAVES = 4, WC = 2, MI = 1, NJ = 1, STAGES = 4, BLOCKS = 4;
+    static constexpr int WAVES = 4, WC = 2, MI = 1, NJ = 1, STAGES = 4, SIMD_WAVES = 4;
 };
 template <> struct MmShape<128, 128> {
-    static constexpr int WAVES = 4, WC = 2, MI = 2, NJ = 2, STAGES = 4, BLOCKS = 2;
+    static constexpr int WAVES = 4, WC = 2, MI = 2, NJ = 2, STAGES = 4, SIMD_WAVES = 2;
 };
 template <> struct MmShape<256, 128> {
-    static constexpr int WAVES = 4, WC = 2, MI = 4, NJ = 2, STAGES = 3, BLOCKS = 2;
+    static constexpr int WAVES = 4, WC = 2, MI = 4, NJ = 2, STAGES = 3, SIMD_WAVES = 2;
 };
 template <> struct MmShape<256, 256> {
-    static constexpr int WAVES = 8, WC = 4, MI = 4, NJ = 2, STAGES = 4, BLOCKS = 2;
+    static constexpr int WAVES = 8, WC = 4, MI = 4, NJ = 2, STAGES = 4, SIMD_WAVES = 2;
 };
 
 // A piece of an operand: R rows of the tile.
@@ -170,7 +170,7 @@ template <int MFMAS, int READS, int LOADS> __device__ __forceinline__ void mm_in
 }
 
 template <typename T, typename TO, bool AA, bool BA, int TM, int TN, int MODE, bool DB>
-__global__ __launch_bounds__((64 * MmShape<TM, TN>::WAVES), (MmShape<TM, TN>::BLOCKS)) void lin_mm_kernel(LinProduct<T> q)
+__global__ __launch_bounds__((64 * MmShape<TM, TN>::WAVES), (MmShape<TM, TN>::SIMD_WAVES)) void lin_mm_kernel(LinProduct<T> q)
 {
     using S = MmShape<TM, TN>;
     using OA = MmOperand<T, AA, TM, S::WAVES>;

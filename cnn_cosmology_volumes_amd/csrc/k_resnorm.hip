@@ -35,9 +35,6 @@ namespace {
 constexpr int RN_T = 256;             // threads a block
 constexpr int RN_FWD_BLOCKS = 2048;   // blocks of a forward launch, 8 a CU
 
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
-
 // How the rows are dealt out: `samples` of `rows` rows, each cut into `parts`.
 struct RnSplit {
     int64_t rows;

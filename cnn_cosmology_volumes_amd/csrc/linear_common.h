@@ -10,9 +10,6 @@ namespace cf {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float widen(float v) { return v; }
-__device__ __forceinline__ float widen(uint16_t v) { return bf2f(v); }
-
 struct LinAct {
     int act;
     float slope;
