@@ -14,8 +14,8 @@
 // last to the first: what the first read last may still lie in the last-level
 // cache.
 //
-// What bounds it: memory.  75.4 M fp32 values in 192 tensors take 184 us (181 with a
-// factor in fp32), which is their 302 MB read twice and written once at 4.9 TB/s; 5.0 M values in 11 tensors
+// What bounds it: memory.  75.4 M fp32 values in 192 tensors take 181 us, which is
+// their 302 MB read twice and written once at 5 TB/s; 5.0 M values in 11 tensors
 // take 15.5 us in the two kernels and 17.6 with the call, which is then the host's.
 #include "cf_internal.h"
 
@@ -112,8 +112,9 @@ __global__ __launch_bounds__(CLIP_T) void clip_norm_kernel(ClipList<T> l, double
     if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
+// (fp32: the fp64 products' registers held to what leaves 8 waves a SIMD: 188 us for 191 with three more.  bf16's 94 leave 5.)
 template <typename T>
-__global__ __launch_bounds__(CLIP_T) void clip_scale_kernel(ClipList<T> l, const double* __restrict__ part, int parts,
+__global__ __launch_bounds__(CLIP_T, (sizeof(T) == 4 ? 8 : 5)) void clip_scale_kernel(ClipList<T> l, const double* __restrict__ part, int parts,
                                                             float max_norm, float* __restrict__ stats)
 {
     constexpr int V = 16 / (int)sizeof(T);
