@@ -509,8 +509,9 @@ def cf_adam_larc(hp, t, params, grads, m, v, lr_out=None, ws=None, stream=None):
 
 def cf_grad_clip(grads, max_norm, out=None, stats=None, ws=None, stream=None):
     """Scales gradients (all fp32 or all bf16, at most CF_MAX_CLIP_TENSORS), in
-    place or into the tensors of `out`, to a global norm of at most max_norm
-    (math.inf: measures only) -> [norm, factor], two floats on the GPU."""
+    place or into the tensors of `out` (each of its gradient's shape), to a global
+    norm of at most max_norm (an fp32 value; math.inf: measures only) -> [norm,
+    factor], two floats on the GPU."""
     k = len(grads)
     if not k or (out is not None and len(out) != k):
         raise ValueError("grads must not be empty, and out be as long")

@@ -309,8 +309,10 @@ cf_status cf_linear_fwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, c
  *   dX[r,i] = sum_o D[r,o] W[i,o]   (dtype; skipped when dX is NULL)
  *   dW[i,o] = sum_r X[r,i] D[r,o];  db[o] = sum_r D[r,o]   (fp32)
  * db may be NULL; pre may be NULL for CF_ACT_LRELU with slope 1.  R's gradient
- * is dY itself.  For CF_BF16 all three take D with 16 bits or more.  dX, dW and db
- * may not overlap any other argument (CF_ERR_INVALID). */
+ * is dY itself.  For CF_BF16 all three take D with 16 bits or more, dX and dW as
+ * the sum of two bf16 values: where W or X is infinite, a gradient that is infinite
+ * by its formula may be NaN.  dX, dW and db may not overlap any other argument
+ * (CF_ERR_INVALID). */
 cf_status cf_linear_bwd(cf_dtype dtype, int64_t rows, int32_t in, int32_t out, const void* X, const void* W,
                         const void* pre, const void* dY, cf_act act, float slope, void* dX, float* dW, float* db,
                         void* ws, size_t ws_bytes, hipStream_t stream);
@@ -532,8 +534,10 @@ size_t cf_resnorm_workspace_size(cf_dtype dtype, cf_dims x, int32_t gate_n);
  *   R = alpha X + gate H;  Y = pre(R)
  *   X, F, R, Y [x.n, x.d, x.h, x.w, x.c] (dtype); Y may be NULL (the last block:
  *   no further norm).
- * Y is made from the unrounded R.  x.c at most 4096 (else CF_ERR_UNSUPPORTED).  R
- * and Y may not overlap any other argument (CF_ERR_INVALID). */
+ * Y is made from the unrounded R.  A row's sum and squares are fp32 sums: they have
+ * to stay in fp32's range (values up to 10^17 do).  x.c at most 4096 (else
+ * CF_ERR_UNSUPPORTED).  R and Y may not overlap any other argument
+ * (CF_ERR_INVALID). */
 cf_status cf_resnorm_fwd(cf_dtype dtype, cf_dims x, const cf_resnorm_params* p, const void* X, const void* F, void* R,
                          void* Y, hipStream_t stream);
 
