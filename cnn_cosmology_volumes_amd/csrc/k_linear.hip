@@ -283,7 +283,8 @@ LinPlan lin_plan(int64_t M, int N, int64_t K, int size, int passes, bool sums, b
             const double rounds = full <= 1.0  ? 1.0
                                   : t.tm == 64 ? full + (f32 ? 0.0 : 0.5)
                                                : (double)((units + t.slots - 1) / t.slots);
-            double us = rounds * (each * t.piece[f32] * share * (f32 && sums ? t.sums : 1.0) + t.rest[f32] + (f32 && residual ? t.residual : 0.0));
+            const double piece = t.piece[f32] * share * (f32 && sums ? t.sums : 1.0);
+            double us = rounds * (each * piece + t.rest[f32] + (f32 && residual ? t.residual : 0.0));
             if (splits > 1) us += 4.0 + (double)M * N * 8.0 * splits / 4.5e6;
             if (!best.tm || us < least) {
                 least = us;
@@ -453,10 +454,10 @@ size_t linear_ws_bytes(cf_dtype dt, int64_t rows, int in, int out, bool bwd)
 LinTiles linear_tiles(cf_dtype dt, int64_t rows, int in, int out, int product)
 {
     const int size = dt == CF_F32 ? 4 : 2;
-    if (product == 0 || product == 5 ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out, size)) return LinTiles{0, 0, 0};
-    const LinPlan p =
-        product == 0 || product == 5 ? lin_plan(rows, out, in, size, 1, false, product == 5)
-        : product == 1               ? lin_plan(rows, in, out, size, 1, false, false)
+    const bool forward = product == 0 || product == 5;
+    if (forward ? lin_few_fwd(rows, in, out, size) : lin_few_bwd(rows, in, out, size)) return LinTiles{0, 0, 0};
+    const LinPlan p = forward        ? lin_plan(rows, out, in, size, 1, false, product == 5)
+                      : product == 1 ? lin_plan(rows, in, out, size, 1, false, false)
                                      : lin_plan(in, out, rows, size, product == 4 && size == 2 ? 2 : 1, product == 2, false);
     return LinTiles{p.tm, p.tn, p.splits};
 }
